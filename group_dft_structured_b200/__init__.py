@@ -46,6 +46,7 @@ _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 _SIGNATURES = {
     "feql_weight_fft_bytes": (_SZ, [_I, _I, _I]),
@@ -71,6 +72,16 @@ _SIGNATURES = {
     "feql_mlp_weight_fft_bytes": (_SZ, [_I, _I, _I, _I]),
     "feql_mlp_weight_fft": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _VP]),
     "feql_mlp_forward": (_I, [_VP, _VP, _VP, _VP, _VP, _I64, _I, _I, _I, _I, _VP]),
+    "feql_norm_forward": (_I, [_VP, _VP, _VP, _VP, _VP, _I64, _I, _I, _F, _I, _VP]),
+    "feql_norm_backward_workspace_bytes": (_SZ, [_I64, _I, _I, _I]),
+    "feql_norm_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _I64, _I, _I, _I,
+                                _VP]),
+    "feql_scan_save_bytes": (_SZ, [_I64, _I64, _I, _I, _I, _I]),
+    "feql_scan_forward": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I, _I, _I, _I,
+                               _VP]),
+    "feql_scan_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I, _I,
+                                _I, _I, _VP]),
+    "feql_scan_step": (_I, [_VP, _VP, _VP, _VP, _I64, _I, _I, _I, _I, _VP]),
     "feql_device_status": (_I, [_VP]),
     "feql_status_string": (ctypes.c_char_p, [_I]),
 }
@@ -237,6 +248,47 @@ def feql_mlp_forward(x, What, b1, b2, y, N: int, C: int, H: int, Co: int, dtype:
                      stream=None) -> None:
     _check(load().feql_mlp_forward(_ptr(x), _ptr(What), _ptr(b1), _ptr(b2), _ptr(y), N, C, H, Co,
                                    dtype, _stream(stream)), "feql_mlp_forward")
+
+
+def feql_norm_forward(x, gamma, beta, y, stats, N: int, C: int, T: int, eps: float, dtype: int,
+                      stream=None) -> None:
+    _check(load().feql_norm_forward(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(stats), N, C,
+                                    T, eps, dtype, _stream(stream)), "feql_norm_forward")
+
+
+def feql_norm_backward_workspace_bytes(N: int, C: int, T: int, dtype: int) -> int:
+    return int(load().feql_norm_backward_workspace_bytes(N, C, T, dtype))
+
+
+def feql_norm_backward(x, dy, stats, gamma, dx, dgamma, dbeta, ws, ws_bytes: int, N: int, C: int,
+                       T: int, dtype: int, stream=None) -> None:
+    _check(load().feql_norm_backward(_ptr(x), _ptr(dy), _ptr(stats), _ptr(gamma), _ptr(dx),
+                                     _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws_bytes, N, C, T,
+                                     dtype, _stream(stream)), "feql_norm_backward")
+
+
+def feql_scan_save_bytes(B: int, N: int, C: int, T: int, shared: bool, dtype: int) -> int:
+    return int(load().feql_scan_save_bytes(B, N, C, T, int(shared), dtype))
+
+
+def feql_scan_forward(u, g, h0, offsets, h, hN, save, B: int, N: int, C: int, T: int,
+                      shared: bool, dtype: int, stream=None) -> None:
+    _check(load().feql_scan_forward(_ptr(u), _ptr(g), _ptr(h0), _ptr(offsets), _ptr(h), _ptr(hN),
+                                    _ptr(save), B, N, C, T, int(shared), dtype,
+                                    _stream(stream)), "feql_scan_forward")
+
+
+def feql_scan_backward(dh, u, g, save, dhN, offsets, du, dg, dh0, B: int, N: int, C: int, T: int,
+                       shared: bool, dtype: int, stream=None) -> None:
+    _check(load().feql_scan_backward(_ptr(dh), _ptr(u), _ptr(g), _ptr(save), _ptr(dhN),
+                                     _ptr(offsets), _ptr(du), _ptr(dg), _ptr(dh0), B, N, C, T,
+                                     int(shared), dtype, _stream(stream)), "feql_scan_backward")
+
+
+def feql_scan_step(u, g, state, h, B: int, C: int, T: int, shared: bool, dtype: int,
+                   stream=None) -> None:
+    _check(load().feql_scan_step(_ptr(u), _ptr(g), _ptr(state), _ptr(h), B, C, T, int(shared),
+                                 dtype, _stream(stream)), "feql_scan_step")
 
 
 def feql_device_status(stream=None) -> int:

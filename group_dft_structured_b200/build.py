@@ -28,6 +28,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC,-O2",
     "--expt-relaxed-constexpr",
     "-shared",
+    "--threads", "0",  # the sources side by side
 ]
 
 
@@ -39,7 +40,7 @@ def nvcc() -> str:
 
 
 def sources() -> list[str]:
-    return [os.path.join(CSRC, "feql_api.cu")]
+    return [os.path.join(CSRC, f) for f in ("feql_api.cu", "feql_ops.cu")]
 
 
 def deps() -> list[str]:

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/feql.h"
+#include "host.cuh"
 #include "plan.cuh"
 #include "simt.cuh"
 #include "simt_ct.cuh"
@@ -25,39 +26,6 @@
 using namespace feql;
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-constexpr int kMaxChannels = 1 << 16;   // per group element
-constexpr int64_t kMaxTokens = (1ll << 31) - 1;  // TMA coordinates are int32
-
-struct DeviceInfo {
-  int sms = 0;
-  int smem_optin = 0;
-  int cc_major = 0, cc_minor = 0;
-};
-
-std::mutex g_mu;
-DeviceInfo g_dev[kMaxDevices];
-bool g_dev_ok[kMaxDevices];
-
-int device_info(DeviceInfo *out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FEQL_ERR_CUDA;
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (!g_dev_ok[dev]) {
-    DeviceInfo d;
-    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
-            cudaSuccess ||
-        cudaDeviceGetAttribute(&d.cc_major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d.cc_minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-      return FEQL_ERR_CUDA;
-    g_dev[dev] = d;
-    g_dev_ok[dev] = true;
-  }
-  *out = g_dev[dev];
-  return FEQL_OK;
-}
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -139,10 +107,6 @@ int make_tmap_f32(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
   return r == CUDA_SUCCESS ? FEQL_OK : FEQL_ERR_CUDA;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool valid_dtype(int dt) { return dt >= FEQL_FP16 && dt <= FEQL_FP16_SIMT; }
-
 // Resolves FEQL_FP32 to the library's fp32 algorithm.
 int resolve(int dt) { return dt == FEQL_FP32 ? FEQL_FP32_SIMT : dt; }
 
@@ -160,17 +124,6 @@ bool is_tc(int dt) { return dt == FEQL_FP16; }
 bool is_tf32(int dt) { return dt == FEQL_FP32_3XTF32; }
 // Layout kind of the Fourier-weight buffer of a (resolved) mode.
 int what_kind(int dt) { return is_tc(dt) ? kWhatF16 : (is_tf32(dt) ? kWhatTF32 : kWhatSimt); }
-bool is_half(int dt) { return dt == FEQL_FP16 || dt == FEQL_FP16_SIMT; }
-
-int check_shape(int C, int D) {
-  if (C <= 0 || D <= 0 || C > kMaxChannels || D > kMaxChannels) return FEQL_ERR_INVALID_ARG;
-  return FEQL_OK;
-}
-
-int launch_status() {
-  return cudaGetLastError() == cudaSuccess ? FEQL_OK : FEQL_ERR_CUDA;
-}
-
 int grid_for(int64_t work, int threads, int sms) {
   int64_t g = cdiv(work, threads);
   const int64_t cap = static_cast<int64_t>(sms) * 8;

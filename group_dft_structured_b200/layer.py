@@ -7,13 +7,15 @@ from __future__ import annotations
 
 import torch
 
-from . import (FEQL_FP16, FEQL_FP16_SIMT, feql_backward, feql_backward_dw,
+from . import (FEQL_FP16, FEQL_FP16_SIMT, FEQL_FP32, feql_backward, feql_backward_dw,
                feql_backward_dw_workspace_bytes, feql_backward_dx, feql_ct_backward_dw,
                feql_ct_backward_dw_workspace_bytes, feql_ct_backward_dx, feql_ct_forward,
                feql_ct_weight_fft, feql_ct_weight_fft_bytes, feql_forward, feql_mlp_forward,
-               feql_mlp_weight_fft, feql_mlp_weight_fft_bytes, feql_p4m_backward_dw,
+               feql_mlp_weight_fft, feql_mlp_weight_fft_bytes, feql_norm_backward,
+               feql_norm_backward_workspace_bytes, feql_norm_forward, feql_p4m_backward_dw,
                feql_p4m_backward_dw_workspace_bytes, feql_p4m_backward_dx, feql_p4m_forward,
-               feql_p4m_weight_fft, feql_p4m_weight_fft_bytes, feql_weight_fft,
+               feql_p4m_weight_fft, feql_p4m_weight_fft_bytes, feql_scan_backward,
+               feql_scan_forward, feql_scan_save_bytes, feql_scan_step, feql_weight_fft,
                feql_weight_fft_bytes)
 
 
@@ -177,3 +179,170 @@ def mlp_forward(x: torch.Tensor, What: torch.Tensor, b1, b2, H: int, Co: int, mo
     y = torch.empty((N, Co, 4), dtype=x.dtype, device=x.device)
     feql_mlp_forward(x, What, b1, b2, y, N, C, H, Co, mode, stream)
     return y
+
+
+# ------------------------------------------- operators between the layers
+# These take CUDA tensors of any strides (a dense copy is made where needed) on
+# one device, which need not be the current one, and run on torch's current
+# stream of that device; what they return belongs to that stream.
+
+def _on(t: torch.Tensor):
+    """The device guard of a call on ``t``'s device."""
+    if not t.is_cuda:
+        raise ValueError(f"expected CUDA tensors (libfeql.so kernels), got one on {t.device}")
+    return torch.cuda.device(t.device)
+
+
+def _mode(t: torch.Tensor) -> int:
+    if t.dtype == torch.float16:
+        return FEQL_FP16
+    if t.dtype == torch.float32:
+        return FEQL_FP32
+    raise TypeError(f"expected float16 or float32 data, not {t.dtype}")
+
+
+def _take(t, name: str, shape, dtype, device):
+    """``t`` checked and dense, on a 16-byte boundary; None stays None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    t = t.detach()
+    if not t.is_contiguous():
+        t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def norm_forward(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5,
+                 save_stats: bool = True):
+    """Layer norm of (N, C, T) features over C*T, affine per channel: (y, stats).
+
+    ``stats`` (N, 2) fp32 (mean, reciprocal deviation) is what norm_backward
+    takes; None without ``save_stats``.
+    """
+    if x.dim() != 3:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected (N, C, T)")
+    N, C, T = x.shape
+    mode = _mode(x)
+    with _on(x):
+        x = _take(x, "x", x.shape, x.dtype, x.device)
+        gamma = _take(gamma, "gamma", (C,), x.dtype, x.device)
+        beta = _take(beta, "beta", (C,), x.dtype, x.device)
+        y = torch.empty_like(x)
+        stats = (torch.empty((N, 2), dtype=torch.float32, device=x.device) if save_stats
+                 else None)
+        feql_norm_forward(x, gamma, beta, y, stats, N, C, T, eps, mode)
+    return y, stats
+
+
+def norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, gamma=None,
+                  with_params: bool = True):
+    """dx, dgamma, dbeta (None, None without ``with_params``) of norm_forward."""
+    if x.dim() != 3:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected (N, C, T)")
+    N, C, T = x.shape
+    mode = _mode(x)
+    with _on(x):
+        x = _take(x, "x", x.shape, x.dtype, x.device)
+        dy = _take(dy, "dy", x.shape, x.dtype, x.device)
+        stats = _take(stats, "stats", (N, 2), torch.float32, x.device)
+        gamma = _take(gamma, "gamma", (C,), x.dtype, x.device)
+        dx = torch.empty_like(x)
+        dgamma = dbeta = None
+        if with_params:
+            dgamma = torch.empty((C,), dtype=x.dtype, device=x.device)
+            dbeta = torch.empty((C,), dtype=x.dtype, device=x.device)
+        nbytes = feql_norm_backward_workspace_bytes(N, C, T, mode)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+        feql_norm_backward(x, dy, stats, gamma, dx, dgamma, dbeta, ws, ws.numel(), N, C, T, mode)
+    return dx, dgamma, dbeta
+
+
+def _scan_sizes(u: torch.Tensor, g: torch.Tensor, offsets):
+    """(B, N, C, T, shared) of a dense (B, L, C, T) or packed (N, C, T) input."""
+    if offsets is None:
+        if u.dim() != 4:
+            raise ValueError(f"u has shape {tuple(u.shape)}, expected (B, L, C, T), or "
+                             "(N, C, T) with offsets")
+        B, N = u.shape[0], u.shape[0] * u.shape[1]
+    else:
+        if u.dim() != 3:
+            raise ValueError(f"u has shape {tuple(u.shape)}, expected (N, C, T) with offsets")
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError("offsets has shape (B + 1,)")
+        B, N = offsets.numel() - 1, u.shape[0]
+    C, T = u.shape[-2:]
+    if g.shape not in (u.shape, u.shape[:-1]):
+        raise ValueError(f"g has shape {tuple(g.shape)}, expected {tuple(u.shape)} or, with one "
+                         f"gate per channel, {tuple(u.shape[:-1])}")
+    return B, N, C, T, g.dim() < u.dim()
+
+
+def scan_forward(u: torch.Tensor, g: torch.Tensor, h0=None, offsets=None, save: bool = True):
+    """h_l = a_l h_{l-1} + (1 - a_l) u_l with a = sigmoid(g): (h, hN, saved).
+
+    Dense: u (B, L, C, T).  Packed: u (N, C, T) and ``offsets`` (B + 1,) int32,
+    sequence b in rows offsets[b]..offsets[b + 1].  g has u's shape, or lacks its
+    last axis (one gate per channel).  h0 and hN are (B, C, T) fp32 states;
+    ``saved`` is what scan_backward takes (None without ``save``).
+    """
+    B, N, C, T, shared = _scan_sizes(u, g, offsets)
+    mode = _mode(u)
+    with _on(u):
+        dev = u.device
+        u = _take(u, "u", u.shape, u.dtype, dev)
+        g = _take(g, "g", g.shape, u.dtype, dev)
+        h0 = _take(h0, "h0", (B, C, T), torch.float32, dev)
+        offsets = _take(offsets, "offsets", (B + 1,), torch.int32, dev)
+        h = torch.empty_like(u)
+        hN = torch.empty((B, C, T), dtype=torch.float32, device=dev)
+        saved = None
+        if save:
+            nbytes = feql_scan_save_bytes(B, N, C, T, shared, mode)
+            saved = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        feql_scan_forward(u, g, h0, offsets, h, hN, saved, B, N, C, T, shared, mode)
+    return h, hN, saved
+
+
+def scan_backward(dh: torch.Tensor, u: torch.Tensor, g: torch.Tensor, saved: torch.Tensor,
+                  dhN=None, offsets=None):
+    """du, dg, dh0 of scan_forward on the same u, g and offsets."""
+    B, N, C, T, shared = _scan_sizes(u, g, offsets)
+    mode = _mode(u)
+    with _on(u):
+        dev = u.device
+        u = _take(u, "u", u.shape, u.dtype, dev)
+        g = _take(g, "g", g.shape, u.dtype, dev)
+        dh = _take(dh, "dh", u.shape, u.dtype, dev)
+        dhN = _take(dhN, "dhN", (B, C, T), torch.float32, dev)
+        offsets = _take(offsets, "offsets", (B + 1,), torch.int32, dev)
+        nbytes = max(feql_scan_save_bytes(B, N, C, T, shared, mode), 16)
+        saved = _take(saved, "saved", (nbytes,), torch.uint8, dev)
+        du, dg = torch.empty_like(u), torch.empty_like(g)
+        dh0 = torch.empty((B, C, T), dtype=torch.float32, device=dev)
+        feql_scan_backward(dh, u, g, saved, dhN, offsets, du, dg, dh0, B, N, C, T, shared, mode)
+    return du, dg, dh0
+
+
+def scan_step(u: torch.Tensor, g: torch.Tensor, state: torch.Tensor) -> torch.Tensor:
+    """One token of each sequence: u (B, C, T), g (B, C, T) or (B, C); the fp32
+    ``state`` (B, C, T) is updated in place and returned rounded to u's type."""
+    if u.dim() != 3:
+        raise ValueError(f"u has shape {tuple(u.shape)}, expected (B, C, T)")
+    B, C, T = u.shape
+    if g.shape not in (u.shape, u.shape[:-1]):
+        raise ValueError(f"g has shape {tuple(g.shape)}, expected {(B, C, T)} or {(B, C)}")
+    mode = _mode(u)
+    with _on(u):
+        if not state.is_contiguous() or state.data_ptr() % 16 != 0:
+            raise ValueError("state is updated in place: it has to be dense and 16-byte aligned")
+        u = _take(u, "u", u.shape, u.dtype, u.device)
+        g = _take(g, "g", g.shape, u.dtype, u.device)
+        s = _take(state, "state", (B, C, T), torch.float32, u.device)
+        h = torch.empty_like(u)
+        feql_scan_step(u, g, s, h, B, C, T, g.dim() < 3, mode)
+    return h

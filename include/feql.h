@@ -251,6 +251,73 @@ int feql_mlp_weight_fft(const void *W1, const void *W2, void *What, int C, int H
 int feql_mlp_forward(const void *x, const void *What, const void *b1, const void *b2, void *y,
                      int64_t N, int C, int H, int Co, int dtype, feql_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators that stand between the layers of an equivariant network (the
+ * EQ-ViT / EQ-Swin / EQ-VMamba blocks of the technical summary, "Livello di
+ * Rete", and the arXiv abstract).  Features are (C, T) per token, the group
+ * index innermost; T = 1 is the ordinary operator on C features.  They serve
+ * any regular representation of a group of order T (1 <= T <= 16, else
+ * FEQL_ERR_UNSUPPORTED): parameters and statistics are shared over the group
+ * axis and all else is pointwise in it, so they commute with the group's
+ * action.  dtype: fp16 data for FEQL_FP16 and FEQL_FP16_SIMT, fp32 for the
+ * others; arithmetic in fp32.  Pointers, streams, errors and N == 0 as above. */
+
+/* Layer norm over all C*T features of a token, affine per channel:
+ *   y[n,c,t] = (x[n,c,t] - mu_n) r_n gamma[c] + beta[c],  r = (var + eps)^-1/2
+ * with the biased variance.  fp32 data must keep (x - mu)^2 below 3.4e38.
+ *   x, y        : device [N][C][T]       gamma, beta : [C] or NULL (1, 0)
+ *   stats       : device fp32 [N][2] (mu, r) for the backward pass, or NULL
+ *   eps         : > 0, finite */
+int feql_norm_forward(const void *x, const void *gamma, const void *beta, void *y, float *stats,
+                      int64_t N, int C, int T, float eps, int dtype, feql_stream stream);
+
+/* Workspace (bytes) feql_norm_backward needs on the current device. */
+size_t feql_norm_backward_workspace_bytes(int64_t N, int C, int T, int dtype);
+
+/* With xh = (x - mu) r and g = dy gamma: dx = r (g - mean(g) - xh mean(g xh)),
+ * dgamma[c] = sum_{n,t} dy xh, dbeta[c] = sum_{n,t} dy (fp32 sums in a fixed
+ * order: bit-identical run to run).
+ *   dx : device [N][C][T] (written)      dgamma, dbeta : [C] or NULL (written) */
+int feql_norm_backward(const void *x, const void *dy, const float *stats, const void *gamma,
+                       void *dx, void *dgamma, void *dbeta, void *ws, size_t ws_bytes, int64_t N,
+                       int C, int T, int dtype, feql_stream stream);
+
+/* Gated linear recurrence over the tokens of B sequences,
+ *   h_l = a_l h_{l-1} + (1 - a_l) u_l,   a = 1 / (1 + exp(-g)),   h_{-1} = h0,
+ * per feature (c, t); gate logits g per channel (shared != 0: g[N][C], one gate
+ * for the T group elements) or per feature (g[N][C][T]).
+ * Dense: offsets NULL, N = B L rows, sequence b in rows [b L, (b+1) L).
+ * Packed: offsets (device int32 [B+1], ascending), sequence b in rows
+ * [offsets[b], offsets[b+1]) of N, none or many; rows of h (and of du, dg) that
+ * belong to no sequence are set to zero.  Offsets outside 0..N are clamped;
+ * descending ones give unspecified values.
+ *   u, h  : device [N][C][T]
+ *   h0    : device fp32 [B][C][T] or NULL (zero)   hN : the same, the states
+ *           after the last rows (h0 for an empty sequence), or NULL
+ *   save  : device, feql_scan_save_bytes(...) bytes for the backward pass, or
+ *           NULL.  Opaque; belongs to these B, N, C, T, shared, dtype, offsets
+ *           and device.
+ * States are fp32 throughout. */
+size_t feql_scan_save_bytes(int64_t B, int64_t N, int C, int T, int shared, int dtype);
+int feql_scan_forward(const void *u, const void *g, const float *h0, const int32_t *offsets,
+                      void *h, float *hN, void *save, int64_t B, int64_t N, int C, int T,
+                      int shared, int dtype, feql_stream stream);
+
+/* Gradients of <dh, h> + <dhN, hN>:
+ *   delta_l = dh_l + a_{l+1} delta_{l+1} (+ dhN at the last row),
+ *   du = (1 - a) delta,  dg = delta (h_{l-1} - u) a (1 - a) (summed over T for
+ *   shared gates),  dh0 = a_0 delta_0 (dhN for an empty sequence).
+ *   dhN : device fp32 [B][C][T] or NULL (zero)   dh0 : the same, or NULL */
+int feql_scan_backward(const void *dh, const void *u, const void *g, const void *save,
+                       const float *dhN, const int32_t *offsets, void *du, void *dg, float *dh0,
+                       int64_t B, int64_t N, int C, int T, int shared, int dtype,
+                       feql_stream stream);
+
+/* One token of each of B sequences: state (fp32 [B][C][T]) becomes
+ * a state + (1 - a) u in place, h [B][C][T] its value in the data type. */
+int feql_scan_step(const void *u, const void *g, float *state, void *h, int64_t B, int C, int T,
+                   int shared, int dtype, feql_stream stream);
+
 /* Synchronises `stream`, then returns and clears the device-side status word
  * of the current device: FEQL_OK, or FEQL_ERR_TIMEOUT when some kernel gave up
  * on a bounded wait since the last call (its outputs are then undefined). */
