@@ -34,6 +34,15 @@ DTYPES = {"fp16": FEQL_FP16, "fp32": FEQL_FP32, "fp32_simt": FEQL_FP32_SIMT,
           "fp32_3xtf32": FEQL_FP32_3XTF32, "fp16_simt": FEQL_FP16_SIMT}
 
 
+FEQL_ACT_NONE = 0
+FEQL_ACT_RELU = 1
+FEQL_ACT_GELU = 2
+FEQL_ACT_SILU = 3
+
+ACTIVATIONS = {"none": FEQL_ACT_NONE, "relu": FEQL_ACT_RELU, "gelu": FEQL_ACT_GELU,
+               "silu": FEQL_ACT_SILU}
+
+
 class FeqlError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -72,6 +81,15 @@ _SIGNATURES = {
     "feql_mlp_weight_fft_bytes": (_SZ, [_I, _I, _I, _I]),
     "feql_mlp_weight_fft": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _VP]),
     "feql_mlp_forward": (_I, [_VP, _VP, _VP, _VP, _VP, _I64, _I, _I, _I, _I, _VP]),
+    "feql_forward_act": (_I, [_VP] * 6 + [_I64, _I, _I, _I, _I, _VP]),
+    "feql_ct_forward_act": (_I, [_I] + [_VP] * 6 + [_I64, _I, _I, _I, _I, _VP]),
+    "feql_p4m_forward_act": (_I, [_VP] * 6 + [_I64, _I, _I, _I, _I, _VP]),
+    "feql_backward_act_workspace_bytes": (_SZ, [_I64, _I, _I, _I, _I]),
+    "feql_backward_act": (_I, [_VP] * 8 + [_SZ, _I64, _I, _I, _I, _I, _VP]),
+    "feql_ct_backward_act_workspace_bytes": (_SZ, [_I, _I64, _I, _I, _I, _I]),
+    "feql_ct_backward_act": (_I, [_I] + [_VP] * 8 + [_SZ, _I64, _I, _I, _I, _I, _VP]),
+    "feql_p4m_backward_act_workspace_bytes": (_SZ, [_I64, _I, _I, _I, _I]),
+    "feql_p4m_backward_act": (_I, [_VP] * 8 + [_SZ, _I64, _I, _I, _I, _I, _VP]),
     "feql_norm_forward": (_I, [_VP, _VP, _VP, _VP, _VP, _I64, _I, _I, _F, _I, _VP]),
     "feql_norm_backward_workspace_bytes": (_SZ, [_I64, _I, _I, _I]),
     "feql_norm_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _I64, _I, _I, _I,
@@ -248,6 +266,63 @@ def feql_mlp_forward(x, What, b1, b2, y, N: int, C: int, H: int, Co: int, dtype:
                      stream=None) -> None:
     _check(load().feql_mlp_forward(_ptr(x), _ptr(What), _ptr(b1), _ptr(b2), _ptr(y), N, C, H, Co,
                                    dtype, _stream(stream)), "feql_mlp_forward")
+
+
+def feql_forward_act(x, What, b, res, y, z, N: int, C: int, D: int, act: int,
+                     dtype: int, stream=None) -> None:
+    _check(load().feql_forward_act(_ptr(x), _ptr(What), _ptr(b), _ptr(res), _ptr(y),
+                                   _ptr(z), N, C, D, act, dtype, _stream(stream)),
+           "feql_forward_act")
+
+
+def feql_backward_act_workspace_bytes(N: int, C: int, D: int, act: int,
+                                      dtype: int) -> int:
+    return int(load().feql_backward_act_workspace_bytes(N, C, D, act, dtype))
+
+
+def feql_backward_act(x, dy, z, What, dx, dW, db, ws, ws_bytes: int, N: int, C: int,
+                      D: int, act: int, dtype: int, stream=None) -> None:
+    _check(load().feql_backward_act(_ptr(x), _ptr(dy), _ptr(z), _ptr(What), _ptr(dx),
+                                    _ptr(dW), _ptr(db), _ptr(ws), ws_bytes, N, C, D,
+                                    act, dtype, _stream(stream)), "feql_backward_act")
+
+
+def feql_ct_forward_act(T: int, x, What, b, res, y, z, N: int, C: int, D: int, act: int,
+                        dtype: int, stream=None) -> None:
+    _check(load().feql_ct_forward_act(T, _ptr(x), _ptr(What), _ptr(b), _ptr(res), _ptr(y),
+                                      _ptr(z), N, C, D, act, dtype, _stream(stream)),
+           "feql_ct_forward_act")
+
+
+def feql_ct_backward_act_workspace_bytes(T: int, N: int, C: int, D: int, act: int,
+                                         dtype: int) -> int:
+    return int(load().feql_ct_backward_act_workspace_bytes(T, N, C, D, act, dtype))
+
+
+def feql_ct_backward_act(T: int, x, dy, z, What, dx, dW, db, ws, ws_bytes: int, N: int, C: int,
+                         D: int, act: int, dtype: int, stream=None) -> None:
+    _check(load().feql_ct_backward_act(T, _ptr(x), _ptr(dy), _ptr(z), _ptr(What), _ptr(dx),
+                                       _ptr(dW), _ptr(db), _ptr(ws), ws_bytes, N, C, D,
+                                       act, dtype, _stream(stream)), "feql_ct_backward_act")
+
+
+def feql_p4m_forward_act(x, What, b, res, y, z, N: int, C: int, D: int, act: int,
+                         dtype: int, stream=None) -> None:
+    _check(load().feql_p4m_forward_act(_ptr(x), _ptr(What), _ptr(b), _ptr(res), _ptr(y),
+                                       _ptr(z), N, C, D, act, dtype, _stream(stream)),
+           "feql_p4m_forward_act")
+
+
+def feql_p4m_backward_act_workspace_bytes(N: int, C: int, D: int, act: int,
+                                          dtype: int) -> int:
+    return int(load().feql_p4m_backward_act_workspace_bytes(N, C, D, act, dtype))
+
+
+def feql_p4m_backward_act(x, dy, z, What, dx, dW, db, ws, ws_bytes: int, N: int, C: int,
+                          D: int, act: int, dtype: int, stream=None) -> None:
+    _check(load().feql_p4m_backward_act(_ptr(x), _ptr(dy), _ptr(z), _ptr(What), _ptr(dx),
+                                        _ptr(dW), _ptr(db), _ptr(ws), ws_bytes, N, C, D,
+                                        act, dtype, _stream(stream)), "feql_p4m_backward_act")
 
 
 def feql_norm_forward(x, gamma, beta, y, stats, N: int, C: int, T: int, eps: float, dtype: int,

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/feql.h"
+#include "act.cuh"
 #include "host.cuh"
 #include "plan.cuh"
 #include "simt.cuh"
@@ -46,23 +47,38 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// cuTensorMapEncodeTiled through the entry point.  A thread that has made no
+// runtime call yet (an autograd engine's, say) has no current context and the
+// driver refuses: then the current device's primary context is made current, as
+// any runtime call would, and the encoding repeated.
+int encode_tiled(CUtensorMap *m, CUtensorMapDataType type, cuuint32_t rank, const void *base,
+                 const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                 CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return FEQL_ERR_CUDA;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    if (enc(m, type, rank, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+      return FEQL_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) break;
+  }
+  return FEQL_ERR_CUDA;
+}
+
 // Row-major fp16 matrix [rows][cols] viewed as a 2-D tensor; box = 64 cols x box_rows
 // rows, 128-byte swizzle, zero fill out of range.
 // Box of box_cols x box_rows, 128-byte swizzle (64 columns: 128-byte rows), or
 // without swizzle for other widths (the 96-byte rows of 8 channels x 6).
 int make_tmap_f16(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
                   int box_rows = kBM, int box_cols = 64) {
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return FEQL_ERR_CUDA;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? FEQL_OK : FEQL_ERR_CUDA;
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box,
+                      box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // A [rows][row_elems] fp16 tensor seen as a stack of 64-element (128-byte)
@@ -73,20 +89,15 @@ int make_tmap_f16(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
 // the next row).
 int make_tmap_f16_boxes(CUtensorMap *m, const void *base, int64_t rows, int64_t row_elems,
                         int box_rows, int box_count, int box_cols = 64) {
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr || row_elems % box_cols != 0) return FEQL_ERR_CUDA;
+  if (row_elems % box_cols != 0) return FEQL_ERR_CUDA;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(box_cols), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(row_elems / box_cols)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_elems) * 2,
                            static_cast<cuuint64_t>(box_cols) * 2};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows),
                        static_cast<cuuint32_t>(box_count)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? FEQL_OK : FEQL_ERR_CUDA;
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box,
+                      box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // Row-major fp32 matrix [rows][cols] viewed as a 2-D tensor; box = 32 cols (128
@@ -95,16 +106,11 @@ int make_tmap_f16_boxes(CUtensorMap *m, const void *base, int64_t rows, int64_t 
 // elements of fp32 per row.
 int make_tmap_f32(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
                   int box_rows = kBM) {
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return FEQL_ERR_CUDA;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 4};
   cuuint32_t box[2] = {32, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? FEQL_OK : FEQL_ERR_CUDA;
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Resolves FEQL_FP32 to the library's fp32 algorithm.
@@ -134,8 +140,10 @@ int grid_for(int64_t work, int threads, int sms) {
 
 // ---------------------------------------------------------------- tc launch
 // tf32: fp32 data in the split-TF32 mode (FEQL_FP32_3XTF32), else fp16.
+// ep: activation, residual and saved z, or nullptr.
 int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const void *bias,
-                   void *out, int64_t N, cudaStream_t stream, bool tf32 = false) {
+                   void *out, int64_t N, cudaStream_t stream, bool tf32 = false,
+                   const Epilogue *ep = nullptr) {
   DeviceInfo dev;
   int st = device_info(&dev);
   if (st != FEQL_OK) return st;
@@ -189,6 +197,11 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
             : make_tmap_f16(&tm_in, in, N, static_cast<int64_t>(P.Ci) * kT);
   if (st != FEQL_OK) return st;
   auto kernel = tf32 ? tc_fourier_gemm_kernel<true> : tc_fourier_gemm_kernel<false>;
+  p.ep = {};
+  if (ep != nullptr) {
+    p.ep = *ep;
+    kernel = tf32 ? tc_fourier_gemm_kernel<true, true> : tc_fourier_gemm_kernel<false, true>;
+  }
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return FEQL_ERR_CUDA;
   kernel<<<grid, kTcThreads, smem, stream>>>(tm_in, p);
@@ -197,14 +210,15 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
 
 template <typename T>
 int launch_simt_fwd(const void *in, const float *Wp, const void *bias, void *out, int64_t N,
-                    int Ci, int Do, cudaStream_t stream) {
+                    int Ci, int Do, cudaStream_t stream, const Epilogue *ep = nullptr) {
   const int64_t gx = cdiv(N, kSimtTile);
   if (gx > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(Do, kSimtTile)));
   if (grid.y > 65535) return FEQL_ERR_UNSUPPORTED;
-  simt_fwd_kernel<T><<<grid, kSimtThreads, 0, stream>>>(
+  auto kernel = ep != nullptr ? simt_fwd_kernel<T, true> : simt_fwd_kernel<T>;
+  kernel<<<grid, kSimtThreads, 0, stream>>>(
       static_cast<const T *>(in), Wp, static_cast<const T *>(bias), static_cast<T *>(out), N, Ci,
-      Do);
+      Do, ep != nullptr ? *ep : Epilogue{});
   return launch_status();
 }
 
@@ -391,7 +405,7 @@ int launch_tc_bwd(TcBwdParams p, const void *x, const void *dy, const uint8_t *w
 // ---------------------------------------------------------------------------
 template <class Gp>
 int launch_g8_fwd(const void *in, const uint8_t *wt, const G8Plan &P, const __half *bias,
-                   void *out, int64_t N, cudaStream_t stream) {
+                   void *out, int64_t N, cudaStream_t stream, const Epilogue *ep = nullptr) {
   DeviceInfo dev;
   int st = device_info(&dev);
   if (st != FEQL_OK) return st;
@@ -435,11 +449,13 @@ int launch_g8_fwd(const void *in, const uint8_t *wt, const G8Plan &P, const __ha
   st = make_tmap_f16(&tm_out, out, N, static_cast<int64_t>(P.Do) * T, 32, 8 * T);
   if (st != FEQL_OK) return st;
   const int smem = g8_fwd_smem(p).total + 1024;
-  if (cudaFuncSetAttribute(tc_g8_fwd_kernel<Gp>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+  auto kernel = ep != nullptr ? tc_g8_fwd_kernel<Gp, true> : tc_g8_fwd_kernel<Gp>;
+  p.ep = ep != nullptr ? *ep : Epilogue{};
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return FEQL_ERR_CUDA;
   const int grid = p.n_units < dev.sms ? p.n_units : dev.sms;
-  tc_g8_fwd_kernel<Gp><<<grid, kG8Threads, smem, stream>>>(tm, tm_out, p);
+  kernel<<<grid, kG8Threads, smem, stream>>>(tm, tm_out, p);
   return launch_status();
 }
 
@@ -616,14 +632,15 @@ int ct_simt_wfft_launch(const void *W, void *What, int C, int D, cudaStream_t s,
 
 template <int T, typename Ty>
 int ct_simt_pass_launch(const void *in, const float *Wp, const void *bias, void *out, int64_t N,
-                        int Ci, int Do, cudaStream_t s) {
+                        int Ci, int Do, cudaStream_t s, const Epilogue *ep) {
   const int64_t gx = cdiv(N, kCtTile);
   if (gx > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(Do, kCtTile)));
   if (grid.y > 65535) return FEQL_ERR_UNSUPPORTED;
-  ct_simt_fwd_kernel<T, Ty><<<grid, kCtThreads, 0, s>>>(
-      static_cast<const Ty *>(in), Wp, static_cast<const Ty *>(bias), static_cast<Ty *>(out), N,
-      Ci, Do);
+  auto kernel = ep != nullptr ? ct_simt_fwd_kernel<T, Ty, true> : ct_simt_fwd_kernel<T, Ty>;
+  kernel<<<grid, kCtThreads, 0, s>>>(static_cast<const Ty *>(in), Wp,
+                                     static_cast<const Ty *>(bias), static_cast<Ty *>(out), N, Ci,
+                                     Do, ep != nullptr ? *ep : Epilogue{});
   return launch_status();
 }
 
@@ -682,9 +699,9 @@ int ct_simt_wfft(int T, const void *W, void *What, int C, int D, cudaStream_t s,
 
 template <typename Ty>
 int ct_simt_pass(int T, const void *in, const float *Wp, const void *bias, void *out, int64_t N,
-                 int Ci, int Do, cudaStream_t s) {
+                 int Ci, int Do, cudaStream_t s, const Epilogue *ep = nullptr) {
   switch (T) {
-#define FEQL_CASE(t) case t: return ct_simt_pass_launch<t, Ty>(in, Wp, bias, out, N, Ci, Do, s);
+#define FEQL_CASE(t) case t: return ct_simt_pass_launch<t, Ty>(in, Wp, bias, out, N, Ci, Do, s, ep);
     FEQL_CT_ORDERS(FEQL_CASE)
 #undef FEQL_CASE
     default: return FEQL_ERR_UNSUPPORTED;
@@ -735,7 +752,7 @@ int g8_weight_fft(const void *W, void *What, int C, int D, feql_stream stream) {
 
 template <class Gp>
 int g8_pass(const void *in, const void *What, const void *bias, void *out, int64_t N, int C, int D,
-            feql_stream stream, int dir) {
+            feql_stream stream, int dir, const Epilogue *ep = nullptr) {
   if (N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK) return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (in == nullptr || What == nullptr || out == nullptr)) return FEQL_ERR_INVALID_ARG;
   if (!aligned16(in) || !aligned16(What) || !aligned16(out)) return FEQL_ERR_INVALID_ARG;
@@ -744,7 +761,7 @@ int g8_pass(const void *in, const void *What, const void *bias, void *out, int64
   const G8Layout L = make_g8_layout(C, D, Gp::kWRows);
   const uint8_t *wt = static_cast<const uint8_t *>(What) + (dir == 0 ? L.off_fwd : L.off_dx);
   return launch_g8_fwd<Gp>(in, wt, dir == 0 ? L.fwd : L.dx, static_cast<const __half *>(bias),
-                           out, N, reinterpret_cast<cudaStream_t>(stream));
+                           out, N, reinterpret_cast<cudaStream_t>(stream), ep);
 }
 
 size_t g8_dw_workspace_bytes(int64_t N, int C, int D, int T) {
@@ -808,7 +825,8 @@ int feql_weight_fft(const void *W, void *What, int C, int D, int dtype, feql_str
 }
 
 static int pass_common(const void *in, const void *What, const void *bias, void *out, int64_t N,
-                       int C, int D, int dtype, feql_stream stream, int dir) {
+                       int C, int D, int dtype, feql_stream stream, int dir,
+                       const Epilogue *ep = nullptr) {
   if (!valid_dtype(dtype) || N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK)
     return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (in == nullptr || What == nullptr || out == nullptr)) return FEQL_ERR_INVALID_ARG;
@@ -822,15 +840,15 @@ static int pass_common(const void *in, const void *What, const void *bias, void 
   const int Ci = dir == 0 ? C : D, Do = dir == 0 ? D : C;
   if (is_tf32(dt)) {
     const uint8_t *wt = static_cast<const uint8_t *>(What) + (dir == 0 ? L.off_fwd : L.off_dx);
-    return launch_tc_gemm(in, wt, dir == 0 ? L.fwd : L.dx, bias, out, N, s, true);
+    return launch_tc_gemm(in, wt, dir == 0 ? L.fwd : L.dx, bias, out, N, s, true, ep);
   }
   if (is_tc(dt)) {
     const uint8_t *wt = static_cast<const uint8_t *>(What) + (dir == 0 ? L.off_fwd : L.off_dx);
-    return launch_tc_gemm(in, wt, dir == 0 ? L.fwd : L.dx, bias, out, N, s);
+    return launch_tc_gemm(in, wt, dir == 0 ? L.fwd : L.dx, bias, out, N, s, false, ep);
   }
   const float *Wp = static_cast<const float *>(What) + (dir == 0 ? L.off_fwd : L.off_dx) / 4;
-  if (is_half(dt)) return launch_simt_fwd<__half>(in, Wp, bias, out, N, Ci, Do, s);
-  return launch_simt_fwd<float>(in, Wp, bias, out, N, Ci, Do, s);
+  if (is_half(dt)) return launch_simt_fwd<__half>(in, Wp, bias, out, N, Ci, Do, s, ep);
+  return launch_simt_fwd<float>(in, Wp, bias, out, N, Ci, Do, s, ep);
 }
 
 int feql_forward(const void *x, const void *What, const void *b, void *y, int64_t N, int C, int D,
@@ -961,12 +979,13 @@ int feql_ct_weight_fft(int T, const void *W, void *What, int C, int D, int dtype
 }
 
 static int ct_pass(int T, const void *in, const void *What, const void *bias, void *out, int64_t N,
-                   int C, int D, int dtype, feql_stream stream, int dir) {
+                   int C, int D, int dtype, feql_stream stream, int dir,
+                   const Epilogue *ep = nullptr) {
   int path = 0;
   const int st = ct_route(T, C, D, dtype, &path);
   if (st != FEQL_OK) return st;
-  if (path == kCtTensor8) return g8_pass<Cyclic8>(in, What, bias, out, N, C, D, stream, dir);
-  if (path == kCtTensor6) return g8_pass<Cyclic6>(in, What, bias, out, N, C, D, stream, dir);
+  if (path == kCtTensor8) return g8_pass<Cyclic8>(in, What, bias, out, N, C, D, stream, dir, ep);
+  if (path == kCtTensor6) return g8_pass<Cyclic6>(in, What, bias, out, N, C, D, stream, dir, ep);
   if (N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK) return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (in == nullptr || What == nullptr || out == nullptr)) return FEQL_ERR_INVALID_ARG;
   if (!aligned16(in) || !aligned16(What) || !aligned16(out)) return FEQL_ERR_INVALID_ARG;
@@ -975,8 +994,8 @@ static int ct_pass(int T, const void *in, const void *What, const void *bias, vo
   const float *Wp = static_cast<const float *>(What) + (dir == 0 ? 0 : static_cast<int64_t>(T) * C * D);
   const int Ci = dir == 0 ? C : D, Do = dir == 0 ? D : C;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return is_half(resolve(dtype)) ? ct_simt_pass<__half>(T, in, Wp, bias, out, N, Ci, Do, s)
-                                 : ct_simt_pass<float>(T, in, Wp, bias, out, N, Ci, Do, s);
+  return is_half(resolve(dtype)) ? ct_simt_pass<__half>(T, in, Wp, bias, out, N, Ci, Do, s, ep)
+                                 : ct_simt_pass<float>(T, in, Wp, bias, out, N, Ci, Do, s, ep);
 }
 
 int feql_ct_forward(int T, const void *x, const void *What, const void *b, void *y, int64_t N,
@@ -1065,6 +1084,160 @@ int feql_p4m_backward_dw(const void *x, const void *dy, void *dW, void *db, void
   const int st = p4m_check(dtype);
   if (st != FEQL_OK) return st;
   return g8_dw<Dihedral4>(x, dy, dW, db, ws, ws_bytes, N, C, D, stream);
+}
+
+// ------------------------------------------- activation and residual epilogue
+// The layer's group: p4m, or the cyclic group of order T.
+struct GroupKind {
+  bool p4m;
+  int T;
+};
+
+// What the entry points of the layer check before they launch, for calls that
+// launch something else first.
+static int act_check(GroupKind G, int64_t N, int C, int D, int act, int dtype) {
+  if (act < FEQL_ACT_NONE || act > FEQL_ACT_SILU) return FEQL_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype) || N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK)
+    return FEQL_ERR_INVALID_ARG;
+  if (G.p4m) return p4m_check(dtype);
+  if (G.T == kT)
+    return is_tc(resolve(dtype, C, D)) && ((C | D) & 1) ? FEQL_ERR_UNSUPPORTED : FEQL_OK;
+  int path = 0;
+  return ct_route(G.T, C, D, dtype, &path);
+}
+
+static int forward_act(GroupKind G, const void *x, const void *What, const void *b, const void *res,
+                       void *y, void *z, int64_t N, int C, int D, int act, int dtype,
+                       feql_stream stream) {
+  const int st = act_check(G, N, C, D, act, dtype);
+  if (st != FEQL_OK) return st;
+  if (!aligned16(res) || !aligned16(z)) return FEQL_ERR_INVALID_ARG;
+  const Epilogue e = make_epilogue(act, res, z);
+  const Epilogue *ep = act == FEQL_ACT_NONE && res == nullptr && z == nullptr ? nullptr : &e;
+  if (G.p4m) return g8_pass<Dihedral4>(x, What, b, y, N, C, D, stream, 0, ep);
+  if (G.T == kT) return pass_common(x, What, b, y, N, C, D, dtype, stream, 0, ep);
+  return ct_pass(G.T, x, What, b, y, N, C, D, dtype, stream, 0, ep);
+}
+
+// Workspace of the activation's backward pass: the weight gradient's, then dz.
+struct ActWorkspace {
+  size_t dw, dz, total;
+};
+
+static ActWorkspace act_workspace(GroupKind G, int64_t N, int C, int D, int act, int dtype) {
+  ActWorkspace w;
+  w.dw = G.p4m ? feql_p4m_backward_dw_workspace_bytes(N, C, D, dtype)
+               : feql_ct_backward_dw_workspace_bytes(G.T, N, C, D, dtype);
+  w.dz = static_cast<size_t>(align_up(static_cast<int64_t>(w.dw), 256));
+  w.total = w.dz + (act == FEQL_ACT_NONE
+                        ? 0
+                        : static_cast<size_t>(N) * D * G.T * (is_half(dtype) ? 2 : 4));
+  return w;
+}
+
+static size_t backward_act_workspace_bytes(GroupKind G, int64_t N, int C, int D, int act,
+                                           int dtype) {
+  if (act_check(G, N, C, D, act, dtype) != FEQL_OK) return 0;
+  const ActWorkspace w = act_workspace(G, N, C, D, act, dtype);
+  return w.total > 16 ? w.total : 16;
+}
+
+static int backward_act(GroupKind G, const void *x, const void *dy, const void *z,
+                        const void *What, void *dx, void *dW, void *db, void *ws, size_t ws_bytes,
+                        int64_t N, int C, int D, int act, int dtype, feql_stream stream) {
+  int st = act_check(G, N, C, D, act, dtype);
+  if (st != FEQL_OK) return st;
+  if (ws == nullptr || (dx == nullptr && dW == nullptr) || (dW == nullptr && db != nullptr))
+    return FEQL_ERR_INVALID_ARG;
+  if (N > 0 && (dy == nullptr || (act != FEQL_ACT_NONE && z == nullptr) ||
+                (dx != nullptr && What == nullptr) || (dW != nullptr && x == nullptr)))
+    return FEQL_ERR_INVALID_ARG;
+  const void *all[] = {x, dy, z, What, dx, dW, db, ws};
+  for (const void *p : all)
+    if (!aligned16(p)) return FEQL_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  st = device_info(&dev);
+  if (st != FEQL_OK) return st;
+  const ActWorkspace w = act_workspace(G, N, C, D, act, dtype);
+  if (ws_bytes < w.total) return FEQL_ERR_INVALID_ARG;
+  const void *dz = dy;
+  if (act != FEQL_ACT_NONE && N > 0) {
+    const int64_t n = N * D * G.T;
+    void *to = static_cast<uint8_t *>(ws) + w.dz;
+    const Epilogue e = make_epilogue(act, nullptr, nullptr);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (is_half(dtype))
+      act_bwd_kernel<__half, 8><<<grid_for(n / 8 + 1, 256, dev.sms), 256, 0, s>>>(
+          static_cast<const __half *>(dy), static_cast<const __half *>(z),
+          static_cast<__half *>(to), n, e);
+    else
+      act_bwd_kernel<float, 4><<<grid_for(n / 4 + 1, 256, dev.sms), 256, 0, s>>>(
+          static_cast<const float *>(dy), static_cast<const float *>(z), static_cast<float *>(to),
+          n, e);
+    st = launch_status();
+    if (st != FEQL_OK) return st;
+    dz = to;
+  }
+  if (!G.p4m && G.T == kT && dx != nullptr && dW != nullptr && N > 0)
+    return feql_backward(x, dz, What, dx, dW, db, ws, w.dw, N, C, D, dtype, stream);
+  if (dx != nullptr) {
+    st = G.p4m ? feql_p4m_backward_dx(dz, What, dx, N, C, D, dtype, stream)
+               : feql_ct_backward_dx(G.T, dz, What, dx, N, C, D, dtype, stream);
+    if (st != FEQL_OK) return st;
+  }
+  if (dW == nullptr) return FEQL_OK;
+  return G.p4m ? feql_p4m_backward_dw(x, dz, dW, db, ws, w.dw, N, C, D, dtype, stream)
+               : feql_ct_backward_dw(G.T, x, dz, dW, db, ws, w.dw, N, C, D, dtype, stream);
+}
+
+int feql_forward_act(const void *x, const void *What, const void *b, const void *res, void *y,
+                     void *z, int64_t N, int C, int D, int act, int dtype, feql_stream stream) {
+  return forward_act({false, kT}, x, What, b, res, y, z, N, C, D, act, dtype, stream);
+}
+
+size_t feql_backward_act_workspace_bytes(int64_t N, int C, int D, int act, int dtype) {
+  return backward_act_workspace_bytes({false, kT}, N, C, D, act, dtype);
+}
+
+int feql_backward_act(const void *x, const void *dy, const void *z, const void *What, void *dx,
+                      void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C, int D,
+                      int act, int dtype, feql_stream stream) {
+  return backward_act({false, kT}, x, dy, z, What, dx, dW, db, ws, ws_bytes, N, C, D, act, dtype,
+                      stream);
+}
+
+int feql_ct_forward_act(int T, const void *x, const void *What, const void *b, const void *res,
+                        void *y, void *z, int64_t N, int C, int D, int act, int dtype,
+                        feql_stream stream) {
+  return forward_act({false, T}, x, What, b, res, y, z, N, C, D, act, dtype, stream);
+}
+
+size_t feql_ct_backward_act_workspace_bytes(int T, int64_t N, int C, int D, int act, int dtype) {
+  return backward_act_workspace_bytes({false, T}, N, C, D, act, dtype);
+}
+
+int feql_ct_backward_act(int T, const void *x, const void *dy, const void *z, const void *What,
+                         void *dx, void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C,
+                         int D, int act, int dtype, feql_stream stream) {
+  return backward_act({false, T}, x, dy, z, What, dx, dW, db, ws, ws_bytes, N, C, D, act, dtype,
+                      stream);
+}
+
+int feql_p4m_forward_act(const void *x, const void *What, const void *b, const void *res, void *y,
+                         void *z, int64_t N, int C, int D, int act, int dtype,
+                         feql_stream stream) {
+  return forward_act({true, 8}, x, What, b, res, y, z, N, C, D, act, dtype, stream);
+}
+
+size_t feql_p4m_backward_act_workspace_bytes(int64_t N, int C, int D, int act, int dtype) {
+  return backward_act_workspace_bytes({true, 8}, N, C, D, act, dtype);
+}
+
+int feql_p4m_backward_act(const void *x, const void *dy, const void *z, const void *What, void *dx,
+                          void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C, int D,
+                          int act, int dtype, feql_stream stream) {
+  return backward_act({true, 8}, x, dy, z, What, dx, dW, db, ws, ws_bytes, N, C, D, act, dtype,
+                      stream);
 }
 
 size_t feql_mlp_weight_fft_bytes(int C, int H, int Co, int dtype) {

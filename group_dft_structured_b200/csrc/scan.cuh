@@ -180,7 +180,8 @@ __device__ __forceinline__ void scan_join(ScanJoin<V, NW, GV> &sm, int parity, i
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       in[j] = fmaf(ea[GV == 1 ? 0 : j], carry[j], eb[j]);
-      const float ta = V > 1 ? __shfl_sync(0xffffffffu, ia[GV == 1 ? 0 : j], src) : ia[GV == 1 ? 0 : j];
+      const float a = ia[GV == 1 ? 0 : j];
+      const float ta = V > 1 ? __shfl_sync(0xffffffffu, a, src) : a;
       const float tb = V > 1 ? __shfl_sync(0xffffffffu, ib[j], src) : ib[j];
       carry[j] = fmaf(ta, carry[j], tb);
     }
@@ -371,7 +372,8 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
   if (live && dhN != nullptr) load_state<V>(dhN + static_cast<int64_t>(b) * p.F + f, carry);
   const int64_t step = static_cast<int64_t>(p.K) * RT;
   int parity = 0;
-  for (int64_t base = len > 0 ? (len - 1) / step * step : -1; base >= 0; base -= step, parity ^= 1) {
+  for (int64_t base = len > 0 ? (len - 1) / step * step : -1; base >= 0;
+       base -= step, parity ^= 1) {
     const int64_t t0 = base + rank * RT;  // the block's first row (a multiple of Q = RT)
     const int64_t l0 = t0 + ty * R;
     Pack<Ty, V> ru[R], rd[R];
@@ -438,7 +440,8 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int q = GV == 1 ? 0 : j;
-        const float before = r == 0 ? in[j] : fmaf(P[r == 0 ? 0 : r - 1][q], in[j], hl[r == 0 ? 0 : r - 1][j]);
+        const int b4 = r == 0 ? 0 : r - 1;
+        const float before = r == 0 ? in[j] : fmaf(P[b4][q], in[j], hl[b4][j]);
         const float delta = d[j] + cin[j];
         o[j] = na[r][q] * delta;
         cin[j] = a[r][q] * delta;
@@ -463,7 +466,8 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
     }
   }
   scan_zero_rest<Ty, V, TY>(p, b, rank, ty, s, e, du, p.F, f, live);
-  scan_zero_rest<Ty, GV, TY>(p, b, rank, ty, s, e, dg, p.FG, gf, live && (!kShared || tx % p.m == 0));
+  scan_zero_rest<Ty, GV, TY>(p, b, rank, ty, s, e, dg, p.FG, gf,
+                             live && (!kShared || tx % p.m == 0));
   if (dh0 != nullptr && live && rank == 0 && ty == 0)
     store_state<V>(dh0 + static_cast<int64_t>(b) * p.F + f, carry);
 }

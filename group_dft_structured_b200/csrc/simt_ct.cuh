@@ -21,6 +21,7 @@
 
 #include <cuda_fp16.h>
 
+#include "act.cuh"
 #include "plan.cuh"
 
 namespace feql {
@@ -138,11 +139,13 @@ __global__ void ct_simt_wfft_kernel(const Ty *__restrict__ W, float *__restrict_
   }
 }
 
-// Forward / dX: out[n][o][:] = irDFT( per bin sum_i Wp_k[o][i] * rDFT(in[n][i][:]) ) (+ bias).
-template <int T, typename Ty>
+// Forward / dX: out[n][o][:] = irDFT( per bin sum_i Wp_k[o][i] * rDFT(in[n][i][:]) ) (+ bias);
+// kEp: then res + act of it (act.cuh).
+template <int T, typename Ty, bool kEp = false>
 __global__ void __launch_bounds__(kCtThreads)
 ct_simt_fwd_kernel(const Ty *__restrict__ in, const float *__restrict__ Wp,
-                   const Ty *__restrict__ bias, Ty *__restrict__ out, int64_t N, int Ci, int Do) {
+                   const Ty *__restrict__ bias, Ty *__restrict__ out, int64_t N, int Ci, int Do,
+                   const Epilogue ep = {}) {
   using B = CtBins<T>;
   __shared__ float cs[B::kBins][T], sn[B::kBins][T];
   __shared__ float Xs[T][kCtK][kCtTile + 1];
@@ -225,7 +228,18 @@ ct_simt_fwd_kernel(const Ty *__restrict__ in, const float *__restrict__ Wp,
       const float bv = bias != nullptr ? ct_load<Ty>(bias + o) : 0.f;
       Ty *dst = out + (n * Do + o) * T;
 #pragma unroll
-      for (int t = 0; t < T; ++t) dst[t] = ct_cast<Ty>(y[t] + bv);
+      for (int t = 0; t < T; ++t) {
+        float v = y[t] + bv;
+        if constexpr (kEp) {
+          // not contracted with the inverse's last product: the same y whether z is saved or not
+          v = __fadd_rn(y[t], bv);
+          const int64_t at = (n * Do + o) * T + t;
+          if (ep.z != nullptr) static_cast<Ty *>(ep.z)[at] = ct_cast<Ty>(act_saved(ep, v));
+          v = act_apply<sizeof(Ty) == 2>(ep, v);
+          if (ep.res != nullptr) v += ct_load<Ty>(static_cast<const Ty *>(ep.res) + at);
+        }
+        dst[t] = ct_cast<Ty>(v);
+      }
     }
 }
 

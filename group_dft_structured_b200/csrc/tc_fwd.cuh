@@ -37,6 +37,7 @@
 
 #include <cuda_fp16.h>
 
+#include "act.cuh"
 #include "plan.cuh"
 #include "rdft4.cuh"
 #include "sm100.cuh"
@@ -87,6 +88,7 @@ struct TcFwdParams {
                         // + weight chunk unless resident, 1 KB aligned
   int bias_floats;      // nD * BD
   void *out;            // [N][Do][4], fp16 (fp32 in split-TF32 mode)
+  Epilogue ep;          // activation, residual, saved z (kernels with kEp)
 };
 
 struct TcSmem {
@@ -151,7 +153,11 @@ struct TcUnits {
 // A_hi B_hi + A_hi B_lo + A_lo B_hi (the lo x lo term, ~2^-22 of the product,
 // is dropped: Ootomo and Yokota's split-TF32 scheme), and the epilogue stores
 // fp32 rows.  Bins are not scaled (fp32 has the range).
-template <bool kTF32>
+//
+// kEp: y = res + act(z) in the epilogue (act.cuh), the pre-activation z stored
+// beside y when the backward pass will want it.  A thread's residual values are
+// loaded before it waits for its accumulators, so the two latencies overlap.
+template <bool kTF32, bool kEp = false>
 __global__ void __maxnreg__(96)
 tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -412,6 +418,22 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
         for (int h = 0; h < 2; ++h) {
           const int c = g * 16 + h * 8;
           uint32_t y0[2][4], y2[2][4], yr[2][4], yi[2][4];
+          uint4 rv[2][2] = {};  // residual of the thread's channel pair (fp16), rows as below
+          if constexpr (kEp && !kTF32) {
+            const int d = j * p.BD + c + tcp;
+            if (p.ep.res != nullptr && d + 2 <= p.Do) {
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int rr = 0; rr < 2; ++rr) {
+                  const int64_t row = row0 + 16 * hf + 8 * rr;
+                  if (row < p.N)
+                    rv[hf][rr] = *reinterpret_cast<const uint4 *>(
+                        static_cast<const __half *>(p.ep.res) + row * row_elems +
+                        static_cast<int64_t>(d) * kT);
+                }
+            }
+          }
           __syncwarp();  // the TMEM loads are warp-collective
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -443,11 +465,23 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
                   const float Yr = __uint_as_float(yr[hf][i]), Yi = __uint_as_float(yi[hf][i]);
                   const float bv = d + cc < p.Do ? sbias[d + cc] : 0.f;
                   const float e = fmaf(0.25f, Y0 + Y2, bv), o = fmaf(0.25f, Y0 - Y2, bv);
-                  if (row < p.N && d + cc < p.Do)
-                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * row_elems +
-                                                static_cast<int64_t>(d + cc) * kT) =
-                        make_float4(fmaf(0.5f, Yr, e), fmaf(-0.5f, Yi, o), fmaf(-0.5f, Yr, e),
-                                    fmaf(0.5f, Yi, o));
+                  if (row < p.N && d + cc < p.Do) {
+                    const int64_t at = row * row_elems + static_cast<int64_t>(d + cc) * kT;
+                    float4 q = make_float4(fmaf(0.5f, Yr, e), fmaf(-0.5f, Yi, o),
+                                           fmaf(-0.5f, Yr, e), fmaf(0.5f, Yi, o));
+                    if constexpr (kEp) {
+                      if (p.ep.z != nullptr)
+                        *reinterpret_cast<float4 *>(static_cast<float *>(p.ep.z) + at) = q;
+                      q = make_float4(act_apply<false>(p.ep, q.x), act_apply<false>(p.ep, q.y),
+                                      act_apply<false>(p.ep, q.z), act_apply<false>(p.ep, q.w));
+                      if (p.ep.res != nullptr) {
+                        const float4 r = *reinterpret_cast<const float4 *>(
+                            static_cast<const float *>(p.ep.res) + at);
+                        q = make_float4(q.x + r.x, q.y + r.y, q.z + r.z, q.w + r.w);
+                      }
+                    }
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = q;
+                  }
                 }
               }
             }
@@ -459,7 +493,8 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
           for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {  // rows r0 and r0 + 8
-              uint32_t w[4];
+              uint32_t w[4], wz[4];
+              const uint32_t rw[4] = {rv[hf][rr].x, rv[hf][rr].y, rv[hf][rr].z, rv[hf][rr].w};
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
                 const int i = 2 * rr + cc;
@@ -468,10 +503,23 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
                 const float bv = cc ? b1 : b0;
                 // planes and weights are both stored divided by 4 (Y = 16 * acc)
                 const float e = fmaf(4.f, Y0 + Y2, bv), o = fmaf(4.f, Y0 - Y2, bv);
-                w[2 * cc] = pack_half2(fmaf(8.f, Yr, e), fmaf(-8.f, Yi, o));
-                w[2 * cc + 1] = pack_half2(fmaf(-8.f, Yr, e), fmaf(8.f, Yi, o));
+                float v[4] = {fmaf(8.f, Yr, e), fmaf(-8.f, Yi, o), fmaf(-8.f, Yr, e),
+                              fmaf(8.f, Yi, o)};
+                if constexpr (kEp) {
+#pragma unroll
+                  for (int q = 0; q < 2; ++q)
+                    act_pair(p.ep, v[2 * q], v[2 * q + 1], rw[2 * cc + q], wz[2 * cc + q]);
+                }
+                w[2 * cc] = pack_half2(v[0], v[1]);
+                w[2 * cc + 1] = pack_half2(v[2], v[3]);
               }
               const int64_t row = row0 + 16 * hf + 8 * rr;
+              if constexpr (kEp) {
+                if (p.ep.z != nullptr && row < p.N)
+                  *reinterpret_cast<uint4 *>(static_cast<__half *>(p.ep.z) + row * row_elems +
+                                             static_cast<int64_t>(d) * kT) =
+                      make_uint4(wz[0], wz[1], wz[2], wz[3]);
+              }
               if (row < p.N)
                 *reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + row * row_elems +
                                            static_cast<int64_t>(d) * kT) =

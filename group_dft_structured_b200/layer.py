@@ -7,16 +7,18 @@ from __future__ import annotations
 
 import torch
 
-from . import (FEQL_FP16, FEQL_FP16_SIMT, FEQL_FP32, feql_backward, feql_backward_dw,
-               feql_backward_dw_workspace_bytes, feql_backward_dx, feql_ct_backward_dw,
+from . import (FEQL_ACT_NONE, FEQL_FP16, FEQL_FP16_SIMT, FEQL_FP32, feql_backward,
+               feql_backward_dw, feql_backward_dw_workspace_bytes, feql_backward_dx,
+               feql_ct_backward_act, feql_ct_backward_act_workspace_bytes, feql_ct_backward_dw,
                feql_ct_backward_dw_workspace_bytes, feql_ct_backward_dx, feql_ct_forward,
-               feql_ct_weight_fft, feql_ct_weight_fft_bytes, feql_forward, feql_mlp_forward,
-               feql_mlp_weight_fft, feql_mlp_weight_fft_bytes, feql_norm_backward,
-               feql_norm_backward_workspace_bytes, feql_norm_forward, feql_p4m_backward_dw,
+               feql_ct_forward_act, feql_ct_weight_fft, feql_ct_weight_fft_bytes, feql_forward,
+               feql_mlp_forward, feql_mlp_weight_fft, feql_mlp_weight_fft_bytes,
+               feql_norm_backward, feql_norm_backward_workspace_bytes, feql_norm_forward,
+               feql_p4m_backward_act, feql_p4m_backward_act_workspace_bytes, feql_p4m_backward_dw,
                feql_p4m_backward_dw_workspace_bytes, feql_p4m_backward_dx, feql_p4m_forward,
-               feql_p4m_weight_fft, feql_p4m_weight_fft_bytes, feql_scan_backward,
-               feql_scan_forward, feql_scan_save_bytes, feql_scan_step, feql_weight_fft,
-               feql_weight_fft_bytes)
+               feql_p4m_forward_act, feql_p4m_weight_fft, feql_p4m_weight_fft_bytes,
+               feql_scan_backward, feql_scan_forward, feql_scan_save_bytes, feql_scan_step,
+               feql_weight_fft, feql_weight_fft_bytes)
 
 
 def torch_dtype(mode: int):
@@ -215,6 +217,102 @@ def _take(t, name: str, shape, dtype, device):
     if not t.is_contiguous():
         t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+# The layer with activation and residual in its epilogue.  ``act`` is one of
+# FEQL_ACT_*; the group order T is the length of x's last axis (p4m: 8).
+
+def _layer_calls(p4m: bool):
+    """The entry points of a group, each taking T first."""
+    if p4m:
+        return ((lambda T, *a: feql_p4m_weight_fft_bytes(*a)),
+                (lambda T, *a: feql_p4m_forward_act(*a)),
+                (lambda T, *a: feql_p4m_backward_act_workspace_bytes(*a)),
+                (lambda T, *a: feql_p4m_backward_act(*a)))
+    return (feql_ct_weight_fft_bytes, feql_ct_forward_act, feql_ct_backward_act_workspace_bytes,
+            feql_ct_backward_act)
+
+
+_CYCLIC_CALLS, _P4M_CALLS = _layer_calls(False), _layer_calls(True)
+
+
+def _layer_input(x: torch.Tensor, mode: int, p4m: bool):
+    if x.dim() != 3 or (p4m and x.shape[2] != 8):
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected "
+                         f"{'(N, C, 8)' if p4m else '(N, C, T)'}")
+    if x.dtype != torch_dtype(mode):
+        raise TypeError(f"x is {x.dtype}, the mode's data is {torch_dtype(mode)}")
+    return x.shape
+
+
+def _forward_act(calls, p4m, x, What, b, D, mode, act, res, save_z):
+    N, C, T = _layer_input(x, mode, p4m)
+    nbytes, forward = calls[0](T, C, D, mode), calls[1]
+    if nbytes == 0:
+        raise ValueError("unsupported (T, C, D, mode)")
+    with _on(x):
+        x = _take(x, "x", x.shape, x.dtype, x.device)
+        What = _take(What, "What", (nbytes,), torch.uint8, x.device)
+        b = _take(b, "b", (D,), x.dtype, x.device)
+        res = _take(res, "res", (N, D, T), x.dtype, x.device)
+        y = torch.empty((N, D, T), dtype=x.dtype, device=x.device)
+        z = torch.empty_like(y) if save_z and act != FEQL_ACT_NONE else None
+        forward(T, x, What, b, res, y, z, N, C, D, act, mode)
+    return y, z
+
+
+def _backward_act(calls, p4m, x, dy, z, What, mode, act, with_dx, with_dw, with_db):
+    N, C, T = _layer_input(x, mode, p4m)
+    if dy.dim() != 3:
+        raise ValueError(f"dy has shape {tuple(dy.shape)}, expected (N, D, T)")
+    D = dy.shape[1]
+    nbytes, workspace, backward = calls[0](T, C, D, mode), calls[2], calls[3]
+    if nbytes == 0:
+        raise ValueError("unsupported (T, C, D, mode)")
+    dx = dW = db = None
+    with _on(x):
+        dev = x.device
+        x = _take(x, "x", x.shape, x.dtype, dev)
+        dy = _take(dy, "dy", (N, D, T), x.dtype, dev)
+        z = _take(z, "z", (N, D, T), x.dtype, dev)
+        What = _take(What, "What", (nbytes,), torch.uint8, dev)
+        ws = torch.empty(workspace(T, N, C, D, act, mode), dtype=torch.uint8, device=dev)
+        if with_dx:
+            dx = torch.empty_like(x)
+        if with_dw or with_db:
+            dW = torch.empty((D, C, T), dtype=x.dtype, device=dev)
+        if with_db:
+            db = torch.empty((D,), dtype=x.dtype, device=dev)
+        if with_dx or dW is not None:
+            backward(T, x, dy, z, What, dx, dW, db, ws, ws.numel(), N, C, D, act, mode)
+    return dx, (dW if with_dw else None), db
+
+
+def ct_forward_act(x: torch.Tensor, What: torch.Tensor, b, D: int, mode: int, act: int, res=None,
+                   save_z: bool = False):
+    """y = res + act(z), z = the C_T layer of x plus b: (y, z).
+
+    ``z`` is what ct_backward_act takes; None without ``save_z`` or activation.
+    """
+    return _forward_act(_CYCLIC_CALLS, False, x, What, b, D, mode, act, res, save_z)
+
+
+def ct_backward_act(x: torch.Tensor, dy: torch.Tensor, z, What: torch.Tensor, mode: int, act: int,
+                    with_dx: bool = True, with_dw: bool = True, with_db: bool = True):
+    """dx, dW, db of ct_forward_act (the residual's gradient is dy), None where not asked."""
+    return _backward_act(_CYCLIC_CALLS, False, x, dy, z, What, mode, act, with_dx, with_dw, with_db)
+
+
+def p4m_forward_act(x: torch.Tensor, What: torch.Tensor, b, D: int, mode: int, act: int, res=None,
+                    save_z: bool = False):
+    """ct_forward_act of the p4m layer."""
+    return _forward_act(_P4M_CALLS, True, x, What, b, D, mode, act, res, save_z)
+
+
+def p4m_backward_act(x: torch.Tensor, dy: torch.Tensor, z, What: torch.Tensor, mode: int, act: int,
+                     with_dx: bool = True, with_dw: bool = True, with_db: bool = True):
+    """ct_backward_act of the p4m layer."""
+    return _backward_act(_P4M_CALLS, True, x, dy, z, What, mode, act, with_dx, with_dw, with_db)
 
 
 def norm_forward(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5,

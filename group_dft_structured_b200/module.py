@@ -15,6 +15,11 @@ unrolling is A[d*8 + g, c*8 + h] = W[d, c, h^-1 g].  ``EqLinear.from_unrolled``
 takes such a dense layer apart into (W, b); ``EqLinear.forward`` runs the
 library's kernels.
 
+Beside it stand the other parts of an equivariant network's block, each with
+autograd: ``EqLinear``'s activation and residual (in the epilogue of its
+products), ``EqNorm`` (layer norm), ``EqScan`` (gated linear recurrence over the
+tokens), and ``EqScanBlock``, a residual block made of them.
+
 Argument marshalling only: every step of the forward and backward passes runs
 in libfeql.so through the C ABI (``layer`` allocates outputs with torch).
 Tensors must live on a CUDA device; there is no CPU path.
@@ -25,8 +30,9 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import FEQL_FP16, FEQL_FP32
+from . import ACTIVATIONS, FEQL_FP16, FEQL_FP32
 from . import layer as _L
 
 
@@ -92,6 +98,33 @@ class EqLinearFunction(torch.autograd.Function):
         return dx, (dW if need_W else None), (db if need_b else None), None, None, None
 
 
+class EqLinearActFunction(torch.autograd.Function):
+    """y = res + act(z), z = EqLinear(x) + b on (N, C, T) tensors; the arguments of
+    EqLinearFunction, ``res`` (or None) and one of FEQL_ACT_*.  Backward: dz =
+    dy act'(z) from the saved z, then dx, dW, db as asked for; dres = dy."""
+
+    @staticmethod
+    def forward(ctx, x, W, b, res, What, mode: int, group: str, act: int):
+        run = _L.p4m_forward_act if group == "p4m" else _L.ct_forward_act
+        y, z = run(x, What, b, W.shape[0], mode, act, res=res,
+                   save_z=any(ctx.needs_input_grad[:3]))
+        ctx.save_for_backward(x, What, z)
+        ctx.mode, ctx.group, ctx.act = mode, group, act
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, What, z = ctx.saved_tensors
+        need_x, need_W, need_b, need_res = ctx.needs_input_grad[:4]
+        dx = dW = db = None
+        if need_x or need_W or need_b:
+            run = _L.p4m_backward_act if ctx.group == "p4m" else _L.ct_backward_act
+            dx, dW, db = run(x, dy, z, What, ctx.mode, ctx.act, with_dx=need_x, with_dw=need_W,
+                             with_db=need_b)
+        return dx, dW, db, (dy if need_res else None), None, None, None, None
+
+
 class EqLinear(torch.nn.Module):
     """Equivariant linear layer of C_T (or p4m) on features (..., C*T), group index innermost.
 
@@ -101,13 +134,18 @@ class EqLinear(torch.nn.Module):
     group D4 (T = 8: rotations (r, 0) at 0..3, reflected (r, 1) at 4..7).  The
     Fourier weight buffer is rebuilt when the weight changes (tracked by its
     storage and version counter), so it is computed once per optimizer step, or
-    once for inference.
+    once for inference.  ``activation`` ("relu", "gelu": the tanh form, "silu") is
+    applied to the output and ``forward``'s ``residual`` added after it, both in
+    the epilogue of the layer's products.
     """
 
     def __init__(self, in_channels: int, out_channels: int, group_order: int = 4,
                  bias: bool = True, dtype: torch.dtype = torch.float16, device=None,
-                 group: str = "cyclic"):
+                 group: str = "cyclic", activation: str = "none"):
         super().__init__()
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation is one of {', '.join(ACTIVATIONS)}, not {activation!r}")
+        self.activation = activation
         if group not in ("cyclic", "p4m"):
             raise ValueError(f"group is 'cyclic' or 'p4m', not {group!r}")
         if group == "p4m" and group_order != 8:
@@ -143,7 +181,7 @@ class EqLinear(torch.nn.Module):
             self._what_key = key
         return self._what
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         C, D, T = self.in_channels, self.out_channels, self.group_order
         if x.shape[-1] != C * T:
             raise ValueError(f"expected features of size C*T = {C * T}, got {x.shape[-1]}")
@@ -153,14 +191,27 @@ class EqLinear(torch.nn.Module):
         x3 = x.reshape(-1, C, T).contiguous()
         if x3.dtype != self.weight.dtype:
             raise TypeError(f"input dtype {x3.dtype} differs from the weight's {self.weight.dtype}")
-        y = EqLinearFunction.apply(x3, self.weight, self.bias, self.fourier_weight(),
-                                   mode_for(self.weight.dtype), self.group)
+        if residual is None and self.activation == "none":
+            y = EqLinearFunction.apply(x3, self.weight, self.bias, self.fourier_weight(),
+                                       mode_for(self.weight.dtype), self.group)
+            return y.reshape(*lead, D * T)
+        if residual is not None:
+            if residual.shape != (*lead, D * T):
+                raise ValueError(f"expected a residual of shape {(*lead, D * T)}, got "
+                                 f"{tuple(residual.shape)}")
+            residual = residual.reshape(-1, D, T)
+        with torch.cuda.device(x.device):
+            What = self.fourier_weight()
+        y = EqLinearActFunction.apply(x3, self.weight, self.bias, residual, What,
+                                      mode_for(self.weight.dtype), self.group,
+                                      ACTIVATIONS[self.activation])
         return y.reshape(*lead, D * T)
 
     def extra_repr(self) -> str:
         return (f"in_channels={self.in_channels}, out_channels={self.out_channels}, "
                 f"group_order={self.group_order}, group={self.group}, "
-                f"bias={self.bias is not None}")
+                f"bias={self.bias is not None}"
+                + (f", activation={self.activation}" if self.activation != "none" else ""))
 
     @classmethod
     def from_unrolled(cls, weight: torch.Tensor, bias: torch.Tensor | None, group_order: int,
@@ -203,3 +254,162 @@ class EqLinear(torch.nn.Module):
             if b is not None:
                 m.bias.copy_(b)
         return m
+
+
+class EqNormFunction(torch.autograd.Function):
+    """Layer norm of (N, C, T) features over C*T, affine per channel."""
+
+    @staticmethod
+    def forward(ctx, x, gamma, beta, eps: float):
+        y, stats = _L.norm_forward(x, gamma, beta, eps, save_stats=any(ctx.needs_input_grad))
+        ctx.save_for_backward(x, stats, gamma)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, stats, gamma = ctx.saved_tensors
+        need_x, need_g, need_b = ctx.needs_input_grad[:3]
+        dx, dgamma, dbeta = _L.norm_backward(dy, x, stats, gamma, with_params=need_g or need_b)
+        return (dx if need_x else None, dgamma if need_g else None, dbeta if need_b else None,
+                None)
+
+
+class EqNorm(torch.nn.Module):
+    """Layer norm of features (..., C*T), group index innermost: each token is
+    normalised over all its C*T features, then scaled and shifted per channel
+    (parameters ``weight`` [C] and ``bias`` [C], or neither without ``affine``).
+    Statistics and parameters are shared over the group axis, so the module
+    commutes with the group's action."""
+
+    def __init__(self, channels: int, group_order: int = 4, eps: float = 1e-5,
+                 affine: bool = True, dtype: torch.dtype = torch.float16, device=None):
+        super().__init__()
+        mode_for(dtype)
+        self.channels, self.group_order, self.eps = channels, group_order, eps
+        self.weight = self.bias = None
+        if affine:
+            self.weight = torch.nn.Parameter(torch.ones((channels,), dtype=dtype, device=device))
+            self.bias = torch.nn.Parameter(torch.zeros((channels,), dtype=dtype, device=device))
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        C, T = self.channels, self.group_order
+        if x.shape[-1] != C * T:
+            raise ValueError(f"expected features of size C*T = {C * T}, got {x.shape[-1]}")
+        y = EqNormFunction.apply(x.reshape(-1, C, T), self.weight, self.bias, self.eps)
+        return y.reshape(x.shape)
+
+    def extra_repr(self) -> str:
+        return (f"channels={self.channels}, group_order={self.group_order}, eps={self.eps}, "
+                f"affine={self.weight is not None}")
+
+
+class EqScanFunction(torch.autograd.Function):
+    """layer.scan_forward with autograd: (h, hN) of (u, g, h0, offsets)."""
+
+    @staticmethod
+    def forward(ctx, u, g, h0, offsets):
+        h, hN, saved = _L.scan_forward(u, g, h0, offsets, save=any(ctx.needs_input_grad[:3]))
+        ctx.save_for_backward(u, g, saved, offsets)
+        ctx.set_materialize_grads(False)
+        return h, hN
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh, dhN):
+        u, g, saved, offsets = ctx.saved_tensors
+        if dh is None:
+            dh = torch.zeros_like(u)
+        du, dg, dh0 = _L.scan_backward(dh, u, g, saved, dhN, offsets)
+        need = ctx.needs_input_grad
+        return (du if need[0] else None, dg if need[1] else None, dh0 if need[2] else None, None)
+
+
+class EqScan(torch.nn.Module):
+    """Gated linear recurrence over the tokens, h = a h + (1 - a) u with
+    a = sigmoid(gate), per feature of (..., C*T).
+
+    ``forward(u, gate, state, offsets)``: u (B, L, C*T), or (N, C*T) rows of
+    packed sequences with ``offsets`` (B + 1,) int32; gate of u's shape, or with
+    C features (one gate per channel, shared over the group axis); state
+    (B, C*T) fp32 or None (zero).  Returns h and the state after the last
+    tokens.  ``step`` takes one token of each sequence, u (B, C*T), and updates
+    the state in place (no autograd).
+    """
+
+    def __init__(self, channels: int, group_order: int = 4):
+        super().__init__()
+        self.channels, self.group_order = channels, group_order
+
+    def _split(self, u, gate):
+        C, T = self.channels, self.group_order
+        if u.shape[-1] != C * T:
+            raise ValueError(f"expected features of size C*T = {C * T}, got {u.shape[-1]}")
+        if gate.shape[:-1] != u.shape[:-1] or gate.shape[-1] not in (C, C * T):
+            raise ValueError(f"expected gates of shape {(*u.shape[:-1], C * T)} or "
+                             f"{(*u.shape[:-1], C)}, got {tuple(gate.shape)}")
+        lead = u.shape[:-1]
+        shared = gate.shape[-1] == C and T > 1
+        return u.reshape(*lead, C, T), gate if shared else gate.reshape(*lead, C, T)
+
+    def forward(self, u: torch.Tensor, gate: torch.Tensor, state: torch.Tensor | None = None,
+                offsets: torch.Tensor | None = None):
+        C, T = self.channels, self.group_order
+        uv, gv = self._split(u, gate)
+        h0 = None if state is None else state.reshape(-1, C, T)
+        h, hN = EqScanFunction.apply(uv, gv, h0, offsets)
+        return h.reshape(u.shape), hN.reshape(-1, C * T)
+
+    @torch.no_grad()
+    def step(self, u: torch.Tensor, gate: torch.Tensor, state: torch.Tensor) -> torch.Tensor:
+        C, T = self.channels, self.group_order
+        uv, gv = self._split(u, gate)
+        return _L.scan_step(uv, gv, state.view(-1, C, T)).reshape(u.shape)
+
+    def extra_repr(self) -> str:
+        return f"channels={self.channels}, group_order={self.group_order}"
+
+
+class EqScanBlock(torch.nn.Module):
+    """Residual block of an equivariant network whose tokens mix by a gated
+    recurrence (the place of the attention or state-space mixer):
+
+        n = norm1(x);  x = x + out(scan(value(n), gate(n)))
+        x = x + fc2(gelu(fc1(norm2(x))))
+
+    on features (B, L, C*T), or (N, C*T) rows of packed sequences with
+    ``offsets``.  Every part commutes with the group's action on the group axis.
+    ``step`` is the block on one token of each sequence, for generation: it takes
+    and updates the (B, C*T) fp32 state that ``forward`` returns.
+    """
+
+    def __init__(self, channels: int, hidden: int, group_order: int = 4,
+                 dtype: torch.dtype = torch.float16, device=None, group: str = "cyclic"):
+        super().__init__()
+        kw = {"dtype": dtype, "device": device}
+        lin = {**kw, "group_order": group_order, "group": group}
+        self.norm1 = EqNorm(channels, group_order, **kw)
+        self.value = EqLinear(channels, channels, **lin)
+        self.gate = EqLinear(channels, channels, **lin)
+        self.scan = EqScan(channels, group_order)
+        self.out = EqLinear(channels, channels, **lin)
+        self.norm2 = EqNorm(channels, group_order, **kw)
+        self.fc1 = EqLinear(channels, hidden, activation="gelu", **lin)
+        self.fc2 = EqLinear(hidden, channels, **lin)
+        with torch.no_grad():
+            self.gate.bias.fill_(2.0)  # memories of some eight tokens to begin with
+
+    def _mlp(self, x):
+        return self.fc2(self.fc1(self.norm2(x)), residual=x)
+
+    def forward(self, x: torch.Tensor, state: torch.Tensor | None = None,
+                offsets: torch.Tensor | None = None):
+        n = self.norm1(x)
+        h, state = self.scan(self.value(n), self.gate(n), state, offsets)
+        return self._mlp(self.out(h, residual=x)), state
+
+    @torch.no_grad()
+    def step(self, x: torch.Tensor, state: torch.Tensor) -> torch.Tensor:
+        n = self.norm1(x)
+        h = self.scan.step(self.value(n), self.gate(n), state)
+        return self._mlp(self.out(h, residual=x))

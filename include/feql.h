@@ -252,6 +252,55 @@ int feql_mlp_forward(const void *x, const void *What, const void *b1, const void
                      int64_t N, int C, int H, int Co, int dtype, feql_stream stream);
 
 /* ---------------------------------------------------------------------------
+ * The layer with bias, activation and residual in the epilogue of its products,
+ * for training and inference:
+ *   z = EqLinear(x) + b,   y = res + act(z)
+ * act is applied to every group value, so the layer stays equivariant.  GELU is
+ * the tanh form (as in the MLP block above), z sigma(2 k0 (z + k1 z^3)) with
+ * k0 = sqrt(2 / pi), k1 = 0.044715; SiLU is z sigma(z).  z is kept in fp32 from
+ * the products to y (one rounding, y's).
+ *   res : device [N][D][T] or NULL (no residual)
+ *   z   : device [N][D][T] (written) for the backward pass, or NULL; a positive z
+ *         that rounds to zero is saved as the least subnormal under ReLU
+ * The other arguments, groups, modes and errors are those of feql_forward,
+ * feql_ct_forward and feql_p4m_forward. */
+typedef enum {
+  FEQL_ACT_NONE = 0,
+  FEQL_ACT_RELU = 1, /* derivative 0 at 0 */
+  FEQL_ACT_GELU = 2,
+  FEQL_ACT_SILU = 3
+} feql_activation;
+
+int feql_forward_act(const void *x, const void *What, const void *b, const void *res, void *y,
+                     void *z, int64_t N, int C, int D, int act, int dtype, feql_stream stream);
+int feql_ct_forward_act(int T, const void *x, const void *What, const void *b, const void *res,
+                        void *y, void *z, int64_t N, int C, int D, int act, int dtype,
+                        feql_stream stream);
+int feql_p4m_forward_act(const void *x, const void *What, const void *b, const void *res, void *y,
+                         void *z, int64_t N, int C, int D, int act, int dtype,
+                         feql_stream stream);
+
+/* Backward: dz = dy act'(z), then dx, dW and db of the layer for dz (the
+ * residual's gradient is dy itself).  dz is rounded to the data type.
+ *   z  : as saved by the forward pass (NULL for FEQL_ACT_NONE)
+ *   dx : device [N][C][T] or NULL          dW : [D][C][T] or NULL
+ *   db : [D] or NULL (NULL without dW); not both dx and dW NULL
+ *   ws : ws_bytes >= feql_*_backward_act_workspace_bytes for these sizes (which
+ *        includes room for dz) */
+size_t feql_backward_act_workspace_bytes(int64_t N, int C, int D, int act, int dtype);
+int feql_backward_act(const void *x, const void *dy, const void *z, const void *What, void *dx,
+                      void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C, int D,
+                      int act, int dtype, feql_stream stream);
+size_t feql_ct_backward_act_workspace_bytes(int T, int64_t N, int C, int D, int act, int dtype);
+int feql_ct_backward_act(int T, const void *x, const void *dy, const void *z, const void *What,
+                         void *dx, void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C,
+                         int D, int act, int dtype, feql_stream stream);
+size_t feql_p4m_backward_act_workspace_bytes(int64_t N, int C, int D, int act, int dtype);
+int feql_p4m_backward_act(const void *x, const void *dy, const void *z, const void *What, void *dx,
+                          void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C, int D,
+                          int act, int dtype, feql_stream stream);
+
+/* ---------------------------------------------------------------------------
  * Operators that stand between the layers of an equivariant network (the
  * EQ-ViT / EQ-Swin / EQ-VMamba blocks of the technical summary, "Livello di
  * Rete", and the arXiv abstract).  Features are (C, T) per token, the group
