@@ -40,7 +40,7 @@ def nvcc() -> str:
 
 
 def sources() -> list[str]:
-    return [os.path.join(CSRC, f) for f in ("feql_api.cu", "feql_ops.cu")]
+    return [os.path.join(CSRC, f) for f in ("feql_api.cu", "feql_ops.cu", "simt_ct.cu")]
 
 
 def deps() -> list[str]:

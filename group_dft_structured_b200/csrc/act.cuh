@@ -9,6 +9,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/feql.h"
@@ -21,6 +22,9 @@ struct Epilogue {
   void *z;          // [N][Do][T] pre-activation for the backward pass, or nullptr
   int act;          // feql_activation
   float ka, kb;     // v = z (ka + kb z^2) of GELU and SiLU
+  float nka, nkb;   // the same times -log2(e): exp(-v) = 2^(z (nka + nkb z^2))
+  float lo;         // max(z, lo): 0 for ReLU, -inf for no activation
+  float least;      // ReLU: the smallest positive z that is saved
 };
 
 inline Epilogue make_epilogue(int act, const void *res, void *z) {
@@ -31,34 +35,64 @@ inline Epilogue make_epilogue(int act, const void *res, void *z) {
   const float k0 = 0.7978845608028654f;  // sqrt(2 / pi)
   e.ka = act == FEQL_ACT_GELU ? 2.f * k0 : 1.f;
   e.kb = act == FEQL_ACT_GELU ? 2.f * k0 * 0.044715f : 0.f;
+  e.nka = -1.4426950408889634f * e.ka;
+  e.nkb = -1.4426950408889634f * e.kb;
+  e.lo = act == FEQL_ACT_RELU ? 0.f : -INFINITY;
+  e.least = act == FEQL_ACT_RELU ? 5.9604645e-8f : 0.f;
   return e;
 }
 
+// Variants of an epilogue: none (the layer alone); max(z, lo), which is ReLU or,
+// with lo = -inf, no activation; the sigmoid family.
+enum EpKind { kEpNone = 0, kEpMax = 1, kEpSigmoid = 2 };
+
+inline int epilogue_kind(const Epilogue &e) {
+  return e.act == FEQL_ACT_GELU || e.act == FEQL_ACT_SILU ? kEpSigmoid : kEpMax;
+}
+
+__device__ __forceinline__ float ex2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
 // sigma(v) and sigma(-v), each to full relative precision.  kFast (fp16
-// outputs): the hardware's exponential and division, about 2^-20, far below the
-// outputs' rounding.
+// outputs): the hardware's exponential and reciprocal, off by 2^-21 or so, far
+// below the outputs' rounding, subnormals flushed.
 template <bool kFast>
 __device__ __forceinline__ void act_sigmoid(float v, float &p, float &q) {
-  const float e = kFast ? __expf(-fabsf(v)) : expf(-fabsf(v));
-  const float big = kFast ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
+  const float e = kFast ? ex2_fast(-kLog2e * fabsf(v)) : expf(-fabsf(v));
+  const float big = kFast ? rcp_fast(1.f + e) : 1.f / (1.f + e);
   const float small = e * big;
   p = v >= 0.f ? big : small;
   q = v >= 0.f ? small : big;
 }
 
-template <bool kFast>
-__device__ __forceinline__ float act_apply(const Epilogue &e, float z) {
-  if (e.act == FEQL_ACT_NONE) return z;
-  if (e.act == FEQL_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-  // exp(-v) overflows to inf for v below -88, where z / inf = -0 stands for a
-  // value under 1e-36
-  const float v = z * fmaf(e.kb * z, z, e.ka);
-  return kFast ? __fdividef(z, 1.f + __expf(-v)) : z / (1.f + expf(-v));
+// res + act(z).  In the sigmoid family exp(-v) overflows to inf for v below -88,
+// where z / inf = -0 stands for a value under 1e-36.
+template <int kKind, bool kFast>
+__device__ __forceinline__ float act_apply(const Epilogue &e, float z, float res) {
+  if constexpr (kKind == kEpMax) return max_nan(z, e.lo) + res;
+  if constexpr (kFast)
+    return fmaf(z, rcp_fast(1.f + ex2_fast(z * fmaf(e.nkb * z, z, e.nka))), res);
+  return z / (1.f + expf(-z * fmaf(e.kb * z, z, e.ka))) + res;
 }
 
 template <bool kFast>
 __device__ __forceinline__ float act_slope(const Epilogue &e, float z) {
-  if (e.act == FEQL_ACT_NONE) return 1.f;
   if (e.act == FEQL_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
   const float z2 = z * z;
   float p, q;
@@ -71,19 +105,21 @@ __device__ __forceinline__ float act_slope(const Epilogue &e, float z) {
 
 // The saved z keeps the side of ReLU's corner it was computed on: a positive
 // value below half the least fp16 subnormal is saved as that subnormal, not 0.
+template <int kKind>
 __device__ __forceinline__ float act_saved(const Epilogue &e, float z) {
-  return e.act == FEQL_ACT_RELU && z > 0.f ? fmaxf(z, 5.9604645e-8f) : z;
+  return kKind == kEpMax && z > 0.f ? fmaxf(z, e.least) : z;
 }
 
 // Two values of an fp16 epilogue: their packed z in zw, and z0, z1 become the
 // results; rw: their residual (zeros where there is none).
+template <int kKind>
 __device__ __forceinline__ void act_pair(const Epilogue &e, float &z0, float &z1, uint32_t rw,
                                          uint32_t &zw) {
-  const __half2 h = __floats2half2_rn(act_saved(e, z0), act_saved(e, z1));
+  const __half2 h = __floats2half2_rn(act_saved<kKind>(e, z0), act_saved<kKind>(e, z1));
   zw = *reinterpret_cast<const uint32_t *>(&h);
   const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&rw));
-  z0 = act_apply<true>(e, z0) + r.x;
-  z1 = act_apply<true>(e, z1) + r.y;
+  z0 = act_apply<kKind, true>(e, z0, r.x);
+  z1 = act_apply<kKind, true>(e, z1, r.y);
 }
 
 // dz = dy act'(z) on n values, V per access; HBM-bound (three streams).  The

@@ -15,7 +15,7 @@
 #include "host.cuh"
 #include "plan.cuh"
 #include "simt.cuh"
-#include "simt_ct.cuh"
+#include "simt_ct_host.cuh"
 #include "sm100.cuh"
 #include "tc_bwd.cuh"
 #include "tc_dw.cuh"
@@ -130,14 +130,6 @@ bool is_tc(int dt) { return dt == FEQL_FP16; }
 bool is_tf32(int dt) { return dt == FEQL_FP32_3XTF32; }
 // Layout kind of the Fourier-weight buffer of a (resolved) mode.
 int what_kind(int dt) { return is_tc(dt) ? kWhatF16 : (is_tf32(dt) ? kWhatTF32 : kWhatSimt); }
-int grid_for(int64_t work, int threads, int sms) {
-  int64_t g = cdiv(work, threads);
-  const int64_t cap = static_cast<int64_t>(sms) * 8;
-  if (g > cap) g = cap;
-  if (g < 1) g = 1;
-  return static_cast<int>(g);
-}
-
 // ---------------------------------------------------------------- tc launch
 // tf32: fp32 data in the split-TF32 mode (FEQL_FP32_3XTF32), else fp16.
 // ep: activation, residual and saved z, or nullptr.
@@ -166,6 +158,8 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
   p.acc_stride = p.nacc == 2 ? 256 : 0;
   p.bias_floats = P.nD * P.BD;
   p.out = out;
+  p.ep = ep != nullptr ? *ep : Epilogue{};
+  p.res_ring = !tf32 && p.ep.res != nullptr ? 1 : 0;
   const int slot = tf32 ? 2 * kXChunkBytes : kXChunkBytes;  // input chunk / its planes
   const int budget = dev.smem_optin - 1024;  // 1 KB for aligning the base
   // Resident weights when the CTA's slice fits beside >= 4 input stages and
@@ -196,15 +190,18 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
   st = tf32 ? make_tmap_f32(&tm_in, in, N, static_cast<int64_t>(P.Ci) * kT)
             : make_tmap_f16(&tm_in, in, N, static_cast<int64_t>(P.Ci) * kT);
   if (st != FEQL_OK) return st;
+  CUtensorMap tm_res = tm_in;  // residual boxes: 32 rows x 16 channels
+  if (p.res_ring) st = make_tmap_f16(&tm_res, p.ep.res, N, static_cast<int64_t>(P.Do) * kT, 32);
+  if (st != FEQL_OK) return st;
   auto kernel = tf32 ? tc_fourier_gemm_kernel<true> : tc_fourier_gemm_kernel<false>;
-  p.ep = {};
-  if (ep != nullptr) {
-    p.ep = *ep;
-    kernel = tf32 ? tc_fourier_gemm_kernel<true, true> : tc_fourier_gemm_kernel<false, true>;
-  }
+  if (ep != nullptr && epilogue_kind(*ep) == kEpSigmoid)
+    kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpSigmoid>
+                  : tc_fourier_gemm_kernel<false, kEpSigmoid>;
+  else if (ep != nullptr)
+    kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpMax> : tc_fourier_gemm_kernel<false, kEpMax>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return FEQL_ERR_CUDA;
-  kernel<<<grid, kTcThreads, smem, stream>>>(tm_in, p);
+  kernel<<<grid, kTcThreads, smem, stream>>>(tm_in, tm_res, p);
   return launch_status();
 }
 
@@ -215,7 +212,9 @@ int launch_simt_fwd(const void *in, const float *Wp, const void *bias, void *out
   if (gx > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(Do, kSimtTile)));
   if (grid.y > 65535) return FEQL_ERR_UNSUPPORTED;
-  auto kernel = ep != nullptr ? simt_fwd_kernel<T, true> : simt_fwd_kernel<T>;
+  auto kernel = ep == nullptr ? simt_fwd_kernel<T>
+                : epilogue_kind(*ep) == kEpSigmoid ? simt_fwd_kernel<T, kEpSigmoid>
+                                                   : simt_fwd_kernel<T, kEpMax>;
   kernel<<<grid, kSimtThreads, 0, stream>>>(
       static_cast<const T *>(in), Wp, static_cast<const T *>(bias), static_cast<T *>(out), N, Ci,
       Do, ep != nullptr ? *ep : Epilogue{});
@@ -449,7 +448,9 @@ int launch_g8_fwd(const void *in, const uint8_t *wt, const G8Plan &P, const __ha
   st = make_tmap_f16(&tm_out, out, N, static_cast<int64_t>(P.Do) * T, 32, 8 * T);
   if (st != FEQL_OK) return st;
   const int smem = g8_fwd_smem(p).total + 1024;
-  auto kernel = ep != nullptr ? tc_g8_fwd_kernel<Gp, true> : tc_g8_fwd_kernel<Gp>;
+  auto kernel = ep == nullptr ? tc_g8_fwd_kernel<Gp>
+                : epilogue_kind(*ep) == kEpSigmoid ? tc_g8_fwd_kernel<Gp, kEpSigmoid>
+                                                   : tc_g8_fwd_kernel<Gp, kEpMax>;
   p.ep = ep != nullptr ? *ep : Epilogue{};
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
@@ -619,107 +620,6 @@ int ct_route(int T, int C, int D, int dtype, int *path) {
   if (dt == FEQL_FP16 && T == 6 && C % 4 == 0 && D % 4 == 0) *path = kCtTensor6;
   return FEQL_OK;
 }
-
-// ---------------------------------------------------------- C_T on CUDA cores
-#define FEQL_CT_ORDERS(X) X(2) X(3) X(5) X(6) X(7) X(8) X(9) X(10) X(11) X(12) X(13) X(14) X(15) X(16)
-
-template <int T, typename Ty>
-int ct_simt_wfft_launch(const void *W, void *What, int C, int D, cudaStream_t s, int sms) {
-  ct_simt_wfft_kernel<T, Ty><<<grid_for(static_cast<int64_t>(C) * D, 256, sms), 256, 0, s>>>(
-      static_cast<const Ty *>(W), static_cast<float *>(What), C, D);
-  return launch_status();
-}
-
-template <int T, typename Ty>
-int ct_simt_pass_launch(const void *in, const float *Wp, const void *bias, void *out, int64_t N,
-                        int Ci, int Do, cudaStream_t s, const Epilogue *ep) {
-  const int64_t gx = cdiv(N, kCtTile);
-  if (gx > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
-  dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(Do, kCtTile)));
-  if (grid.y > 65535) return FEQL_ERR_UNSUPPORTED;
-  auto kernel = ep != nullptr ? ct_simt_fwd_kernel<T, Ty, true> : ct_simt_fwd_kernel<T, Ty>;
-  kernel<<<grid, kCtThreads, 0, s>>>(static_cast<const Ty *>(in), Wp,
-                                     static_cast<const Ty *>(bias), static_cast<Ty *>(out), N, Ci,
-                                     Do, ep != nullptr ? *ep : Epilogue{});
-  return launch_status();
-}
-
-struct CtDwPlan {
-  int tiles_d, tiles_c, splits;
-  int64_t split_len;
-};
-
-// Token splits: about two blocks per SM over all (d, c) tiles, at most 64 (the
-// reduce sums them serially per output).
-CtDwPlan make_ct_dw_plan(int64_t N, int C, int D, int sms) {
-  CtDwPlan p;
-  p.tiles_d = static_cast<int>(cdiv(D, kCtTile));
-  p.tiles_c = static_cast<int>(cdiv(C, kCtTile));
-  int64_t s = 2 * static_cast<int64_t>(sms) / (p.tiles_d * p.tiles_c);
-  if (s < 1) s = 1;
-  if (s > 64) s = 64;
-  const int64_t chunks = cdiv(N, kCtK);
-  if (s > chunks) s = chunks;
-  p.split_len = N > 0 ? align_up(cdiv(N, s), kCtK) : kCtK;
-  p.splits = N > 0 ? static_cast<int>(cdiv(N, p.split_len)) : 0;
-  return p;
-}
-
-int64_t ct_dw_ws_floats(const CtDwPlan &p, int T, int C, int D) {
-  return static_cast<int64_t>(p.splits) * (static_cast<int64_t>(T) * D * C + D);
-}
-
-template <int T, typename Ty>
-int ct_simt_dw_launch(const void *x, const void *dy, void *dW, void *db, float *ws, size_t ws_bytes,
-                      int64_t N, int C, int D, cudaStream_t s, int sms) {
-  const CtDwPlan p = make_ct_dw_plan(N, C, D, sms);
-  if (ws_bytes < static_cast<size_t>(ct_dw_ws_floats(p, T, C, D)) * 4) return FEQL_ERR_INVALID_ARG;
-  float *ws_db = ws + static_cast<int64_t>(p.splits) * T * D * C;
-  if (p.splits > 0) {
-    const int64_t grid = static_cast<int64_t>(p.splits) * p.tiles_d * p.tiles_c;
-    if (grid > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
-    ct_simt_dw_kernel<T, Ty><<<static_cast<unsigned>(grid), kCtThreads, 0, s>>>(
-        static_cast<const Ty *>(x), static_cast<const Ty *>(dy), ws, ws_db, N, C, D, p.split_len,
-        p.tiles_d, p.tiles_c);
-  }
-  ct_simt_dw_reduce_kernel<T, Ty><<<grid_for(static_cast<int64_t>(D) * C + D, 256, sms), 256, 0, s>>>(
-      ws, ws_db, static_cast<Ty *>(dW), static_cast<Ty *>(db), p.splits, C, D);
-  return launch_status();
-}
-
-template <typename Ty>
-int ct_simt_wfft(int T, const void *W, void *What, int C, int D, cudaStream_t s, int sms) {
-  switch (T) {
-#define FEQL_CASE(t) case t: return ct_simt_wfft_launch<t, Ty>(W, What, C, D, s, sms);
-    FEQL_CT_ORDERS(FEQL_CASE)
-#undef FEQL_CASE
-    default: return FEQL_ERR_UNSUPPORTED;
-  }
-}
-
-template <typename Ty>
-int ct_simt_pass(int T, const void *in, const float *Wp, const void *bias, void *out, int64_t N,
-                 int Ci, int Do, cudaStream_t s, const Epilogue *ep = nullptr) {
-  switch (T) {
-#define FEQL_CASE(t) case t: return ct_simt_pass_launch<t, Ty>(in, Wp, bias, out, N, Ci, Do, s, ep);
-    FEQL_CT_ORDERS(FEQL_CASE)
-#undef FEQL_CASE
-    default: return FEQL_ERR_UNSUPPORTED;
-  }
-}
-
-template <typename Ty>
-int ct_simt_dw(int T, const void *x, const void *dy, void *dW, void *db, float *ws, size_t ws_bytes,
-               int64_t N, int C, int D, cudaStream_t s, int sms) {
-  switch (T) {
-#define FEQL_CASE(t) \
-  case t: return ct_simt_dw_launch<t, Ty>(x, dy, dW, db, ws, ws_bytes, N, C, D, s, sms);
-    FEQL_CT_ORDERS(FEQL_CASE)
-#undef FEQL_CASE
-    default: return FEQL_ERR_UNSUPPORTED;
-  }
-}
-
 
 // FEQL_FP16 is the one mode of the p4m kernels.
 int p4m_check(int dtype) {

@@ -676,10 +676,10 @@ struct G8Units {
 
 // 18 warps over the 4 SM sub-partitions put 5 warps on two 16K-register slices:
 // 5 x 32 x 96 = 15,360 registers fit, 104 would not.
-// kEp: y = res + act(z) (act.cuh).  A lane holds whole fibres of its token row, so
+// kEp != kEpNone: y = res + act(z) (act.cuh).  A lane holds whole fibres of its token row, so
 // it reads the residual and writes z directly, 16 bytes at a time; y goes through
 // the staging box as always.
-template <class Gp, bool kEp = false>
+template <class Gp, int kEp = kEpNone>
 __global__ void __maxnreg__(96)
 tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
                   const G8FwdParams p) {
@@ -863,7 +863,7 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
           uint32_t rw[2 * T], zw[2 * T];
           const int64_t row = static_cast<int64_t>(m) * kBM + quad * 32 + lane;
           const int64_t at = (row * p.Do + d0 + 4 * h) * T;
-          if constexpr (kEp) {
+          if constexpr (kEp != kEpNone) {
 #pragma unroll
             for (int q = 0; q < T / 2; ++q) {
               uint4 v = {};
@@ -886,12 +886,12 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
 #pragma unroll
             for (int e = 0; e < T / 2; ++e) {
               float z0 = y[2 * e] + bv, z1 = y[2 * e + 1] + bv;
-              if constexpr (kEp)
-                act_pair(p.ep, z0, z1, rw[i * (T / 2) + e], zw[i * (T / 2) + e]);
+              if constexpr (kEp != kEpNone)
+                act_pair<kEp>(p.ep, z0, z1, rw[i * (T / 2) + e], zw[i * (T / 2) + e]);
               hv[i][e] = pack_half2(z0, z1);
             }
           }
-          if constexpr (kEp) {
+          if constexpr (kEp != kEpNone) {
 #pragma unroll
             for (int q = 0; q < T / 2; ++q)
               if (p.ep.z != nullptr && row < p.N && d0 + 4 * h + (T == 8 ? q : 3) < p.Do)

@@ -59,4 +59,13 @@ inline int launch_status() {
   return cudaGetLastError() == cudaSuccess ? FEQL_OK : FEQL_ERR_CUDA;
 }
 
+// Blocks of a grid-stride loop over `work` items.
+inline int grid_for(int64_t work, int threads, int sms) {
+  int64_t g = (work + threads - 1) / threads;
+  const int64_t cap = static_cast<int64_t>(sms) * 8;
+  if (g > cap) g = cap;
+  if (g < 1) g = 1;
+  return static_cast<int>(g);
+}
+
 }  // namespace feql

@@ -68,8 +68,8 @@ __device__ __forceinline__ void irdft4(float Y0, float Y2, float Y1r, float Y1i,
 }
 
 // Forward / dX: out[n][o][:] = irdft( sum_i What_k[o][i] * rdft(in[n][i][:]) ) (+ bias[o]).
-// kEp: then y = res + act(z) (act.cuh).
-template <typename T, bool kEp = false>
+// kEp != kEpNone: then y = res + act(z) (act.cuh).
+template <typename T, int kEp = kEpNone>
 __global__ void __launch_bounds__(kSimtThreads)
 simt_fwd_kernel(const T *__restrict__ in, const float *__restrict__ Wp, const T *__restrict__ bias,
                 T *__restrict__ out, int64_t N, int Ci, int Do, const Epilogue ep = {}) {
@@ -148,14 +148,14 @@ simt_fwd_kernel(const T *__restrict__ in, const float *__restrict__ Wp, const T 
         const float bv = to_f32(bias[o]);
         y[0] += bv; y[1] += bv; y[2] += bv; y[3] += bv;
       }
-      if constexpr (kEp) {
+      if constexpr (kEp != kEpNone) {
         const int64_t at = (n * Do + o) * kT;
         float r[4] = {0.f, 0.f, 0.f, 0.f}, z[4];
         if (ep.res != nullptr) Vec4<T>::load(static_cast<const T *>(ep.res) + at, r);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          z[t] = act_saved(ep, y[t]);
-          y[t] = act_apply<sizeof(T) == 2>(ep, y[t]) + r[t];
+          z[t] = act_saved<kEp>(ep, y[t]);
+          y[t] = act_apply<kEp, sizeof(T) == 2>(ep, y[t], r[t]);
         }
         if (ep.z != nullptr) Vec4<T>::store(static_cast<T *>(ep.z) + at, z);
       }

@@ -23,12 +23,10 @@
 
 #include "act.cuh"
 #include "plan.cuh"
+#include "simt_ct_host.cuh"
 
 namespace feql {
 
-constexpr int kCtMaxT = 16;
-constexpr int kCtTile = 32;     // tokens x outputs (or d x c for dW) per block
-constexpr int kCtK = 8;         // channels (or tokens, for dW) per shared-memory chunk
 constexpr int kCtThreads = 256; // 16 x 16 threads, 2 x 2 outputs each
 
 template <int T>
@@ -140,8 +138,8 @@ __global__ void ct_simt_wfft_kernel(const Ty *__restrict__ W, float *__restrict_
 }
 
 // Forward / dX: out[n][o][:] = irDFT( per bin sum_i Wp_k[o][i] * rDFT(in[n][i][:]) ) (+ bias);
-// kEp: then res + act of it (act.cuh).
-template <int T, typename Ty, bool kEp = false>
+// kEp != kEpNone: then res + act of it (act.cuh).
+template <int T, typename Ty, int kEp = kEpNone>
 __global__ void __launch_bounds__(kCtThreads)
 ct_simt_fwd_kernel(const Ty *__restrict__ in, const float *__restrict__ Wp,
                    const Ty *__restrict__ bias, Ty *__restrict__ out, int64_t N, int Ci, int Do,
@@ -230,13 +228,14 @@ ct_simt_fwd_kernel(const Ty *__restrict__ in, const float *__restrict__ Wp,
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         float v = y[t] + bv;
-        if constexpr (kEp) {
+        if constexpr (kEp != kEpNone) {
           // not contracted with the inverse's last product: the same y whether z is saved or not
           v = __fadd_rn(y[t], bv);
           const int64_t at = (n * Do + o) * T + t;
-          if (ep.z != nullptr) static_cast<Ty *>(ep.z)[at] = ct_cast<Ty>(act_saved(ep, v));
-          v = act_apply<sizeof(Ty) == 2>(ep, v);
-          if (ep.res != nullptr) v += ct_load<Ty>(static_cast<const Ty *>(ep.res) + at);
+          if (ep.z != nullptr) static_cast<Ty *>(ep.z)[at] = ct_cast<Ty>(act_saved<kEp>(ep, v));
+          const float r =
+              ep.res != nullptr ? ct_load<Ty>(static_cast<const Ty *>(ep.res) + at) : 0.f;
+          v = act_apply<kEp, sizeof(Ty) == 2>(ep, v, r);
         }
         dst[t] = ct_cast<Ty>(v);
       }

@@ -72,6 +72,8 @@ __device__ __forceinline__ int tc_xf_ordinal(int w) {
 constexpr int kXChunkBytes = kBM * kCK * kT * 2;  // 16 KB: 128 rows x 128 B
 constexpr int kPlaneBytes = kBM * kCK * 2;        // 4 KB: 128 rows x 32 B
 constexpr int kTmemCols = 512;
+constexpr int kResDepth = 2;                      // residual boxes in flight per epilogue warp
+constexpr int kResBox = 32 * 128;                 // 4 KB: 32 rows x 16 channels x 4 fp16
 
 struct TcFwdParams {
   const uint8_t *wt;    // weight chunks of this direction
@@ -87,23 +89,26 @@ struct TcFwdParams {
   int stage_bytes;      // input chunk slot (16 KB; 32 KB of planes in split-TF32 mode)
                         // + weight chunk unless resident, 1 KB aligned
   int bias_floats;      // nD * BD
+  int res_ring;         // 1: the epilogue warps' residual rings are there
   void *out;            // [N][Do][4], fp16 (fp32 in split-TF32 mode)
   Epilogue ep;          // activation, residual, saved z (kernels with kEp)
 };
 
 struct TcSmem {
   // offsets (bytes) from the 1024-aligned dynamic smem base
-  int wres, stage0, bias, bars, total;
+  int wres, stage0, res, bias, bars, total;
 };
 
 __host__ __device__ inline TcSmem tc_fwd_smem(const TcFwdParams &p) {
   TcSmem s;
   s.wres = 0;
   s.stage0 = p.resident ? p.wres_bytes : 0;
-  s.bias = s.stage0 + p.stages * p.stage_bytes;
+  s.res = s.stage0 + p.stages * p.stage_bytes;
+  s.bias = s.res + (p.res_ring ? 4 * kTeams * kResDepth * kResBox : 0);
   s.bars = s.bias + static_cast<int>(align_up(p.bias_floats * 4, 16));
-  // full, tready, empty per stage; acc_full, acc_empty per acc buffer; final; wfull; tmem slot
-  s.total = s.bars + (3 * p.stages + 2 * 2 + 2) * 8 + 16;
+  // full, tready, empty per stage; acc_full, acc_empty per acc buffer; final; wfull; tmem
+  // slot; residual boxes
+  s.total = s.bars + (3 * p.stages + 2 * 2 + 2) * 8 + 16 + 4 * kTeams * kResDepth * 8;
   return s;
 }
 
@@ -154,12 +159,17 @@ struct TcUnits {
 // is dropped: Ootomo and Yokota's split-TF32 scheme), and the epilogue stores
 // fp32 rows.  Bins are not scaled (fp32 has the range).
 //
-// kEp: y = res + act(z) in the epilogue (act.cuh), the pre-activation z stored
-// beside y when the backward pass will want it.  A thread's residual values are
-// loaded before it waits for its accumulators, so the two latencies overlap.
-template <bool kTF32, bool kEp = false>
+// kEp != kEpNone: y = res + act(z) in the epilogue (act.cuh), the pre-activation
+// z stored beside y when the backward pass will want it.  An fp16 residual comes
+// by TMA: each epilogue warp loads the 32-row x 16-channel boxes (4 KB) of its
+// own column groups, in the order in which it will use them, into a private
+// ring of kResDepth slots, so the loads run kResDepth groups ahead (direct loads
+// in the group that uses them cost an HBM latency each: 123 us instead of
+// 78 us on 65536 x 192 -> 192).
+template <bool kTF32, int kEp = kEpNone>
 __global__ void __maxnreg__(96)
-tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdParams p) {
+tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
+                       const __grid_constant__ CUtensorMap tm_res, const TcFwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -174,10 +184,13 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
   uint64_t *final_bar = acc_empty + 2;
   uint64_t *wfull = final_bar + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(wfull + 1);
+  uint64_t *res_full = wfull + 3;  // [epilogue warp][slot]
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
+    if (kEp != kEpNone)
+      for (int i = 0; i < 4 * kTeams * kResDepth; ++i) mbar_init(&res_full[i], 1);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&tready[s], 4);
@@ -394,6 +407,33 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
     int last_g = -1;
     for (int g = g0; g < groups; g += gstep) last_g = g;
     int it = 0;
+    // the residual ring: the group that the next load is for, slots issued and used
+    const bool ring = kEp != kEpNone && !kTF32 && p.res_ring && last_g >= 0;
+    uint8_t *rbox = smem + L.res + ew * kResDepth * kResBox;
+    uint64_t *rbar = res_full + ew * kResDepth;
+    TcUnits ahead(p);
+    int ahead_g = g0, issued = 0, used = 0;
+    if (!split && eteam == 1 && ahead.valid) ahead.next();  // this team takes the odd units
+    auto issue_res = [&]() {
+      if (!ahead.valid) return;
+      if (lane == 0) {
+        const int s = issued % kResDepth;
+        mbar_arrive_expect_tx(&rbar[s], kResBox);
+        tma_load_2d(rbox + s * kResBox, &tm_res, (ahead.j * p.BD + ahead_g * 16) * kT,
+                    ahead.m * kBM + quad * 32, &rbar[s]);
+      }
+      ++issued;
+      ahead_g += gstep;
+      if (ahead_g > last_g) {
+        ahead_g = g0;
+        ahead.next();
+        if (!split && ahead.valid) ahead.next();
+      }
+    };
+    if (ring) {
+      if (lane == 0) tma_prefetch_desc(&tm_res);
+      for (int i = 0; i < kResDepth; ++i) issue_res();
+    }
     for (TcUnits U(p); U.valid; U.next(), ++it) {
       const int m = U.m, j = U.j;
       if (!split && it % kTeams != eteam) continue;
@@ -414,24 +454,24 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
       const int64_t row0 = static_cast<int64_t>(m) * kBM + quad * 32 + (lane >> 2);
       const int64_t row_elems = static_cast<int64_t>(p.Do) * kT;
       for (int g = g0; g < groups; g += gstep) {
+        const uint8_t *rslot = rbox + (used % kResDepth) * kResBox;
+        if (ring && ok) ok = mbar_wait(&rbar[used % kResDepth], (used / kResDepth) & 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int c = g * 16 + h * 8;
           uint32_t y0[2][4], y2[2][4], yr[2][4], yi[2][4];
-          uint4 rv[2][2] = {};  // residual of the thread's channel pair (fp16), rows as below
-          if constexpr (kEp && !kTF32) {
-            const int d = j * p.BD + c + tcp;
-            if (p.ep.res != nullptr && d + 2 <= p.Do) {
+          float4 rv[2][2][2];  // fp32 residual, loaded while the accumulators are awaited
+          if constexpr (kEp != kEpNone && kTF32) {
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                  const int64_t row = row0 + 16 * hf + 8 * rr;
-                  if (row < p.N)
-                    rv[hf][rr] = *reinterpret_cast<const uint4 *>(
-                        static_cast<const __half *>(p.ep.res) + row * row_elems +
-                        static_cast<int64_t>(d) * kT);
-                }
+            for (int i = 0; i < 8; ++i) {
+              const int hf = i >> 2, rr = (i >> 1) & 1, cc = i & 1;
+              const int64_t row = row0 + 16 * hf + 8 * rr;
+              const int d = j * p.BD + c + tcp + cc;
+              rv[hf][rr][cc] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (p.ep.res != nullptr && row < p.N && d < p.Do)
+                rv[hf][rr][cc] = *reinterpret_cast<const float4 *>(
+                    static_cast<const float *>(p.ep.res) + row * row_elems +
+                    static_cast<int64_t>(d) * kT);
             }
           }
           __syncwarp();  // the TMEM loads are warp-collective
@@ -469,16 +509,14 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
                     const int64_t at = row * row_elems + static_cast<int64_t>(d + cc) * kT;
                     float4 q = make_float4(fmaf(0.5f, Yr, e), fmaf(-0.5f, Yi, o),
                                            fmaf(-0.5f, Yr, e), fmaf(0.5f, Yi, o));
-                    if constexpr (kEp) {
+                    if constexpr (kEp != kEpNone) {
                       if (p.ep.z != nullptr)
                         *reinterpret_cast<float4 *>(static_cast<float *>(p.ep.z) + at) = q;
-                      q = make_float4(act_apply<false>(p.ep, q.x), act_apply<false>(p.ep, q.y),
-                                      act_apply<false>(p.ep, q.z), act_apply<false>(p.ep, q.w));
-                      if (p.ep.res != nullptr) {
-                        const float4 r = *reinterpret_cast<const float4 *>(
-                            static_cast<const float *>(p.ep.res) + at);
-                        q = make_float4(q.x + r.x, q.y + r.y, q.z + r.z, q.w + r.w);
-                      }
+                      const float4 r = rv[hf][rr][cc];
+                      q = make_float4(act_apply<kEp, false>(p.ep, q.x, r.x),
+                                      act_apply<kEp, false>(p.ep, q.y, r.y),
+                                      act_apply<kEp, false>(p.ep, q.z, r.z),
+                                      act_apply<kEp, false>(p.ep, q.w, r.w));
                     }
                     *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = q;
                   }
@@ -494,7 +532,14 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {  // rows r0 and r0 + 8
               uint32_t w[4], wz[4];
-              const uint32_t rw[4] = {rv[hf][rr].x, rv[hf][rr].y, rv[hf][rr].z, rv[hf][rr].w};
+              uint4 rv = {};
+              if constexpr (kEp != kEpNone) {
+                const int r = (lane >> 2) + 16 * hf + 8 * rr;  // row of the box
+                if (ring)
+                  rv = *reinterpret_cast<const uint4 *>(
+                      rslot + r * 128 + (((4 * h + (lane & 3)) ^ (r & 7)) << 4));
+              }
+              const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
                 const int i = 2 * rr + cc;
@@ -505,16 +550,16 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
                 const float e = fmaf(4.f, Y0 + Y2, bv), o = fmaf(4.f, Y0 - Y2, bv);
                 float v[4] = {fmaf(8.f, Yr, e), fmaf(-8.f, Yi, o), fmaf(-8.f, Yr, e),
                               fmaf(8.f, Yi, o)};
-                if constexpr (kEp) {
+                if constexpr (kEp != kEpNone) {
 #pragma unroll
                   for (int q = 0; q < 2; ++q)
-                    act_pair(p.ep, v[2 * q], v[2 * q + 1], rw[2 * cc + q], wz[2 * cc + q]);
+                    act_pair<kEp>(p.ep, v[2 * q], v[2 * q + 1], rw[2 * cc + q], wz[2 * cc + q]);
                 }
                 w[2 * cc] = pack_half2(v[0], v[1]);
                 w[2 * cc + 1] = pack_half2(v[2], v[3]);
               }
               const int64_t row = row0 + 16 * hf + 8 * rr;
-              if constexpr (kEp) {
+              if constexpr (kEp != kEpNone) {
                 if (p.ep.z != nullptr && row < p.N)
                   *reinterpret_cast<uint4 *>(static_cast<__half *>(p.ep.z) + row * row_elems +
                                              static_cast<int64_t>(d) * kT) =
@@ -527,8 +572,16 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in, const TcFwdPar
             }
           }
         }
+        if (ring) {
+          ++used;
+          __syncwarp();  // every lane has read the slot that the next load overwrites
+          if (ok) issue_res();
+        }
       }
     }
+    // a warp that gave up waiting still has loads of its own in flight
+    if (ring && !ok)
+      for (; used < issued; ++used) mbar_wait(&rbar[used % kResDepth], (used / kResDepth) & 1);
   }
 
   tc_fence_before();
