@@ -94,11 +94,9 @@ _SIGNATURES = {
     "feql_norm_backward_workspace_bytes": (_SZ, [_I64, _I, _I, _I]),
     "feql_norm_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _I64, _I, _I, _I,
                                 _VP]),
-    "feql_scan_save_bytes": (_SZ, [_I64, _I64, _I, _I, _I, _I]),
-    "feql_scan_forward": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I, _I, _I, _I,
-                               _VP]),
-    "feql_scan_backward": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I, _I,
-                                _I, _I, _VP]),
+    "feql_scan_workspace_bytes": (_SZ, [_I64, _I64, _I, _I, _I, _I, _I]),
+    "feql_scan_forward": (_I, [_VP] * 7 + [_SZ, _I64, _I64, _I, _I, _I, _I, _VP]),
+    "feql_scan_backward": (_I, [_VP] * 11 + [_SZ, _I64, _I64, _I, _I, _I, _I, _VP]),
     "feql_scan_step": (_I, [_VP, _VP, _VP, _VP, _I64, _I, _I, _I, _I, _VP]),
     "feql_device_status": (_I, [_VP]),
     "feql_status_string": (ctypes.c_char_p, [_I]),
@@ -342,22 +340,24 @@ def feql_norm_backward(x, dy, stats, gamma, dx, dgamma, dbeta, ws, ws_bytes: int
                                      dtype, _stream(stream)), "feql_norm_backward")
 
 
-def feql_scan_save_bytes(B: int, N: int, C: int, T: int, shared: bool, dtype: int) -> int:
-    return int(load().feql_scan_save_bytes(B, N, C, T, int(shared), dtype))
+def feql_scan_workspace_bytes(B: int, N: int, C: int, T: int, shared: bool, packed: bool,
+                              dtype: int) -> int:
+    return int(load().feql_scan_workspace_bytes(B, N, C, T, int(shared), int(packed), dtype))
 
 
-def feql_scan_forward(u, g, h0, offsets, h, hN, save, B: int, N: int, C: int, T: int,
+def feql_scan_forward(u, g, h0, offsets, h, hN, ws, ws_bytes: int, B: int, N: int, C: int, T: int,
                       shared: bool, dtype: int, stream=None) -> None:
     _check(load().feql_scan_forward(_ptr(u), _ptr(g), _ptr(h0), _ptr(offsets), _ptr(h), _ptr(hN),
-                                    _ptr(save), B, N, C, T, int(shared), dtype,
+                                    _ptr(ws), ws_bytes, B, N, C, T, int(shared), dtype,
                                     _stream(stream)), "feql_scan_forward")
 
 
-def feql_scan_backward(dh, u, g, save, dhN, offsets, du, dg, dh0, B: int, N: int, C: int, T: int,
-                       shared: bool, dtype: int, stream=None) -> None:
-    _check(load().feql_scan_backward(_ptr(dh), _ptr(u), _ptr(g), _ptr(save), _ptr(dhN),
-                                     _ptr(offsets), _ptr(du), _ptr(dg), _ptr(dh0), B, N, C, T,
-                                     int(shared), dtype, _stream(stream)), "feql_scan_backward")
+def feql_scan_backward(dh, u, g, h, h0, dhN, offsets, du, dg, dh0, ws, ws_bytes: int, B: int,
+                       N: int, C: int, T: int, shared: bool, dtype: int, stream=None) -> None:
+    _check(load().feql_scan_backward(_ptr(dh), _ptr(u), _ptr(g), _ptr(h), _ptr(h0), _ptr(dhN),
+                                     _ptr(offsets), _ptr(du), _ptr(dg), _ptr(dh0), _ptr(ws),
+                                     ws_bytes, B, N, C, T, int(shared), dtype,
+                                     _stream(stream)), "feql_scan_backward")
 
 
 def feql_scan_step(u, g, state, h, B: int, C: int, T: int, shared: bool, dtype: int,

@@ -50,35 +50,11 @@ inline int epilogue_kind(const Epilogue &e) {
   return e.act == FEQL_ACT_GELU || e.act == FEQL_ACT_SILU ? kEpSigmoid : kEpMax;
 }
 
-__device__ __forceinline__ float ex2_fast(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float rcp_fast(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 // The larger of two, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-// sigma(v) and sigma(-v), each to full relative precision.  kFast (fp16
-// outputs): the hardware's exponential and reciprocal, off by 2^-21 or so, far
-// below the outputs' rounding, subnormals flushed.
-template <bool kFast>
-__device__ __forceinline__ void act_sigmoid(float v, float &p, float &q) {
-  const float e = kFast ? ex2_fast(-kLog2e * fabsf(v)) : expf(-fabsf(v));
-  const float big = kFast ? rcp_fast(1.f + e) : 1.f / (1.f + e);
-  const float small = e * big;
-  p = v >= 0.f ? big : small;
-  q = v >= 0.f ? small : big;
 }
 
 // res + act(z).  In the sigmoid family exp(-v) overflows to inf for v below -88,
@@ -96,7 +72,7 @@ __device__ __forceinline__ float act_slope(const Epilogue &e, float z) {
   if (e.act == FEQL_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
   const float z2 = z * z;
   float p, q;
-  act_sigmoid<kFast>(z * fmaf(e.kb, z2, e.ka), p, q);
+  sigmoid_pair<kFast>(z * fmaf(e.kb, z2, e.ka), p, q);
   // where sigma(-v) or sigma(v) has underflowed the second term is 0, whatever
   // its other factor
   const float pq = p * q;

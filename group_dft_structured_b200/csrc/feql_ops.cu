@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/feql.h"
 #include "host.cuh"
 #include "norm.cuh"
@@ -158,14 +160,12 @@ int norm_check(int64_t N, int C, int T, int dtype) {
 
 // ------------------------------------------------------------------- scan
 struct ScanPlan {
-  int V, NW;
+  int V, TX, NW;
   ScanShape s;
 };
 
-// Rows per thread.  Forward: what keeps the local states and products (two
-// fp32 per value, one more for fp32 data in flight) within 128 registers, so
-// that two blocks of 256 threads share an SM; the backward holds twice as much
-// per value.
+// Rows per thread: what keeps the values in use within 128 registers, so that
+// two blocks of 256 threads share an SM.
 constexpr int scan_rows_fwd(bool half, int V) { return V == 4 && !half ? 4 : 8; }
 constexpr int scan_rows_bwd(int V) { return V == 4 ? 4 : 8; }
 
@@ -173,9 +173,14 @@ constexpr int scan_rows_bwd(int V) { return V == 4 ? 4 : 8; }
 // shared gates, a channel) is not a multiple of 4.  One warp per block walks
 // a sequence by itself when there are enough (sequence, tile) units to fill
 // the GPU with warps or the sequences are short; else eight warps share a
-// tile of rows, and clusters of blocks split the rows while the units do not
-// give every SM two blocks and the sequences are long enough.
-ScanPlan scan_plan(int B, int64_t N, int C, int T, bool shared, bool half, int sms) {
+// tile of rows.  (Six warps and 96 registers, for three blocks per SM, were
+// measured: no faster, 105 against 104 us on the 384 units of 128 x 3136 x 24 x 4
+// backward, of which 296 blocks of eight run at a time.)  Then sequences are cut into segments where whole ones would
+// leave SMs idle: dense sequences when not every SM gets a unit, packed ones
+// (whose longest the host does not know) always, in segments of an even share
+// for two blocks (16 of one warp) per SM, two (16) tiles at least.
+ScanPlan scan_plan(int B, int64_t N, int C, int T, bool shared, bool packed, bool half, bool bwd,
+                   int sms) {
   ScanPlan q;
   const int F = C * T;
   const bool sh = shared && T > 1;
@@ -190,71 +195,116 @@ ScanPlan scan_plan(int B, int64_t N, int C, int T, bool shared, bool half, int s
   q.s.T = T;
   q.s.FG = shared ? C : F;
   q.s.m = sh ? T / q.V : 1;
-  q.s.FT = sh ? kScanLanes / T * T : kScanLanes;
+  // lanes along features: 32 features to a tile, or 64 where hardly a lane stays
+  // idle (rows of 128 bytes: half the cache lines per byte, fewer groups to join)
+  q.TX = 32 / q.V;
+  if (q.V == 4 && ceil_div(F, 64) * 64 * 8 <= 9 * F && (!sh || 64 % T == 0)) q.TX = 16;
+  const int most = q.TX * q.V;
+  q.s.FT = sh ? most / T * T : most;
   q.s.ntiles = static_cast<int>(ceil_div(F, q.s.FT));
   const int64_t units = static_cast<int64_t>(B) * q.s.ntiles;
   const int64_t avg = B > 0 ? ceil_div(N, B) : 0;
-  const int warp_rows = q.V * scan_rows_fwd(half, q.V);
-  q.NW = (units >= 16ll * sms || avg <= 2 * warp_rows) ? 1 : 8;
-  q.s.K = 1;
-  if (q.NW == 8)
-    while (q.s.K < kScanMaxCluster && units * q.s.K < 2 * sms && 8ll * warp_rows * q.s.K < avg)
-      q.s.K *= 2;
-  q.s.Q = q.NW * q.V * scan_rows_bwd(q.V);
+  const int warp_rows = 32 / q.TX * (bwd ? scan_rows_bwd(q.V) : scan_rows_fwd(half, q.V));
+  q.NW = (units >= 16ll * sms || avg <= 64) ? 1 : 8;
+  const int tile = q.NW * warp_rows;
+  q.s.seg_rows = 0;
+  if (packed || (q.NW == 8 && units < sms)) {
+    const int64_t blocks = static_cast<int64_t>(sms) * (q.NW == 8 ? 2 : 16);
+    const int64_t share = ceil_div(ceil_div(N * q.s.ntiles, blocks), tile) * tile;
+    const int64_t least = q.NW == 8 ? 2 * tile : 16 * tile;
+    const int64_t rows = share > least ? share : least;
+    if (rows < (packed ? N : q.s.L)) q.s.seg_rows = rows;
+  }
+  q.s.slots = q.s.seg_rows == 0 ? B : N / q.s.seg_rows + B;
+  q.s.maps = nullptr;
   return q;
 }
 
-int64_t scan_save_floats(const ScanPlan &q) {
-  return (q.s.N / q.s.Q + q.s.B) * static_cast<int64_t>(q.s.F);
+size_t scan_maps_bytes(const ScanPlan &q) {
+  if (q.s.seg_rows == 0) return 0;
+  return static_cast<size_t>(q.s.slots) * q.s.ntiles * 2 * q.TX * q.V * 4;
 }
 
+// The main kernel, as the programmatic dependent of the maps' kernel where
+// there is one: its first loads need nothing of it.
 template <typename... Args>
-int scan_launch(void (*kernel)(Args...), const ScanPlan &q, cudaStream_t st, Args... args) {
-  const int64_t grid = static_cast<int64_t>(q.s.B) * q.s.ntiles * q.s.K;
-  if (grid > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
+int scan_launch(void (*kernel)(Args...), const ScanPlan &q, int smem, cudaStream_t st,
+                Args... args) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return FEQL_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(q.s.K);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = q.s.K > 1 ? 1 : 0;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.numAttrs = q.s.seg_rows != 0 ? 1 : 0;
+  cfg.gridDim = dim3(static_cast<unsigned>(q.s.slots * q.s.ntiles));
   cfg.blockDim = dim3(static_cast<unsigned>(q.NW * 32));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FEQL_OK : FEQL_ERR_CUDA;
 }
 
+template <typename Ty, int V, int TX, bool kShared, bool kRev>
+int scan_maps(const ScanPlan &q, const Ty *x, const Ty *g, cudaStream_t st) {
+  if (q.s.seg_rows == 0) return FEQL_OK;
+  const unsigned grid = static_cast<unsigned>(q.s.slots * q.s.ntiles);
+  scan_maps_kernel<Ty, V, TX, 8, kShared, kRev><<<grid, 256, 0, st>>>(x, g, q.s);
+  return launch_status();
+}
+
 #define FEQL_SCAN_CASES(X, Ty) \
-  X(Ty, 4, 8, true) X(Ty, 4, 8, false) X(Ty, 4, 1, true) X(Ty, 4, 1, false) \
-  X(Ty, 2, 8, true) X(Ty, 2, 8, false) X(Ty, 2, 1, true) X(Ty, 2, 1, false) \
-  X(Ty, 1, 8, true) X(Ty, 1, 8, false) X(Ty, 1, 1, true) X(Ty, 1, 1, false)
+  X(Ty, 4, 16, 8, true) X(Ty, 4, 16, 8, false) X(Ty, 4, 16, 1, true) X(Ty, 4, 16, 1, false) \
+  X(Ty, 4, 8, 8, true) X(Ty, 4, 8, 8, false) X(Ty, 4, 8, 1, true) X(Ty, 4, 8, 1, false) \
+  X(Ty, 2, 16, 8, true) X(Ty, 2, 16, 8, false) X(Ty, 2, 16, 1, true) X(Ty, 2, 16, 1, false) \
+  X(Ty, 1, 32, 8, true) X(Ty, 1, 32, 8, false) X(Ty, 1, 32, 1, true) X(Ty, 1, 32, 1, false)
+
+template <typename Ty, int V, int TX, int NW, bool kShared>
+int scan_fwd_run(const ScanPlan &q, const Ty *u, const Ty *g, const float *h0, Ty *h, float *hN,
+                 cudaStream_t st) {
+  constexpr int R = scan_rows_fwd(sizeof(Ty) == 2, V);
+  const int bad = scan_maps<Ty, V, TX, kShared, false>(q, u, g, st);
+  if (bad != FEQL_OK) return bad;
+  return scan_launch(scan_fwd_kernel<Ty, V, TX, R, NW, kShared>, q,
+                     scan_feed_bytes<Ty, V, R, NW, kShared>(1), st, u, g, h0, h, hN, q.s);
+}
+
+template <typename Ty, int V, int TX, int NW, bool kShared>
+int scan_bwd_run(const ScanPlan &q, const Ty *dh, const Ty *u, const Ty *g, const Ty *h,
+                 const float *h0, const float *dhN, Ty *du, Ty *dg, float *dh0, cudaStream_t st) {
+  constexpr int R = scan_rows_bwd(V);
+  const int bad = scan_maps<Ty, V, TX, kShared, true>(q, dh, g, st);
+  if (bad != FEQL_OK) return bad;
+  return scan_launch(scan_bwd_kernel<Ty, V, TX, R, NW, kShared>, q,
+                     scan_feed_bytes<Ty, V, R, NW, kShared>(3), st, dh, u, g, h, h0, dhN, du, dg,
+                     dh0, q.s);
+}
 
 template <typename Ty>
 int scan_fwd(const ScanPlan &q, const void *u, const void *g, const float *h0, void *h, float *hN,
-             float *save, cudaStream_t st) {
+             cudaStream_t st) {
   const bool sh = q.s.FG != q.s.F;
-#define FEQL_CASE(T_, VV, NWW, SH)                                                             \
-  if (q.V == VV && q.NW == NWW && sh == SH)                                                    \
-    return scan_launch(scan_fwd_kernel<T_, VV, scan_rows_fwd(sizeof(T_) == 2, VV), NWW, SH>, q, \
-                       st, static_cast<const T_ *>(u), static_cast<const T_ *>(g), h0,         \
-                       static_cast<T_ *>(h), hN, save, q.s);
+#define FEQL_CASE(T_, VV, XX, NWW, SH)                                               \
+  if (q.V == VV && q.TX == XX && q.NW == NWW && sh == SH)                            \
+    return scan_fwd_run<T_, VV, XX, NWW, SH>(q, static_cast<const T_ *>(u),          \
+                                             static_cast<const T_ *>(g), h0,         \
+                                             static_cast<T_ *>(h), hN, st);
   FEQL_SCAN_CASES(FEQL_CASE, Ty)
 #undef FEQL_CASE
   return FEQL_ERR_UNSUPPORTED;
 }
 
 template <typename Ty>
-int scan_bwd(const ScanPlan &q, const void *dh, const void *u, const void *g, const float *save,
-             const float *dhN, void *du, void *dg, float *dh0, cudaStream_t st) {
+int scan_bwd(const ScanPlan &q, const void *dh, const void *u, const void *g, const void *h,
+             const float *h0, const float *dhN, void *du, void *dg, float *dh0, cudaStream_t st) {
   const bool sh = q.s.FG != q.s.F;
-#define FEQL_CASE(T_, VV, NWW, SH)                                                            \
-  if (q.V == VV && q.NW == NWW && sh == SH)                                                   \
-    return scan_launch(scan_bwd_kernel<T_, VV, scan_rows_bwd(VV), NWW, SH>, q, st,            \
-                       static_cast<const T_ *>(dh), static_cast<const T_ *>(u),               \
-                       static_cast<const T_ *>(g), save, dhN, static_cast<T_ *>(du),          \
-                       static_cast<T_ *>(dg), dh0, q.s);
+#define FEQL_CASE(T_, VV, XX, NWW, SH)                                                          \
+  if (q.V == VV && q.TX == XX && q.NW == NWW && sh == SH)                                       \
+    return scan_bwd_run<T_, VV, XX, NWW, SH>(                                                   \
+        q, static_cast<const T_ *>(dh), static_cast<const T_ *>(u), static_cast<const T_ *>(g), \
+        static_cast<const T_ *>(h), h0, dhN, static_cast<T_ *>(du), static_cast<T_ *>(dg), dh0, \
+        st);
   FEQL_SCAN_CASES(FEQL_CASE, Ty)
 #undef FEQL_CASE
   return FEQL_ERR_UNSUPPORTED;
@@ -346,56 +396,71 @@ int feql_norm_backward(const void *x, const void *dy, const float *stats, const 
               : norm_reduce<float>(part, dgamma, dbeta, C, m, rows, s);
 }
 
-size_t feql_scan_save_bytes(int64_t B, int64_t N, int C, int T, int shared, int dtype) {
+size_t feql_scan_workspace_bytes(int64_t B, int64_t N, int C, int T, int shared, int packed_rows,
+                                 int dtype) {
+  const bool packed = packed_rows != 0;
   if (scan_check(B, N, C, T, dtype, true) != FEQL_OK) return 0;
   DeviceInfo dev;
   if (device_info(&dev) != FEQL_OK) return 0;
-  const ScanPlan q =
-      scan_plan(static_cast<int>(B), N, C, T, shared != 0, is_half(dtype), dev.sms);
-  const size_t bytes = static_cast<size_t>(scan_save_floats(q)) * 4;
-  return bytes > 16 ? bytes : 16;
+  size_t most = 16;
+  for (bool bwd : {false, true}) {
+    const size_t bytes = scan_maps_bytes(
+        scan_plan(static_cast<int>(B), N, C, T, shared != 0, packed, is_half(dtype), bwd, dev.sms));
+    if (bytes > most) most = bytes;
+  }
+  return most;
+}
+
+// The checked plan of a call: FEQL_OK and the plan, or what to return.
+static int scan_prepare(int64_t B, int64_t N, int C, int T, int shared, int dtype,
+                        const int32_t *offsets, bool bwd, void *ws, size_t ws_bytes, ScanPlan *q) {
+  DeviceInfo dev;
+  const int st = device_info(&dev);
+  if (st != FEQL_OK) return st;
+  const bool packed = offsets != nullptr;
+  *q = scan_plan(static_cast<int>(B), N, C, T, shared != 0, packed, is_half(dtype), bwd, dev.sms);
+  if (q->s.slots * q->s.ntiles > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
+  if (q->s.seg_rows != 0 && (ws == nullptr || ws_bytes < scan_maps_bytes(*q)))
+    return FEQL_ERR_INVALID_ARG;
+  q->s.offsets = offsets;
+  q->s.maps = static_cast<float *>(ws);
+  return FEQL_OK;
 }
 
 int feql_scan_forward(const void *u, const void *g, const float *h0, const int32_t *offsets,
-                      void *h, float *hN, void *save, int64_t B, int64_t N, int C, int T,
-                      int shared, int dtype, feql_stream stream) {
+                      void *h, float *hN, void *ws, size_t ws_bytes, int64_t B, int64_t N, int C,
+                      int T, int shared, int dtype, feql_stream stream) {
   const int bad = scan_check(B, N, C, T, dtype, offsets != nullptr);
   if (bad != FEQL_OK) return bad;
   if (!ok_ptr(u, N > 0) || !ok_ptr(g, N > 0) || !ok_ptr(h, N > 0) || !ok_ptr(h0, false) ||
-      !ok_ptr(hN, false) || !ok_ptr(save, false) || !ok_ptr(offsets, false))
+      !ok_ptr(hN, false) || !ok_ptr(offsets, false) || !ok_ptr(ws, false))
     return FEQL_ERR_INVALID_ARG;
   if (B == 0) return FEQL_OK;
-  DeviceInfo dev;
-  const int st = device_info(&dev);
+  ScanPlan q;
+  const int st = scan_prepare(B, N, C, T, shared, dtype, offsets, false, ws, ws_bytes, &q);
   if (st != FEQL_OK) return st;
-  ScanPlan q = scan_plan(static_cast<int>(B), N, C, T, shared != 0, is_half(dtype), dev.sms);
-  q.s.offsets = offsets;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  float *sv = static_cast<float *>(save);
-  return is_half(dtype) ? scan_fwd<__half>(q, u, g, h0, h, hN, sv, s)
-                        : scan_fwd<float>(q, u, g, h0, h, hN, sv, s);
+  return is_half(dtype) ? scan_fwd<__half>(q, u, g, h0, h, hN, s)
+                        : scan_fwd<float>(q, u, g, h0, h, hN, s);
 }
 
-int feql_scan_backward(const void *dh, const void *u, const void *g, const void *save,
-                       const float *dhN, const int32_t *offsets, void *du, void *dg, float *dh0,
-                       int64_t B, int64_t N, int C, int T, int shared, int dtype,
-                       feql_stream stream) {
+int feql_scan_backward(const void *dh, const void *u, const void *g, const void *h,
+                       const float *h0, const float *dhN, const int32_t *offsets, void *du,
+                       void *dg, float *dh0, void *ws, size_t ws_bytes, int64_t B, int64_t N,
+                       int C, int T, int shared, int dtype, feql_stream stream) {
   const int bad = scan_check(B, N, C, T, dtype, offsets != nullptr);
   if (bad != FEQL_OK) return bad;
-  if (!ok_ptr(dh, N > 0) || !ok_ptr(u, N > 0) || !ok_ptr(g, N > 0) || !ok_ptr(save, N > 0) ||
-      !ok_ptr(du, N > 0) || !ok_ptr(dg, N > 0) || !ok_ptr(dhN, false) || !ok_ptr(dh0, false) ||
-      !ok_ptr(offsets, false))
+  if (!ok_ptr(dh, N > 0) || !ok_ptr(u, N > 0) || !ok_ptr(g, N > 0) || !ok_ptr(h, N > 0) ||
+      !ok_ptr(du, N > 0) || !ok_ptr(dg, N > 0) || !ok_ptr(h0, false) || !ok_ptr(dhN, false) ||
+      !ok_ptr(dh0, false) || !ok_ptr(offsets, false) || !ok_ptr(ws, false))
     return FEQL_ERR_INVALID_ARG;
   if (B == 0) return FEQL_OK;
-  DeviceInfo dev;
-  const int st = device_info(&dev);
+  ScanPlan q;
+  const int st = scan_prepare(B, N, C, T, shared, dtype, offsets, true, ws, ws_bytes, &q);
   if (st != FEQL_OK) return st;
-  ScanPlan q = scan_plan(static_cast<int>(B), N, C, T, shared != 0, is_half(dtype), dev.sms);
-  q.s.offsets = offsets;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const float *sv = static_cast<const float *>(save);
-  return is_half(dtype) ? scan_bwd<__half>(q, dh, u, g, sv, dhN, du, dg, dh0, s)
-                        : scan_bwd<float>(q, dh, u, g, sv, dhN, du, dg, dh0, s);
+  return is_half(dtype) ? scan_bwd<__half>(q, dh, u, g, h, h0, dhN, du, dg, dh0, s)
+                        : scan_bwd<float>(q, dh, u, g, h, h0, dhN, du, dg, dh0, s);
 }
 
 int feql_scan_step(const void *u, const void *g, float *state, void *h, int64_t B, int C, int T,

@@ -13,16 +13,24 @@
 // An affine step (a, b): h -> a h + b composes associatively, so a block takes a
 // tile of rows x 32 features at once: a thread scans R rows of V neighbouring
 // features in registers (local states and prefix products), the row groups of
-// a warp join by shuffles, the warps through shared memory, and a cluster of K
-// blocks, which splits a long sequence's rows when there are too few sequences
-// and features to fill the GPU, through distributed shared memory; the block
-// then walks to the next tile with the state in registers.  Every value is read
-// once and written once.  States, products and sums are fp32.
+// a warp join by shuffles and the warps through shared memory, one barrier per
+// tile; the block then walks to the next tile with the state in shared memory.
+// Rows come a tile ahead by cp.async into slots that only the
+// copying thread reads (no barrier), so loads never wait for the joins.  Every
+// value is read once and written once.  States, products and sums are fp32.
 //
-// The backward pass needs h_{l-1}.  The forward saves the fp32 state that
-// enters every tile of the backward kernel (1/Q of the rows), and the backward
-// kernel scans its tile again from there: cheaper than reading h back, and the
-// gradient sees unrounded states.
+// Where whole sequences are too few or too uneven to fill the GPU, their rows
+// are cut into segments of seg_rows, a block to each: a first kernel reads u and
+// g and reduces each segment to its affine map, and the main kernel's block of a
+// segment starts from the maps before it.  That reads the inputs twice, the
+// second time partly from L2, for as many more blocks.  (Sequences of one
+// segment have no map and cost nothing more.)
+//
+// The backward pass needs h_{l-1} and reads the forward's h: in fp16 its rounding
+// moves dg by at most half a step of h against (h - u), less than dg's own
+// rounding.  Recomputing h from saved tile states was tried: it saves one of six
+// streams but scans every tile twice, 118 us against 104 on 128 x 3136 x 24 x 4
+// with channel gates.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -32,8 +40,9 @@
 
 namespace feql {
 
-constexpr int kScanMaxCluster = 8;
-constexpr int kScanLanes = 32;  // features per tile at most (TX * V)
+// Tiles in shared memory: one in use, the others on their way.  (A third was
+// measured: no faster, 68.3 against 62.4 us on 65536 x 96 x 4.)
+constexpr int kStages = 2;
 
 struct ScanShape {
   const int *offsets;  // [B + 1] row offsets of packed sequences, or nullptr (dense)
@@ -44,8 +53,9 @@ struct ScanShape {
   int m;               // shared gates: lanes per channel (T / V)
   int FT;              // features per tile
   int ntiles;
-  int K;               // blocks per cluster (split of the sequence's rows)
-  int Q;               // rows between saved states
+  int64_t seg_rows;    // rows of a segment (a multiple of the tiles), 0: sequences are whole
+  int64_t slots;       // segment slots: N / seg_rows + B, or B
+  float *maps;         // [slots][ntiles][2][TX V] affine maps of the segments
 };
 
 // Sequence b's rows [s, e), forced into the buffers whatever the offsets hold.
@@ -63,6 +73,32 @@ __device__ __forceinline__ void scan_rows(const ScanShape &p, int b, int64_t &s,
   if (e < s) e = s;
 }
 
+// Segment slots: sequence b's k-th segment is slot s / seg_rows + b + k, so that
+// the slots of two sequences cannot meet: ceil(len / n) <= e / n - s / n + 1.
+// Which sequence a slot belongs to: the last b whose first slot is not behind it,
+// by a search over the offsets, 32 candidates a round (the whole warp calls).
+__device__ __forceinline__ int scan_slot_owner(const ScanShape &p, int64_t slot) {
+  if (p.seg_rows == 0) return static_cast<int>(slot);
+  int lo = 0, hi = p.B;  // the owner is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int c = lo + static_cast<int>(threadIdx.x & 31) * step;
+    bool ok = false;
+    if (c < hi) {
+      int64_t s, e;
+      scan_rows(p, c, s, e);
+      ok = s / p.seg_rows + c <= slot;
+    }
+    // ascending offsets: a run of lanes from 0; whatever they hold, lane 0 stands for lo
+    const unsigned m = __ballot_sync(0xffffffffu, ok) | 1u;
+    const int last = 31 - __clz(m);
+    const int top = lo + (last + 1) * step;
+    lo += last * step;
+    hi = top < hi ? top : hi;
+  }
+  return lo;
+}
+
 // fp32 states of V neighbouring features (F and f are multiples of V).
 template <int V>
 __device__ __forceinline__ void load_state(const float *p, float (&v)[V]) {
@@ -77,399 +113,676 @@ __device__ __forceinline__ void store_state(float *p, const float (&v)[V]) {
   k.store(p);
 }
 
-// Saved states: sequence b's k-th is row s / Q + b + k of [N / Q + B][F].  The
-// ranges of two sequences cannot meet: ceil(len / Q) <= e / Q - s / Q + 1.
-__device__ __forceinline__ int64_t scan_save_row(const ScanShape &p, int b, int64_t s, int64_t l) {
-  return s / p.Q + b + l / p.Q;
+// Row r of a thread's local scan: the prefix product and the state from zero.
+template <int V, int GV>
+__device__ __forceinline__ void scan_local(int r, const float (&a)[GV], const float (&na)[GV],
+                                           const float (&u)[V], float (&P)[GV],
+                                           const float (&Pb)[GV], float (&h)[V],
+                                           const float (&hb)[V]) {
+  float nav[V], av[V], b[V];
+  spread(nav, na);
+  vec_mul(b, nav, u);
+  if (r == 0) {
+#pragma unroll
+    for (int j = 0; j < GV; ++j) P[j] = a[j];
+#pragma unroll
+    for (int j = 0; j < V; ++j) h[j] = b[j];
+  } else {
+    spread(av, a);
+    vec_mul(P, a, Pb);
+    vec_fma(h, av, hb, b);
+  }
 }
 
-// a = sigma(g) and na = 1 - a = sigma(-g), each to full relative precision (a
-// subtraction would lose the small one).  fp16 gates: the hardware's exponential
-// and division, about 2^-21, far below the rounding of the outputs.
-template <typename Ty>
-__device__ __forceinline__ void scan_gate(float g, float &a, float &na) {
-  const float e = sizeof(Ty) == 2 ? __expf(-fabsf(g)) : expf(-fabsf(g));
-  const float big = sizeof(Ty) == 2 ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
-  const float small = e * big;
-  a = g >= 0.f ? big : small;
-  na = g >= 0.f ? small : big;
-}
-
-__device__ __forceinline__ uint32_t cluster_rank_addr(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_store(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Block-wide join of the threads' affine maps, thread (tx, ty) holding rows
-// ty R .. of features tx V ..: from the state `carry` that enters the cluster's
-// rows, `in` = the state that enters this thread's rows, and carry becomes the
-// state after the cluster's last row.  kRev: rows run from high to low (the
-// last warp, row group and block come first).  GV: values of A per thread (1
-// when the V features share a gate).
-template <int V, int NW, int GV>
-struct ScanJoin {
-  static constexpr int TX = kScanLanes / V;  // lanes along features; V row groups per warp
-  // [parity][warp][A | B][feature] and, for clusters, [parity][rank][A | B][feature]
-  float warp_tot[2][NW][2][kScanLanes];
-  float rank_tot[2][kScanMaxCluster][2][kScanLanes];
+// The tile loops below come in two forms: kFull, every row of the tile is there
+// and nothing is checked, and the general one for a sequence's last tile.
+template <bool kFull>
+struct ScanRows {
+  int n;  // rows of this thread
+  __device__ __forceinline__ bool has(int r) const { return kFull || r < n; }
 };
 
-template <int V, int NW, int GV, bool kRev>
-__device__ __forceinline__ void scan_join(ScanJoin<V, NW, GV> &sm, int parity, int K, int rank,
-                                          const float (&A)[GV], const float (&Bv)[V],
-                                          float (&carry)[V], float (&in)[V]) {
-  constexpr int TX = ScanJoin<V, NW, GV>::TX;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tx = lane % TX, ty = lane / TX;  // row group within the warp
-  const int pos = kRev ? V - 1 - ty : ty;    // its place in scan order
-  // inclusive scan over the warp's row groups
-  float ia[GV], ib[V];
-#pragma unroll
-  for (int j = 0; j < GV; ++j) ia[j] = A[j];
-#pragma unroll
-  for (int j = 0; j < V; ++j) ib[j] = Bv[j];
-#pragma unroll
-  for (int o = 1; o < V; o <<= 1) {
-    float pa[GV], pb[V];
-#pragma unroll
-    for (int j = 0; j < GV; ++j)
-      pa[j] = kRev ? __shfl_down_sync(0xffffffffu, ia[j], o * TX)
-                   : __shfl_up_sync(0xffffffffu, ia[j], o * TX);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      pb[j] = kRev ? __shfl_down_sync(0xffffffffu, ib[j], o * TX)
-                   : __shfl_up_sync(0xffffffffu, ib[j], o * TX);
-    if (pos >= o) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) ib[j] = fmaf(ia[GV == 1 ? 0 : j], pb[j], ib[j]);
-#pragma unroll
-      for (int j = 0; j < GV; ++j) ia[j] *= pa[j];
-    }
+// Rows of one operand on their way to a thread: R rows of V values per tile.
+// kAsync (4 bytes or more): by cp.async into kStages slots of shared memory;
+// else in registers, one tile ahead.
+template <typename Ty, int V, int R, int NT, bool kAsync>
+struct ScanFeed {
+  static constexpr int kAhead = kStages - 1;
+  static constexpr int kBytes = kStages * R * NT * V * static_cast<int>(sizeof(Ty));
+  Ty *base;  // this thread's values of slot 0
+  int slot = 0;
+  __device__ __forceinline__ void init(uint8_t *smem) {
+    base = reinterpret_cast<Ty *>(smem) + threadIdx.x * V;
   }
-  // exclusive maps within the warp
-  float ea[GV], eb[V];
+  __device__ __forceinline__ Ty *at(int st, int r) { return base + (st * R + r) * NT * V; }
+  template <bool kFull>
+  __device__ __forceinline__ void issue(int st, const Ty *p, int stride, ScanRows<kFull> rows,
+                                        bool skip0 = false) {
 #pragma unroll
-  for (int j = 0; j < GV; ++j) {
-    ea[j] = 1.f;
-    if constexpr (V > 1) {
-      const float q = kRev ? __shfl_down_sync(0xffffffffu, ia[j], TX)
-                           : __shfl_up_sync(0xffffffffu, ia[j], TX);
-      if (pos > 0) ea[j] = q;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    eb[j] = 0.f;
-    if constexpr (V > 1) {
-      const float q = kRev ? __shfl_down_sync(0xffffffffu, ib[j], TX)
-                           : __shfl_up_sync(0xffffffffu, ib[j], TX);
-      if (pos > 0) eb[j] = q;
-    }
-  }
-  if (NW == 1 && K == 1) {
-    // the warp is the block: its total comes from the last row group's lanes
-    const int src = (kRev ? 0 : V - 1) * TX + tx;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      in[j] = fmaf(ea[GV == 1 ? 0 : j], carry[j], eb[j]);
-      const float a = ia[GV == 1 ? 0 : j];
-      const float ta = V > 1 ? __shfl_sync(0xffffffffu, a, src) : a;
-      const float tb = V > 1 ? __shfl_sync(0xffffffffu, ib[j], src) : ib[j];
-      carry[j] = fmaf(ta, carry[j], tb);
-    }
-    return;
-  }
-  if (pos == V - 1) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      sm.warp_tot[parity][warp][0][tx * V + j] = ia[GV == 1 ? 0 : j];
-      sm.warp_tot[parity][warp][1][tx * V + j] = ib[j];
-    }
-  }
-  __syncthreads();
-  float c[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) c[j] = carry[j];
-  if (K > 1) {
-    if (threadIdx.x < kScanLanes) {
-      float ta = 1.f, tb = 0.f;
-#pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        const int w = kRev ? NW - 1 - i : i;
-        const float a = sm.warp_tot[parity][w][0][threadIdx.x];
-        tb = fmaf(a, tb, sm.warp_tot[parity][w][1][threadIdx.x]);
-        ta *= a;
+    for (int r = 0; r < R; ++r)
+      if (rows.has(r) && !(r == 0 && skip0)) {
+        const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(at(st, r)));
+        constexpr int kN = V * static_cast<int>(sizeof(Ty));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(
+                         p + static_cast<int64_t>(r) * stride),
+                     "n"(kN)
+                     : "memory");
       }
-      const uint32_t at = static_cast<uint32_t>(
-          __cvta_generic_to_shared(&sm.rank_tot[parity][rank][0][threadIdx.x]));
-      for (int r = 0; r < K; ++r) {
-        const uint32_t to = cluster_rank_addr(at, r);
-        cluster_store(to, ta);
-        cluster_store(to + kScanLanes * 4, tb);
-      }
-    }
-    // One barrier per tile: the other parity's buffer takes the next tile's
-    // totals, and this one is written again only after the next barrier, which
-    // every block reaches with its reads of this tile done.
-    cluster_sync();
-    for (int i = 0; i < K; ++i) {
-      const int r = kRev ? K - 1 - i : i;
-      if (r == rank) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) c[j] = carry[j];
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        carry[j] = fmaf(sm.rank_tot[parity][r][0][tx * V + j], carry[j],
-                        sm.rank_tot[parity][r][1][tx * V + j]);
-    }
   }
-  float mine[V];
-#pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    const int w = kRev ? NW - 1 - i : i;
-    if (w == warp) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) mine[j] = c[j];
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      c[j] = fmaf(sm.warp_tot[parity][w][0][tx * V + j], c[j],
-                  sm.warp_tot[parity][w][1][tx * V + j]);
+  __device__ __forceinline__ void take(int st) { slot = st; }
+  __device__ __forceinline__ void get(int r, float (&f)[V]) {
+    Pack<Ty, V> k;
+    k.load(at(slot, r));
+    k.unpack(f);
   }
+};
+
+template <typename Ty, int V, int R, int NT>
+struct ScanFeed<Ty, V, R, NT, false> {
+  static constexpr int kAhead = 1;
+  static constexpr int kBytes = 0;
+  Pack<Ty, V> now[R], next[R];
+  __device__ __forceinline__ void init(uint8_t *) {}
+  template <bool kFull>
+  __device__ __forceinline__ void issue(int, const Ty *p, int stride, ScanRows<kFull> rows,
+                                        bool skip0 = false) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    in[j] = fmaf(ea[GV == 1 ? 0 : j], mine[j], eb[j]);
-    if (K == 1) carry[j] = c[j];
+    for (int r = 0; r < R; ++r)
+      if (rows.has(r) && !(r == 0 && skip0)) next[r].load(p + static_cast<int64_t>(r) * stride);
   }
+  __device__ __forceinline__ void take(int) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) now[r] = next[r];
+  }
+  __device__ __forceinline__ void get(int r, float (&f)[V]) { now[r].unpack(f); }
+};
+
+template <typename Ty, int V>
+constexpr bool scan_async() { return V * sizeof(Ty) >= 4; }
+
+// Shared memory of the feeds: u (and h, dh), and g unless it is shared over the
+// group axis (a two-byte gate per row and channel comes by registers).
+template <typename Ty, int V, int R, int NW, bool kShared>
+constexpr int scan_feed_bytes(int streams) {
+  return (streams + (kShared ? 0 : 1)) * ScanFeed<Ty, V, R, NW * 32, scan_async<Ty, V>()>::kBytes;
 }
+
+__device__ __forceinline__ void async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kStages>
+__device__ __forceinline__ void async_wait_tile() {  // the oldest tile is there
+  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+}
+
+// Block-wide join of the threads' affine maps in scan order (kRev: from the last
+// row to the first).  A thread holds the map (A, B) of its rows; GV values of A,
+// 1 when its V features share a gate.
+template <int F, int NW>
+struct ScanJoinSmem {
+  float tot[2][NW][2][F];  // [parity][warp][A | B][feature]
+  float carry[2][F];       // state that enters the tile of this parity
+};
+
+template <int V, int TX, int NW, int GV, bool kRev>
+struct ScanJoin {
+  static constexpr int RG = 32 / TX;         // row groups of a warp
+  using Smem = ScanJoinSmem<TX * V, NW>;
+  float ia[GV], ib[V];                       // inclusive map within the warp
+  float ea[GV], eb[V];                       // exclusive map within the warp
+
+  __device__ __forceinline__ static int tx() { return threadIdx.x % TX; }
+  __device__ __forceinline__ static int pos() {  // the row group's place within the warp
+    const int ty = (threadIdx.x & 31) / TX;
+    return kRev ? RG - 1 - ty : ty;
+  }
+  __device__ __forceinline__ static int wpos() {  // the warp's place within the block
+    const int w = threadIdx.x >> 5;
+    return kRev ? NW - 1 - w : w;
+  }
+  // the threads that end up with the state after the tile's last row
+  __device__ __forceinline__ static bool last() { return pos() == RG - 1 && wpos() == NW - 1; }
+
+  __device__ __forceinline__ static float prev(float v, int o) {
+    return kRev ? __shfl_down_sync(0xffffffffu, v, o * TX) : __shfl_up_sync(0xffffffffu, v, o * TX);
+  }
+
+  // Scans the warp's row groups and leaves the warp's total for the others.
+  __device__ __forceinline__ void scan(Smem &sm, int parity, const float (&A)[GV],
+                                       const float (&B)[V]) {
+    const int ps = pos();
+#pragma unroll
+    for (int j = 0; j < GV; ++j) ia[j] = A[j];
+#pragma unroll
+    for (int j = 0; j < V; ++j) ib[j] = B[j];
+#pragma unroll
+    for (int o = 1; o < RG; o <<= 1) {
+      float pa[GV], pb[V];
+#pragma unroll
+      for (int j = 0; j < GV; ++j) pa[j] = prev(ia[j], o);
+#pragma unroll
+      for (int j = 0; j < V; ++j) pb[j] = prev(ib[j], o);
+      if (ps >= o) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) ib[j] = fmaf(ia[GV == 1 ? 0 : j], pb[j], ib[j]);
+#pragma unroll
+        for (int j = 0; j < GV; ++j) ia[j] *= pa[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < GV; ++j) {
+      const float q = RG > 1 ? prev(ia[j], 1) : 1.f;
+      ea[j] = ps > 0 ? q : 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float q = RG > 1 ? prev(ib[j], 1) : 0.f;
+      eb[j] = ps > 0 ? q : 0.f;
+    }
+    if (NW > 1 && ps == RG - 1) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        sm.tot[parity][wpos()][0][tx() * V + j] = ia[GV == 1 ? 0 : j];
+        sm.tot[parity][wpos()][1][tx() * V + j] = ib[j];
+      }
+    }
+  }
+
+  // After the block's barrier: `in` = the state that enters this thread's rows.
+  // The state that enters the tile is `carry` at first, then in shared memory; the
+  // last() threads leave the one after the tile there and in `carry`.
+  __device__ __forceinline__ void join(Smem &sm, int parity, bool first, float (&carry)[V],
+                                       float (&in)[V]) {
+    float c[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      c[j] = (first || NW == 1) ? carry[j] : sm.carry[parity][tx() * V + j];
+    if (NW > 1) {
+      const int w1 = wpos();
+#pragma unroll
+      for (int w = 0; w < NW - 1; ++w)
+        if (w < w1) {  // the same for a whole warp
+          float wa[V], wb[V];
+          load_state<V>(&sm.tot[parity][w][0][tx() * V], wa);
+          load_state<V>(&sm.tot[parity][w][1][tx() * V], wb);
+          vec_fma(c, wa, c, wb);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) in[j] = fmaf(ea[GV == 1 ? 0 : j], c[j], eb[j]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) c[j] = fmaf(ia[GV == 1 ? 0 : j], c[j], ib[j]);
+    if (NW == 1) {  // from the last row group's lanes to all
+      const int src = (kRev ? 0 : RG - 1) * TX + tx();
+#pragma unroll
+      for (int j = 0; j < V; ++j) carry[j] = __shfl_sync(0xffffffffu, c[j], src);
+    } else if (last()) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        carry[j] = c[j];
+        sm.carry[parity ^ 1][tx() * V + j] = c[j];
+      }
+    }
+  }
+};
 
 // Rows that belong to no sequence (before the first offset, behind the last)
 // are zeroed in the outputs, so that what consumes them sees numbers: by the
 // blocks of the first and of the last sequence, each for its features.
 template <typename Ty, int V, int TY>
-__device__ __forceinline__ void scan_zero_rest(const ScanShape &p, int b, int rank, int ty,
+__device__ __forceinline__ void scan_zero_rest(const ScanShape &p, int b, int seg, int nseg, int ty,
                                                int64_t s, int64_t e, Ty *out, int width, int col,
                                                bool live) {
   if (p.offsets == nullptr || !live) return;
   Pack<Ty, V> z;
   z.zero();
-  const int64_t step = static_cast<int64_t>(p.K) * TY;
+  const int64_t step = static_cast<int64_t>(nseg) * TY;
   if (b == 0)
-    for (int64_t r = static_cast<int64_t>(rank) * TY + ty; r < s; r += step)
+    for (int64_t r = static_cast<int64_t>(seg) * TY + ty; r < s; r += step)
       z.store(out + r * width + col);
   if (b == p.B - 1)
-    for (int64_t r = e + static_cast<int64_t>(rank) * TY + ty; r < p.N; r += step)
+    for (int64_t r = e + static_cast<int64_t>(seg) * TY + ty; r < p.N; r += step)
       z.store(out + r * width + col);
 }
 
-template <typename Ty, int V, int R, int NW, bool kShared>
-__global__ void __launch_bounds__(NW * 32)
-scan_fwd_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, const float *__restrict__ h0,
-                Ty *__restrict__ h, float *__restrict__ hN, float *__restrict__ save,
-                const ScanShape p) {
+// Blocks of NW warps that an SM holds: by registers (128 a thread, 80 where the
+// walks keep little).
+constexpr int scan_blocks(int NW, bool lean) { return NW == 8 ? (lean ? 3 : 2) : 16; }
+
+// What a block works on: sequence b, its segment seg of nseg (a sequence without
+// rows has one, empty), feature tile; a thread's features f .. f + V, and its row
+// group ty.
+template <int V, int TX, int NW, bool kShared>
+struct ScanPlace {
+  int b, seg, nseg, tile, tx, ty, f, gf;
+  int64_t slot;
+  bool live;                  // this thread's features exist
+  bool work;                  // the slot holds a segment
+  int64_t s, e, len, r0, r1;  // rows of the sequence; the segment's within it
+  __device__ __forceinline__ explicit ScanPlace(const ScanShape &p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    tx = lane % TX;
+    ty = warp * (32 / TX) + lane / TX;
+    slot = blockIdx.x / p.ntiles;
+    tile = blockIdx.x % p.ntiles;
+    f = tile * p.FT + tx * V;
+    live = tx * V < p.FT && f < p.F;
+    if (!live) f = tile * p.FT;  // a lane without features reads another's and writes nothing
+    gf = kShared ? f / p.T : f;
+    b = scan_slot_owner(p, slot);
+    scan_rows(p, b, s, e);
+    len = e - s;
+    seg = 0;
+    nseg = 1;
+    r0 = 0;
+    r1 = len;
+    if (p.seg_rows != 0) {
+      seg = static_cast<int>(slot - (s / p.seg_rows + b));
+      nseg = static_cast<int>((len + p.seg_rows - 1) / p.seg_rows);
+      if (nseg < 1) nseg = 1;
+      r0 = seg * p.seg_rows;
+      r1 = r0 + p.seg_rows < len ? r0 + p.seg_rows : len;
+    }
+    work = seg >= 0 && seg < nseg;
+  }
+  // The map of segment q, this thread's features: A at [0][..], B at [1][..].
+  __device__ __forceinline__ float *map(const ScanShape &p, int q) const {
+    return p.maps + ((slot - seg + q) * p.ntiles + tile) * 2 * TX * V + tx * V;
+  }
+};
+
+// kRev: the gradient's maps c -> A c + B, B from dh; else the states', B from u.
+// Each row group walks its share of the segment's rows by itself, eight at a
+// time with the next eight on their way, and the groups join once at the end.
+template <typename Ty, int V, int TX, int NW, bool kShared, bool kRev>
+__global__ void __launch_bounds__(NW * 32, 2)
+scan_maps_kernel(const Ty *__restrict__ x, const Ty *__restrict__ g, const ScanShape p) {
   constexpr int GV = kShared ? 1 : V;
-  constexpr int TX = kScanLanes / V, TY = NW * V, RT = TY * R;
-  __shared__ ScanJoin<V, NW, GV> sm;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tx = lane % TX, ty = warp * V + lane / TX;
-  const int rank = blockIdx.x % p.K, unit = blockIdx.x / p.K;
-  const int tile = unit % p.ntiles, b = unit / p.ntiles;
-  const int f = tile * p.FT + tx * V;
-  const bool live = tx * V < p.FT && f < p.F;
-  const int gf = kShared ? f / p.T : f;
-  int64_t s, e;
-  scan_rows(p, b, s, e);
-  const int64_t len = e - s;
-  float carry[V] = {};
-  if (live && h0 != nullptr) load_state<V>(h0 + static_cast<int64_t>(b) * p.F + f, carry);
-  int parity = 0;
-  for (int64_t base = 0; base < len; base += static_cast<int64_t>(p.K) * RT, parity ^= 1) {
-    const int64_t l0 = base + rank * RT + ty * R;
-    Pack<Ty, V> ru[R];
-    Pack<Ty, GV> rg[R];
+  constexpr int TY = NW * 32 / TX, R = V == 4 && sizeof(Ty) == 4 ? 4 : 8;
+  using J = ScanJoin<V, TX, NW, GV, kRev>;
+  __shared__ __align__(16) typename J::Smem sm;
+  const ScanPlace<V, TX, NW, kShared> at(p);
+  // (the same for a whole block; a sequence's last segment in scan order has no use)
+  if (!at.work || at.seg == (kRev ? 0 : at.nseg - 1)) return;
+  const int64_t rows = at.r1 - at.r0;
+  const int64_t share = (rows + TY - 1) / TY;
+  const int64_t l0 = at.r0 + at.ty * share;
+  const int64_t l1 = l0 + share < at.r1 ? l0 + share : at.r1;
+  float A[GV], B[V];
+#pragma unroll
+  for (int j = 0; j < GV; ++j) A[j] = 1.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) B[j] = 0.f;
+  const int64_t n = l1 > l0 ? l1 - l0 : 0;
+  const int64_t first = at.s + (kRev ? l1 - 1 : l0);
+  const Ty *px = x + first * p.F + at.f, *pg = g + first * p.FG + at.gf;
+  const int sx = kRev ? -p.F : p.F, sg = kRev ? -p.FG : p.FG;
+  Pack<Ty, V> rx[R], nx[R];
+  Pack<Ty, GV> rg[R], ng[R];
+  auto fetch = [&](int64_t k) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (live && l0 + r < len) {
-        ru[r].load(u + (s + l0 + r) * p.F + f);
-        rg[r].load(g + (s + l0 + r) * p.FG + gf);
+      if (k + r < n) {
+        nx[r].load(px + static_cast<int64_t>(r) * sx);
+        ng[r].load(pg + static_cast<int64_t>(r) * sg);
       }
-    // local states from a zero state, and prefix products
-    float P[R][GV], hl[R][V];
+    px += static_cast<int64_t>(R) * sx;
+    pg += static_cast<int64_t>(R) * sg;
+  };
+  fetch(0);
+  for (int64_t k = 0; k < n; k += R) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float a[GV], na[GV], uv[V];
-      if (live && l0 + r < len) {
-        float gv[GV];
-        rg[r].unpack(gv);
-        ru[r].unpack(uv);
-#pragma unroll
-        for (int j = 0; j < GV; ++j) scan_gate<Ty>(gv[j], a[j], na[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < GV; ++j) { a[j] = 1.f; na[j] = 0.f; }
-#pragma unroll
-        for (int j = 0; j < V; ++j) uv[j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < GV; ++j) P[r][j] = r == 0 ? a[j] : a[j] * P[r == 0 ? 0 : r - 1][j];
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int q = GV == 1 ? 0 : j;
-        hl[r][j] = r == 0 ? na[q] * uv[j] : fmaf(a[q], hl[r == 0 ? 0 : r - 1][j], na[q] * uv[j]);
-      }
+      rx[r] = nx[r];
+      rg[r] = ng[r];
     }
-    float in[V];
-    scan_join<V, NW, GV, false>(sm, parity, p.K, rank, P[R - 1], hl[R - 1], carry, in);
-    if (live && l0 < len) {
-      if (save != nullptr && l0 % p.Q == 0)
-        store_state<V>(save + scan_save_row(p, b, s, l0) * p.F + f, in);
+    fetch(k + R);
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (l0 + r < len) {
-          float o[V];
+    for (int r = 0; r < R; ++r)
+      if (k + r < n) {
+        float xv[V], gv[GV], a[GV], na[GV], av[V], nav[V];
+        rx[r].unpack(xv);
+        rg[r].unpack(gv);
 #pragma unroll
-          for (int j = 0; j < V; ++j) o[j] = fmaf(P[r][GV == 1 ? 0 : j], in[j], hl[r][j]);
-          Pack<Ty, V> k;
-          k.pack(o);
-          k.store(h + (s + l0 + r) * p.F + f);
+        for (int j = 0; j < GV; ++j) sigmoid_pair<sizeof(Ty) == 2>(gv[j], a[j], na[j]);
+        spread(av, a);
+        if constexpr (kRev) {
+          vec_add(B, B, xv);
+          vec_mul(B, B, av);
+        } else {
+          spread(nav, na);
+          vec_mul(xv, nav, xv);
+          vec_fma(B, av, B, xv);
         }
+        vec_mul(A, A, a);
+      }
+  }
+  // joined: the map's constant part is where a zero state goes, its factor the product
+  J join;
+  join.scan(sm, 0, A, B);
+  if (NW > 1) __syncthreads();
+  float carry[V] = {}, in[V], prod[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) prod[j] = 1.f;
+  join.join(sm, 0, true, carry, in);
+  if (NW > 1) {
+#pragma unroll
+    for (int w = 0; w < NW - 1; ++w)
+#pragma unroll
+      for (int j = 0; j < V; ++j) prod[j] *= sm.tot[0][w][0][at.tx * V + j];
+  }
+  if (J::last() && at.live) {
+    float *to = at.map(p, at.seg);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      to[j] = prod[j] * join.ia[GV == 1 ? 0 : j];
+      to[TX * V + j] = carry[j];
     }
   }
-  scan_zero_rest<Ty, V, TY>(p, b, rank, ty, s, e, h, p.F, f, live);
-  if (hN != nullptr && live && rank == 0 && ty == 0)
-    store_state<V>(hN + static_cast<int64_t>(b) * p.F + f, carry);
 }
 
-template <typename Ty, int V, int R, int NW, bool kShared>
-__global__ void __launch_bounds__(NW * 32)
-scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *__restrict__ g,
-                const float *__restrict__ save, const float *__restrict__ dhN,
-                Ty *__restrict__ du, Ty *__restrict__ dg, float *__restrict__ dh0,
-                const ScanShape p) {
-  constexpr int GV = kShared ? 1 : V;
-  constexpr int TX = kScanLanes / V, TY = NW * V, RT = TY * R;
-  __shared__ ScanJoin<V, NW, GV> sf, sr;  // the states (forward) and the gradient (reverse)
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tx = lane % TX, ty = warp * V + lane / TX;
-  const int rank = blockIdx.x % p.K, unit = blockIdx.x / p.K;
-  const int tile = unit % p.ntiles, b = unit / p.ntiles;
-  const int f = tile * p.FT + tx * V;
-  const bool live = tx * V < p.FT && f < p.F;
-  const int gf = kShared ? f / p.T : f;
-  int64_t s, e;
-  scan_rows(p, b, s, e);
-  const int64_t len = e - s;
-  float carry[V] = {};
-  if (live && dhN != nullptr) load_state<V>(dhN + static_cast<int64_t>(b) * p.F + f, carry);
-  const int64_t step = static_cast<int64_t>(p.K) * RT;
-  int parity = 0;
-  for (int64_t base = len > 0 ? (len - 1) / step * step : -1; base >= 0;
-       base -= step, parity ^= 1) {
-    const int64_t t0 = base + rank * RT;  // the block's first row (a multiple of Q = RT)
-    const int64_t l0 = t0 + ty * R;
-    Pack<Ty, V> ru[R], rd[R];
-    Pack<Ty, GV> rg[R];
+// The state that enters segment seg: the maps before it (kRev: behind it, from
+// the sequence's last one), applied to the state at the sequence's end.
+template <bool kRev, int V, int TX, int NW, bool kShared>
+__device__ __forceinline__ void scan_enter(const ScanShape &p,
+                                           const ScanPlace<V, TX, NW, kShared> &at,
+                                           float (&carry)[V]) {
+  const int n = kRev ? at.nseg - 1 - at.seg : at.seg;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const float *m = at.map(p, kRev ? at.nseg - 1 - i : i);
+    float A[V], B[V];
+    load_state<V>(m, A);
+    load_state<V>(m + TX * V, B);
+    vec_fma(carry, A, carry, B);
+  }
+}
+
+// Before the first use of the maps: their kernel has finished.  Every block
+// waits, so that the grid never ends before it.
+__device__ __forceinline__ void scan_wait_maps(const ScanShape &p) {
+  if (p.seg_rows != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A row's gates; rows that are not there pass the state on: a = 1, 1 - a = 0.
+template <typename Ty, int GV, class Feed>
+__device__ __forceinline__ void scan_row_gates(Feed &fg, int r, bool there, float (&a)[GV],
+                                               float (&na)[GV]) {
+  if (there) {
+    float gv[GV];
+    fg.get(r, gv);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (live && l0 + r < len) {
-        ru[r].load(u + (s + l0 + r) * p.F + f);
-        rd[r].load(dh + (s + l0 + r) * p.F + f);
-        rg[r].load(g + (s + l0 + r) * p.FG + gf);
-      }
-    float state[V] = {};  // the state that enters the block's rows
-    if (live && t0 < len) load_state<V>(save + scan_save_row(p, b, s, t0) * p.F + f, state);
-    float a[R][GV], na[R][GV], P[R][GV], hl[R][V];
+    for (int j = 0; j < GV; ++j) sigmoid_pair<sizeof(Ty) == 2>(gv[j], a[j], na[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < GV; ++j) { a[j] = 1.f; na[j] = 0.f; }
+  }
+}
+
+template <typename Ty, int V, int TX, int R, int NW, bool kShared>
+__global__ void __launch_bounds__(NW * 32, scan_blocks(NW, kShared && V > 1))
+scan_fwd_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, const float *__restrict__ h0,
+                Ty *__restrict__ h, float *__restrict__ hN, const ScanShape p) {
+  constexpr int GV = kShared ? 1 : V;
+  constexpr int TY = NW * 32 / TX, RT = TY * R, NT = NW * 32;
+  constexpr bool kAsync = scan_async<Ty, V>(), kLean = kShared && V > 1;
+  using J = ScanJoin<V, TX, NW, GV, false>;
+  extern __shared__ __align__(16) uint8_t feeds[];
+  __shared__ __align__(16) typename J::Smem sm;
+  ScanFeed<Ty, V, R, NT, kAsync> fu;
+  ScanFeed<Ty, GV, R, NT, kAsync && !kShared> fg;
+  fu.init(feeds);
+  fg.init(feeds + fu.kBytes);
+  const ScanPlace<V, TX, NW, kShared> at(p);
+  if (!at.work) {
+    scan_wait_maps(p);
+    return;
+  }
+  const int64_t rows = at.r1 - at.r0;
+  const int steps = static_cast<int>((rows + RT - 1) / RT);
+  const int whole = static_cast<int>(rows / RT);  // tiles with all their rows
+  const int64_t row = at.s + at.r0 + at.ty * R;   // this thread's first row of the next load
+  const Ty *pu = u + row * p.F + at.f, *pg = g + row * p.FG + at.gf;
+  const int64_t du = static_cast<int64_t>(RT) * p.F, dg = static_cast<int64_t>(RT) * p.FG;
+  // rows of tile i that are this thread's
+  auto have = [&](int i) {
+    const int64_t n = rows - (static_cast<int64_t>(i) * RT + at.ty * R);
+    return n < 0 ? 0 : (n < R ? static_cast<int>(n) : R);
+  };
+  auto issue_u = [&](int i) {
+    if (i < whole) fu.issue(i % kStages, pu, p.F, ScanRows<true>{R});
+    else if (i < steps) fu.issue(i % kStages, pu, p.F, ScanRows<false>{have(i)});
+    pu += du;
+  };
+  auto issue_g = [&](int i) {
+    if (i < whole) fg.issue(i % kStages, pg, p.FG, ScanRows<true>{R});
+    else if (i < steps) fg.issue(i % kStages, pg, p.FG, ScanRows<false>{have(i)});
+    pg += dg;
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < fu.kAhead) issue_u(i);
+    if (i < fg.kAhead) issue_g(i);
+    async_commit();
+  }
+  float carry[V] = {};
+  if (h0 != nullptr) load_state<V>(h0 + static_cast<int64_t>(at.b) * p.F + at.f, carry);
+  scan_wait_maps(p);
+  scan_enter<false>(p, at, carry);
+  Ty *ph = h + row * p.F + at.f;
+  auto tile = [&](int i, auto rows_of) {
+    // the map of the thread's rows: a gate per channel is kept and u read again
+    // for the second walk, a gate per value the local states and products
+    constexpr int K = kLean ? 1 : R;
+    float a[R][GV], na[R][GV], P[K][GV], hl[K][V];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float uv[V];
-      if (live && l0 + r < len) {
-        float gv[GV];
-        rg[r].unpack(gv);
-        ru[r].unpack(uv);
+      float uv[V] = {};
+      scan_row_gates<Ty, GV>(fg, r, rows_of.has(r), a[r], na[r]);
+      if (rows_of.has(r)) fu.get(r, uv);
+      const int k = kLean ? 0 : r, kb = kLean || r == 0 ? 0 : r - 1;
+      scan_local<V, GV>(r, a[r], na[r], uv, P[k], P[kb], hl[k], hl[kb]);
+    }
+    J join;
+    float in[V];
+    join.scan(sm, i & 1, P[K - 1], hl[K - 1]);
+    if (NW > 1) __syncthreads();
+    join.join(sm, i & 1, i == 0, carry, in);
+    if (!at.live) return;
 #pragma unroll
-        for (int j = 0; j < GV; ++j) scan_gate<Ty>(gv[j], a[r][j], na[r][j]);
-      } else {
+    for (int r = 0; r < R; ++r)
+      if (rows_of.has(r)) {
+        float o[V];
+        if constexpr (kLean) {
+          float uv[V], av[V], nav[V];
+          fu.get(r, uv);
+          spread(av, a[r]);
+          spread(nav, na[r]);
+          vec_mul(uv, nav, uv);
+          vec_fma(in, av, in, uv);
 #pragma unroll
-        for (int j = 0; j < GV; ++j) { a[r][j] = 1.f; na[r][j] = 0.f; }
-#pragma unroll
-        for (int j = 0; j < V; ++j) uv[j] = 0.f;
-        rd[r].zero();
+          for (int j = 0; j < V; ++j) o[j] = in[j];
+        } else {
+          float pv[V];
+          spread(pv, P[kLean ? 0 : r]);
+          vec_fma(o, pv, in, hl[kLean ? 0 : r]);
+        }
+        Pack<Ty, V> k;
+        k.pack(o);
+        k.store(ph + static_cast<int64_t>(r) * p.F);
       }
-#pragma unroll
-      for (int j = 0; j < GV; ++j)
-        P[r][j] = r == 0 ? a[r][j] : a[r][j] * P[r == 0 ? 0 : r - 1][j];
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int q = GV == 1 ? 0 : j;
-        hl[r][j] = r == 0 ? na[r][q] * uv[j]
-                          : fmaf(a[r][q], hl[r == 0 ? 0 : r - 1][j], na[r][q] * uv[j]);
+  };
+  for (int i = 0; i < steps; ++i, ph += du) {
+    async_wait_tile<kStages>();
+    fu.take(i % kStages);
+    fg.take(i % kStages);
+    issue_u(i + fu.kAhead);
+    issue_g(i + fg.kAhead);
+    async_commit();
+    if (i < whole) tile(i, ScanRows<true>{R});
+    else tile(i, ScanRows<false>{have(i)});
+  }
+  if (hN != nullptr && at.live && at.seg == at.nseg - 1 && J::last())
+    store_state<V>(hN + static_cast<int64_t>(at.b) * p.F + at.f, carry);
+  scan_zero_rest<Ty, V, TY>(p, at.b, at.seg, at.nseg, at.ty, at.s, at.e, h, p.F, at.f, at.live);
+}
+
+// h: the forward's output; the state before the first row of a sequence is h0.
+template <typename Ty, int V, int TX, int R, int NW, bool kShared>
+__global__ void __launch_bounds__(NW * 32, scan_blocks(NW, false))
+scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *__restrict__ g,
+                const Ty *__restrict__ h, const float *__restrict__ h0,
+                const float *__restrict__ dhN, Ty *__restrict__ du, Ty *__restrict__ dg,
+                float *__restrict__ dh0, const ScanShape p) {
+  constexpr int GV = kShared ? 1 : V;
+  constexpr int TY = NW * 32 / TX, RT = TY * R, NT = NW * 32;
+  constexpr bool kAsync = scan_async<Ty, V>();
+  using J = ScanJoin<V, TX, NW, GV, true>;
+  extern __shared__ __align__(16) uint8_t feeds[];
+  __shared__ __align__(16) typename J::Smem sm;
+  ScanFeed<Ty, V, R, NT, kAsync> fu, fd, fh;
+  ScanFeed<Ty, GV, R, NT, kAsync && !kShared> fg;
+  fu.init(feeds);
+  fd.init(feeds + fu.kBytes);
+  fh.init(feeds + 2 * fu.kBytes);
+  fg.init(feeds + 3 * fu.kBytes);
+  const ScanPlace<V, TX, NW, kShared> at(p);
+  if (!at.work) {
+    scan_wait_maps(p);
+    return;
+  }
+  const int64_t rows = at.r1 - at.r0;
+  const int steps = static_cast<int>((rows + RT - 1) / RT);
+  const int part = steps - static_cast<int>(rows / RT);  // 1: the first step's tile lacks rows
+  // step i takes tile steps - 1 - i: the tiles run from the segment's end
+  const int64_t row = at.s + at.r0 + static_cast<int64_t>(steps - 1) * RT + at.ty * R;
+  const Ty *pu = u + row * p.F + at.f, *pd = dh + row * p.F + at.f;
+  // the rows before; before the sequence's first row stands h0
+  const Ty *ph = h + (row - 1) * p.F + at.f;
+  const bool top = at.seg == 0 && at.ty == 0;
+  const Ty *pg = g + row * p.FG + at.gf;
+  const int64_t step = static_cast<int64_t>(RT) * p.F, gstep = static_cast<int64_t>(RT) * p.FG;
+  auto have = [&]() {  // this thread's rows of the last tile
+    const int64_t n = rows - (static_cast<int64_t>(steps - 1) * RT + at.ty * R);
+    return n < 0 ? 0 : (n < R ? static_cast<int>(n) : R);
+  };
+  auto issue_x = [&](int i) {
+    if (i < steps) {
+      const int st = i % kStages;
+      const bool none = top && i == steps - 1;
+      if (i < part) {
+        const ScanRows<false> n{have()};
+        fu.issue(st, pu, p.F, n);
+        fd.issue(st, pd, p.F, n);
+        fh.issue(st, ph, p.F, n, none);
+      } else {
+        const ScanRows<true> n{R};
+        fu.issue(st, pu, p.F, n);
+        fd.issue(st, pd, p.F, n);
+        fh.issue(st, ph, p.F, n, none);
       }
     }
-    float Bc[V], in[V], cin[V];
+    pu -= step;
+    pd -= step;
+    ph -= step;
+  };
+  auto issue_g = [&](int i) {
+    if (i < part) fg.issue(i % kStages, pg, p.FG, ScanRows<false>{have()});
+    else if (i < steps) fg.issue(i % kStages, pg, p.FG, ScanRows<true>{R});
+    pg -= gstep;
+  };
 #pragma unroll
-    for (int j = 0; j < V; ++j) Bc[j] = 0.f;
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < fu.kAhead) issue_x(i);
+    if (i < fg.kAhead) issue_g(i);
+    async_commit();
+  }
+  float carry[V] = {}, start[V] = {};
+  const int64_t state = static_cast<int64_t>(at.b) * p.F + at.f;
+  if (dhN != nullptr) load_state<V>(dhN + state, carry);
+  if (top && h0 != nullptr) load_state<V>(h0 + state, start);
+  scan_wait_maps(p);
+  scan_enter<true>(p, at, carry);
+  Ty *pdu = du + row * p.F + at.f, *pdg = dg + row * p.FG + at.gf;
+  auto tile = [&](int i, auto rows_of) {
+    float a[R][GV], na[R][GV], A[GV], d[R][V], Bc[V] = {}, cin[V];
+#pragma unroll
+    for (int j = 0; j < GV; ++j) A[j] = 1.f;
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      float d[V];
-      rd[r].unpack(d);
+      float av[V];
+      scan_row_gates<Ty, GV>(fg, r, rows_of.has(r), a[r], na[r]);
 #pragma unroll
-      for (int j = 0; j < V; ++j) Bc[j] = a[r][GV == 1 ? 0 : j] * (d[j] + Bc[j]);
+      for (int j = 0; j < V; ++j) d[r][j] = 0.f;
+      if (rows_of.has(r)) fd.get(r, d[r]);
+      spread(av, a[r]);
+      vec_add(Bc, Bc, d[r]);
+      vec_mul(Bc, Bc, av);
+      vec_mul(A, A, a[r]);
     }
-    scan_join<V, NW, GV, false>(sf, parity, 1, 0, P[R - 1], hl[R - 1], state, in);
-    scan_join<V, NW, GV, true>(sr, parity, p.K, rank, P[R - 1], Bc, carry, cin);
+    J join;
+    join.scan(sm, i & 1, A, Bc);
+    if (NW > 1) __syncthreads();
+    join.join(sm, i & 1, i == 0, carry, cin);
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      float d[V], uv[V], o[V], gsum = 0.f, og[GV];
-      rd[r].unpack(d);
-      const bool row = live && l0 + r < len;
-      if (row) {
-        ru[r].unpack(uv);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) uv[j] = 0.f;
+      float uv[V] = {}, before[V] = {}, o[V], gg[V], av[V], nav[V], og[GV];
+      if (rows_of.has(r)) {
+        fu.get(r, uv);
+        fh.get(r, before);
       }
+      if (r == 0 && top && i == steps - 1) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int q = GV == 1 ? 0 : j;
-        const int b4 = r == 0 ? 0 : r - 1;
-        const float before = r == 0 ? in[j] : fmaf(P[b4][q], in[j], hl[b4][j]);
-        const float delta = d[j] + cin[j];
-        o[j] = na[r][q] * delta;
-        cin[j] = a[r][q] * delta;
-        const float gg = cin[j] * na[r][q] * (before - uv[j]);
-        if (kShared) gsum += gg;
-        else og[q] = gg;
+        for (int j = 0; j < V; ++j) before[j] = start[j];
       }
+      spread(av, a[r]);
+      spread(nav, na[r]);
+      vec_add(d[r], d[r], cin);  // delta
+      vec_mul(o, nav, d[r]);
+      vec_mul(cin, av, d[r]);
+      vec_sub(before, before, uv);
       if constexpr (kShared) {
+        vec_mul(gg, d[r], before);
+        float gsum = gg[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) gsum += gg[j];
+        gsum *= a[r][0] * na[r][0];
         // a channel's T features sit in m neighbouring lanes
         float sum = gsum;
         for (int k = 1; k < p.m; ++k) sum += __shfl_down_sync(0xffffffffu, gsum, k);
         og[0] = sum;
+      } else {
+        vec_mul(gg, o, before);
+        vec_mul(gg, gg, av);
+#pragma unroll
+        for (int j = 0; j < V; ++j) og[GV == 1 ? 0 : j] = gg[j];
       }
-      if (row) {
+      if (rows_of.has(r) && at.live) {
         Pack<Ty, V> k;
         k.pack(o);
-        k.store(du + (s + l0 + r) * p.F + f);
+        k.store(pdu + static_cast<int64_t>(r) * p.F);
         Pack<Ty, GV> kg;
         kg.pack(og);
-        if (!kShared || tx % p.m == 0) kg.store(dg + (s + l0 + r) * p.FG + gf);
+        if (!kShared || at.tx % p.m == 0) kg.store(pdg + static_cast<int64_t>(r) * p.FG);
       }
     }
+  };
+  for (int i = 0; i < steps; ++i, pdu -= step, pdg -= gstep) {
+    async_wait_tile<kStages>();
+    fu.take(i % kStages);
+    fd.take(i % kStages);
+    fh.take(i % kStages);
+    fg.take(i % kStages);
+    issue_x(i + fu.kAhead);
+    issue_g(i + fg.kAhead);
+    async_commit();
+    if (i < part) tile(i, ScanRows<false>{have()});
+    else tile(i, ScanRows<true>{R});
   }
-  scan_zero_rest<Ty, V, TY>(p, b, rank, ty, s, e, du, p.F, f, live);
-  scan_zero_rest<Ty, GV, TY>(p, b, rank, ty, s, e, dg, p.FG, gf,
-                             live && (!kShared || tx % p.m == 0));
-  if (dh0 != nullptr && live && rank == 0 && ty == 0)
-    store_state<V>(dh0 + static_cast<int64_t>(b) * p.F + f, carry);
+  if (dh0 != nullptr && at.live && at.seg == 0 && J::last()) store_state<V>(dh0 + state, carry);
+  scan_zero_rest<Ty, V, TY>(p, at.b, at.seg, at.nseg, at.ty, at.s, at.e, du, p.F, at.f, at.live);
+  scan_zero_rest<Ty, GV, TY>(p, at.b, at.seg, at.nseg, at.ty, at.s, at.e, dg, p.FG, at.gf,
+                             at.live && (!kShared || at.tx % p.m == 0));
 }
 
 // One token of each of B sequences: h = a h + (1 - a) u on the fp32 states in
@@ -482,7 +795,8 @@ scan_step_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, float *__re
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
     float a, na;
-    scan_gate<Ty>(widen(g[i / T]), a, na);  // T = 1 for a gate per (c, t)
+    // T = 1 for a gate per (c, t)
+    sigmoid_pair<sizeof(Ty) == 2>(widen(g[i / T]), a, na);
     const float v = fmaf(a, state[i], na * widen(u[i]));
     state[i] = v;
     h[i] = narrow<Ty>(v);

@@ -74,4 +74,91 @@ struct Pack {
   __device__ __forceinline__ void zero() { w = decltype(w){}; }
 };
 
+// fp32 vectors of V values, two to an instruction where V allows (sm_100's paired
+// fp32 pipe): the same roundings as one by one.
+template <int V>
+__device__ __forceinline__ void vec_fma(float (&d)[V], const float (&a)[V], const float (&b)[V],
+                                        const float (&c)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2)
+      asm("{.reg .b64 a, b, c, d;\n\t"
+          "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+          "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
+          : "=f"(d[j]), "=f"(d[j + 1])
+          : "f"(a[j]), "f"(a[j + 1]), "f"(b[j]), "f"(b[j + 1]), "f"(c[j]), "f"(c[j + 1]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = fmaf(a[j], b[j], c[j]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void vec_mul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2)
+      asm("{.reg .b64 a, b, d;\n\t"
+          "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+          "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
+          : "=f"(d[j]), "=f"(d[j + 1])
+          : "f"(a[j]), "f"(a[j + 1]), "f"(b[j]), "f"(b[j + 1]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = a[j] * b[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void vec_add(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2)
+      asm("{.reg .b64 a, b, d;\n\t"
+          "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+          "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
+          : "=f"(d[j]), "=f"(d[j + 1])
+          : "f"(a[j]), "f"(a[j + 1]), "f"(b[j]), "f"(b[j + 1]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = a[j] + b[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void vec_sub(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+  float n[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) n[j] = -1.f;
+  vec_fma(d, b, n, a);
+}
+// Gate values of a row spread over its V features: themselves, or the one.
+template <int V, int GV>
+__device__ __forceinline__ void spread(float (&d)[V], const float (&g)[GV]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) d[j] = g[GV == 1 ? 0 : j];
+}
+
+__device__ __forceinline__ float ex2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sigma(v) and sigma(-v), each to full relative precision.  kFast (fp16
+// outputs): the hardware's exponential and reciprocal, off by 2^-21 or so, far
+// below the outputs' rounding, subnormals flushed.
+template <bool kFast>
+__device__ __forceinline__ void sigmoid_pair(float v, float &p, float &q) {
+  const float e = kFast ? ex2_fast(-kLog2e * fabsf(v)) : expf(-fabsf(v));
+  const float big = kFast ? rcp_fast(1.f + e) : 1.f / (1.f + e);
+  const float small = e * big;
+  p = v >= 0.f ? big : small;
+  q = v >= 0.f ? small : big;
+}
+
 }  // namespace feql

@@ -17,7 +17,8 @@ from . import (FEQL_ACT_NONE, FEQL_FP16, FEQL_FP16_SIMT, FEQL_FP32, feql_backwar
                feql_p4m_backward_act, feql_p4m_backward_act_workspace_bytes, feql_p4m_backward_dw,
                feql_p4m_backward_dw_workspace_bytes, feql_p4m_backward_dx, feql_p4m_forward,
                feql_p4m_forward_act, feql_p4m_weight_fft, feql_p4m_weight_fft_bytes,
-               feql_scan_backward, feql_scan_forward, feql_scan_save_bytes, feql_scan_step,
+               feql_scan_backward, feql_scan_forward, feql_scan_step,
+               feql_scan_workspace_bytes,
                feql_weight_fft, feql_weight_fft_bytes)
 
 
@@ -386,7 +387,8 @@ def scan_forward(u: torch.Tensor, g: torch.Tensor, h0=None, offsets=None, save: 
     Dense: u (B, L, C, T).  Packed: u (N, C, T) and ``offsets`` (B + 1,) int32,
     sequence b in rows offsets[b]..offsets[b + 1].  g has u's shape, or lacks its
     last axis (one gate per channel).  h0 and hN are (B, C, T) fp32 states;
-    ``saved`` is what scan_backward takes (None without ``save``).
+    ``saved`` is what scan_backward takes (h and h0, which it reads; None without
+    ``save``).
     """
     B, N, C, T, shared = _scan_sizes(u, g, offsets)
     mode = _mode(u)
@@ -398,16 +400,14 @@ def scan_forward(u: torch.Tensor, g: torch.Tensor, h0=None, offsets=None, save: 
         offsets = _take(offsets, "offsets", (B + 1,), torch.int32, dev)
         h = torch.empty_like(u)
         hN = torch.empty((B, C, T), dtype=torch.float32, device=dev)
-        saved = None
-        if save:
-            nbytes = feql_scan_save_bytes(B, N, C, T, shared, mode)
-            saved = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        feql_scan_forward(u, g, h0, offsets, h, hN, saved, B, N, C, T, shared, mode)
-    return h, hN, saved
+        nbytes = feql_scan_workspace_bytes(B, N, C, T, shared, offsets is not None, mode)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        feql_scan_forward(u, g, h0, offsets, h, hN, ws, ws.numel(), B, N, C, T, shared, mode)
+    return h, hN, ((h, h0) if save else None)
 
 
-def scan_backward(dh: torch.Tensor, u: torch.Tensor, g: torch.Tensor, saved: torch.Tensor,
-                  dhN=None, offsets=None):
+def scan_backward(dh: torch.Tensor, u: torch.Tensor, g: torch.Tensor, saved, dhN=None,
+                  offsets=None):
     """du, dg, dh0 of scan_forward on the same u, g and offsets."""
     B, N, C, T, shared = _scan_sizes(u, g, offsets)
     mode = _mode(u)
@@ -418,11 +418,14 @@ def scan_backward(dh: torch.Tensor, u: torch.Tensor, g: torch.Tensor, saved: tor
         dh = _take(dh, "dh", u.shape, u.dtype, dev)
         dhN = _take(dhN, "dhN", (B, C, T), torch.float32, dev)
         offsets = _take(offsets, "offsets", (B + 1,), torch.int32, dev)
-        nbytes = max(feql_scan_save_bytes(B, N, C, T, shared, mode), 16)
-        saved = _take(saved, "saved", (nbytes,), torch.uint8, dev)
+        h = _take(saved[0], "h", u.shape, u.dtype, dev)
+        h0 = _take(saved[1], "h0", (B, C, T), torch.float32, dev)
         du, dg = torch.empty_like(u), torch.empty_like(g)
         dh0 = torch.empty((B, C, T), dtype=torch.float32, device=dev)
-        feql_scan_backward(dh, u, g, saved, dhN, offsets, du, dg, dh0, B, N, C, T, shared, mode)
+        nbytes = feql_scan_workspace_bytes(B, N, C, T, shared, offsets is not None, mode)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        feql_scan_backward(dh, u, g, h, h0, dhN, offsets, du, dg, dh0, ws, ws.numel(), B, N, C, T,
+                           shared, mode)
     return du, dg, dh0
 
 

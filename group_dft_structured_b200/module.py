@@ -309,18 +309,18 @@ class EqScanFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, u, g, h0, offsets):
-        h, hN, saved = _L.scan_forward(u, g, h0, offsets, save=any(ctx.needs_input_grad[:3]))
-        ctx.save_for_backward(u, g, saved, offsets)
+        h, hN, _ = _L.scan_forward(u, g, h0, offsets, save=False)
+        ctx.save_for_backward(u, g, h, h0, offsets)
         ctx.set_materialize_grads(False)
         return h, hN
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dh, dhN):
-        u, g, saved, offsets = ctx.saved_tensors
+        u, g, h, h0, offsets = ctx.saved_tensors
         if dh is None:
             dh = torch.zeros_like(u)
-        du, dg, dh0 = _L.scan_backward(dh, u, g, saved, dhN, offsets)
+        du, dg, dh0 = _L.scan_backward(dh, u, g, (h, h0), dhN, offsets)
         need = ctx.needs_input_grad
         return (du if need[0] else None, dg if need[1] else None, dh0 if need[2] else None, None)
 

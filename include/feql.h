@@ -343,24 +343,25 @@ int feql_norm_backward(const void *x, const void *dy, const float *stats, const 
  *   u, h  : device [N][C][T]
  *   h0    : device fp32 [B][C][T] or NULL (zero)   hN : the same, the states
  *           after the last rows (h0 for an empty sequence), or NULL
- *   save  : device, feql_scan_save_bytes(...) bytes for the backward pass, or
- *           NULL.  Opaque; belongs to these B, N, C, T, shared, dtype, offsets
- *           and device.
+ *   ws    : device scratch of ws_bytes >= feql_scan_workspace_bytes(...) (packed: 1
+ *           with offsets, else 0), here and in the backward pass
  * States are fp32 throughout. */
-size_t feql_scan_save_bytes(int64_t B, int64_t N, int C, int T, int shared, int dtype);
+size_t feql_scan_workspace_bytes(int64_t B, int64_t N, int C, int T, int shared, int packed,
+                                 int dtype);
 int feql_scan_forward(const void *u, const void *g, const float *h0, const int32_t *offsets,
-                      void *h, float *hN, void *save, int64_t B, int64_t N, int C, int T,
-                      int shared, int dtype, feql_stream stream);
+                      void *h, float *hN, void *ws, size_t ws_bytes, int64_t B, int64_t N, int C,
+                      int T, int shared, int dtype, feql_stream stream);
 
 /* Gradients of <dh, h> + <dhN, hN>:
  *   delta_l = dh_l + a_{l+1} delta_{l+1} (+ dhN at the last row),
  *   du = (1 - a) delta,  dg = delta (h_{l-1} - u) a (1 - a) (summed over T for
  *   shared gates),  dh0 = a_0 delta_0 (dhN for an empty sequence).
- *   dhN : device fp32 [B][C][T] or NULL (zero)   dh0 : the same, or NULL */
-int feql_scan_backward(const void *dh, const void *u, const void *g, const void *save,
-                       const float *dhN, const int32_t *offsets, void *du, void *dg, float *dh0,
-                       int64_t B, int64_t N, int C, int T, int shared, int dtype,
-                       feql_stream stream);
+ *   h, h0 : the forward's output and initial states (NULL as there)
+ *   dhN   : device fp32 [B][C][T] or NULL (zero)   dh0 : the same, or NULL */
+int feql_scan_backward(const void *dh, const void *u, const void *g, const void *h,
+                       const float *h0, const float *dhN, const int32_t *offsets, void *du,
+                       void *dg, float *dh0, void *ws, size_t ws_bytes, int64_t B, int64_t N,
+                       int C, int T, int shared, int dtype, feql_stream stream);
 
 /* One token of each of B sequences: state (fp32 [B][C][T]) becomes
  * a state + (1 - a) u in place, h [B][C][T] its value in the data type. */

@@ -44,19 +44,19 @@ def test_norm_refusals(lib):
 
 def test_scan_refusals(lib):
     f = lib.feql_scan_forward
-    assert f(None, P, None, None, P, None, None, 2, 8, 4, 4, 0, FP16, None) == INV
-    assert f(P, P, None, None, None, None, None, 2, 8, 4, 4, 0, FP16, None) == INV
-    assert f(P, P, None, None, P, None, None, 3, 8, 4, 4, 0, FP16, None) == INV  # 8 rows, 3 sequences
-    assert f(P, P, None, None, P, None, None, 0, 8, 4, 4, 0, FP16, None) == INV
-    assert f(P, P, None, None, P, None, None, -1, 8, 4, 4, 0, FP16, None) == INV
-    assert f(P, P, None, None, P, None, None, 2, 8, 4, 17, 0, FP16, None) == UNS
-    assert f(P, P, P + 4, None, P, None, None, 2, 8, 4, 4, 0, FP16, None) == INV
-    assert f(P, P, None, P + 4, P, None, None, 2, 8, 4, 4, 0, FP16, None) == INV
-    assert f(P, P, None, None, P, None, None, 2, 8, 4, 4, 0, -1, None) == INV
-    assert f(None, None, None, None, None, None, None, 0, 0, 4, 4, 0, FP16, None) == F.FEQL_OK
+    assert f(None, P, None, None, P, None, P, 1 << 30, 2, 8, 4, 4, 0, FP16, None) == INV
+    assert f(P, P, None, None, None, None, P, 1 << 30, 2, 8, 4, 4, 0, FP16, None) == INV
+    assert f(P, P, None, None, P, None, P, 1 << 30, 3, 8, 4, 4, 0, FP16, None) == INV  # 8 rows, 3 sequences
+    assert f(P, P, None, None, P, None, P, 1 << 30, 0, 8, 4, 4, 0, FP16, None) == INV
+    assert f(P, P, None, None, P, None, P, 1 << 30, -1, 8, 4, 4, 0, FP16, None) == INV
+    assert f(P, P, None, None, P, None, P, 1 << 30, 2, 8, 4, 17, 0, FP16, None) == UNS
+    assert f(P, P, P + 4, None, P, None, P, 1 << 30, 2, 8, 4, 4, 0, FP16, None) == INV
+    assert f(P, P, None, P + 4, P, None, P, 1 << 30, 2, 8, 4, 4, 0, FP16, None) == INV
+    assert f(P, P, None, None, P, None, P, 1 << 30, 2, 8, 4, 4, 0, -1, None) == INV
+    assert f(None, None, None, None, None, None, P, 1 << 30, 0, 0, 4, 4, 0, FP16, None) == F.FEQL_OK
     b = lib.feql_scan_backward
-    assert b(P, P, P, None, None, None, P, P, None, 2, 8, 4, 4, 0, FP16, None) == INV
-    assert b(P, P, P, P, None, None, P, None, None, 2, 8, 4, 4, 0, FP16, None) == INV
+    assert b(P, P, P, None, None, None, None, P, P, None, P, 1 << 30, 2, 8, 4, 4, 0, FP16, None) == INV
+    assert b(P, P, P, P, None, None, None, P, None, None, P, 1 << 30, 2, 8, 4, 4, 0, FP16, None) == INV
     s = lib.feql_scan_step
     assert s(P, P, None, P, 2, 4, 4, 0, FP16, None) == INV
     assert s(P, P, P, P, 2, 4, 17, 0, FP16, None) == UNS

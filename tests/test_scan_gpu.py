@@ -9,6 +9,7 @@ parts of both signs may cancel: so roundings count against the sum of the parts'
 sizes, M_l = a M_{l-1} + (1 - a) |u|, not against |h|.  The error then obeys the
 recurrence itself, E_l = a E_{l-1} + e M_l, which the tests run in float64; the
 gradient's the same from the other end, with M_l = |dh_l| + a_{l+1} M_{l+1}.
+The gates' gradient takes h_{l-1} from the forward's output: half a step of it off.
 Outputs add half a step of their type.
 """
 
@@ -98,6 +99,7 @@ def check(u, g, dh, h0, dhN, off, out):
         return
     within(du, rdu, half * np.abs(rdu) + tiny + na * (Ed + e * np.abs(delta)), "du")
     diff = np.abs(before - U64)
+    Eb = Eb + half * np.abs(before) + tiny
     Eg = a * na * (np.abs(delta) * (Eb + U * (np.abs(before) + np.abs(U64))) + Ed * diff +
                    (2 * e + 4 * U) * np.abs(delta) * diff)
     if g.ndim < u.ndim:
@@ -125,7 +127,7 @@ DENSE = [  # B, L, C, T
     (1, 1, 1, 1), (1, 2, 3, 1), (3, 5, 2, 2), (2, 31, 5, 3), (4, 64, 24, 4), (2, 257, 7, 4),
     (5, 49, 6, 6), (1, 300, 3, 5), (2, 700, 4, 12), (3, 130, 2, 16), (1, 129, 9, 7),
     (300, 9, 24, 4), (2, 2049, 8, 4), (1, 5000, 6, 4), (1, 4097, 5, 2), (1, 3001, 3, 3),
-    (2, 1023, 2, 15), (1, 2500, 1, 8), (700, 3, 16, 8), (1, 40, 40, 13),
+    (2, 1023, 2, 15), (1, 2500, 1, 8), (700, 3, 16, 8), (1, 40, 40, 13), (1, 34001, 2, 4),
 ]
 
 
@@ -141,6 +143,8 @@ def test_dense(B, L_, C, T, shared, dt):
 PACKED = [
     ([0, 5, 5, 40, 41, 300], 300), ([0, 0, 0, 17], 17), ([3, 3, 50, 700, 700], 731),
     ([0, 0], 6), ([0, 1500, 1502, 1502, 2100], 2100), ([0, 3000], 3100),
+    ([0, 1, 9000, 9000, 9100], 9107),
+    (list(range(0, 200)) + [8000] + [8000 + i for i in range(60)], 8070),
     (list(range(0, 401)) + [900], 902),
 ]
 
@@ -287,7 +291,7 @@ def test_refusals():
         L.scan_forward(u, u, offsets=off)
     h, hN, saved = L.scan_forward(u, u)
     with pytest.raises(ValueError):
-        L.scan_backward(u, u, u, saved[:-4])
+        L.scan_backward(u, u, u, (h[:, :4], None))
     with pytest.raises(ValueError):
         L.scan_backward(u[:, :4], u, u, saved)
     state = torch.zeros(6, 2, 4, device="cuda").permute(1, 0, 2)
