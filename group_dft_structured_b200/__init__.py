@@ -127,10 +127,23 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """torch's current stream of the current device as a raw cudaStream_t."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        # without the Stream object in between, where torch offers it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -266,10 +279,10 @@ def feql_mlp_forward(x, What, b1, b2, y, N: int, C: int, H: int, Co: int, dtype:
                                    dtype, _stream(stream)), "feql_mlp_forward")
 
 
-def feql_forward_act(x, What, b, res, y, z, N: int, C: int, D: int, act: int,
+def feql_forward_act(x, What, b, res, y, slope, N: int, C: int, D: int, act: int,
                      dtype: int, stream=None) -> None:
     _check(load().feql_forward_act(_ptr(x), _ptr(What), _ptr(b), _ptr(res), _ptr(y),
-                                   _ptr(z), N, C, D, act, dtype, _stream(stream)),
+                                   _ptr(slope), N, C, D, act, dtype, _stream(stream)),
            "feql_forward_act")
 
 
@@ -278,17 +291,17 @@ def feql_backward_act_workspace_bytes(N: int, C: int, D: int, act: int,
     return int(load().feql_backward_act_workspace_bytes(N, C, D, act, dtype))
 
 
-def feql_backward_act(x, dy, z, What, dx, dW, db, ws, ws_bytes: int, N: int, C: int,
+def feql_backward_act(x, dy, slope, What, dx, dW, db, ws, ws_bytes: int, N: int, C: int,
                       D: int, act: int, dtype: int, stream=None) -> None:
-    _check(load().feql_backward_act(_ptr(x), _ptr(dy), _ptr(z), _ptr(What), _ptr(dx),
+    _check(load().feql_backward_act(_ptr(x), _ptr(dy), _ptr(slope), _ptr(What), _ptr(dx),
                                     _ptr(dW), _ptr(db), _ptr(ws), ws_bytes, N, C, D,
                                     act, dtype, _stream(stream)), "feql_backward_act")
 
 
-def feql_ct_forward_act(T: int, x, What, b, res, y, z, N: int, C: int, D: int, act: int,
+def feql_ct_forward_act(T: int, x, What, b, res, y, slope, N: int, C: int, D: int, act: int,
                         dtype: int, stream=None) -> None:
     _check(load().feql_ct_forward_act(T, _ptr(x), _ptr(What), _ptr(b), _ptr(res), _ptr(y),
-                                      _ptr(z), N, C, D, act, dtype, _stream(stream)),
+                                      _ptr(slope), N, C, D, act, dtype, _stream(stream)),
            "feql_ct_forward_act")
 
 
@@ -297,17 +310,17 @@ def feql_ct_backward_act_workspace_bytes(T: int, N: int, C: int, D: int, act: in
     return int(load().feql_ct_backward_act_workspace_bytes(T, N, C, D, act, dtype))
 
 
-def feql_ct_backward_act(T: int, x, dy, z, What, dx, dW, db, ws, ws_bytes: int, N: int, C: int,
+def feql_ct_backward_act(T: int, x, dy, slope, What, dx, dW, db, ws, ws_bytes: int, N: int, C: int,
                          D: int, act: int, dtype: int, stream=None) -> None:
-    _check(load().feql_ct_backward_act(T, _ptr(x), _ptr(dy), _ptr(z), _ptr(What), _ptr(dx),
+    _check(load().feql_ct_backward_act(T, _ptr(x), _ptr(dy), _ptr(slope), _ptr(What), _ptr(dx),
                                        _ptr(dW), _ptr(db), _ptr(ws), ws_bytes, N, C, D,
                                        act, dtype, _stream(stream)), "feql_ct_backward_act")
 
 
-def feql_p4m_forward_act(x, What, b, res, y, z, N: int, C: int, D: int, act: int,
+def feql_p4m_forward_act(x, What, b, res, y, slope, N: int, C: int, D: int, act: int,
                          dtype: int, stream=None) -> None:
     _check(load().feql_p4m_forward_act(_ptr(x), _ptr(What), _ptr(b), _ptr(res), _ptr(y),
-                                       _ptr(z), N, C, D, act, dtype, _stream(stream)),
+                                       _ptr(slope), N, C, D, act, dtype, _stream(stream)),
            "feql_p4m_forward_act")
 
 
@@ -316,9 +329,9 @@ def feql_p4m_backward_act_workspace_bytes(N: int, C: int, D: int, act: int,
     return int(load().feql_p4m_backward_act_workspace_bytes(N, C, D, act, dtype))
 
 
-def feql_p4m_backward_act(x, dy, z, What, dx, dW, db, ws, ws_bytes: int, N: int, C: int,
+def feql_p4m_backward_act(x, dy, slope, What, dx, dW, db, ws, ws_bytes: int, N: int, C: int,
                           D: int, act: int, dtype: int, stream=None) -> None:
-    _check(load().feql_p4m_backward_act(_ptr(x), _ptr(dy), _ptr(z), _ptr(What), _ptr(dx),
+    _check(load().feql_p4m_backward_act(_ptr(x), _ptr(dy), _ptr(slope), _ptr(What), _ptr(dx),
                                         _ptr(dW), _ptr(db), _ptr(ws), ws_bytes, N, C, D,
                                         act, dtype, _stream(stream)), "feql_p4m_backward_act")
 

@@ -329,8 +329,9 @@ int launch_tc_dw(TcDwParams p, const void *x, const void *dy, __half *dW, __half
 
 // Fused backward plan; false when the shape is outside the fused kernel's
 // range (then feql_backward runs the dX and dW kernels one after the other).
+// act: with the slope boxes of an activation.
 bool make_tc_bwd_plan(int64_t N, int C, int D, const WhatLayout &L, const DeviceInfo &dev,
-                      TcBwdParams &p) {
+                      TcBwdParams &p, bool act = false) {
   if (N <= 0 || L.dx.nD != 1) return false;
   p.N = N;
   p.C = C;
@@ -352,6 +353,7 @@ bool make_tc_bwd_plan(int64_t N, int C, int D, const WhatLayout &L, const Device
   if (s > cdiv(N, kBwTB)) s = cdiv(N, kBwTB);
   p.split_len = align_up(cdiv(N, s), kBwTB);
   p.splits = static_cast<int>(cdiv(N, p.split_len));
+  p.slope_bytes = act ? p.nqd * kBwBox : 0;
   const int budget = dev.smem_optin - 1024;
   p.stages = 4;
   while (p.stages > 2 && tc_bwd_smem(p).total > budget) --p.stages;
@@ -365,7 +367,8 @@ bool make_tc_bwd_plan(int64_t N, int C, int D, const WhatLayout &L, const Device
 }
 
 int launch_tc_bwd(TcBwdParams p, const void *x, const void *dy, const uint8_t *wt, __half *dx,
-                  __half *dW, __half *db, float *ws, const DeviceInfo &dev, cudaStream_t stream) {
+                  __half *dW, __half *db, float *ws, const DeviceInfo &dev, cudaStream_t stream,
+                  const void *slope = nullptr) {
   if (dev.cc_major != 10) return FEQL_ERR_UNSUPPORTED;
   p.wt = wt;
   p.dx = dx;
@@ -383,12 +386,21 @@ int launch_tc_bwd(TcBwdParams p, const void *x, const void *dy, const uint8_t *w
                                   p.nqc) == FEQL_OK;
   if (!p.stack_x) st = make_tmap_f16(&tm_x, x, p.N, static_cast<int64_t>(p.C) * kT, kBwTB);
   if (st != FEQL_OK) return st;
+  CUtensorMap tm_s = tm_dy;  // slopes as dy
   // db from the dW bin-0 MMA when the last x box has a padding channel
-  auto kernel = (p.C % 16) != 0 ? tc_bwd_kernel<true> : tc_bwd_kernel<false>;
+  const bool dbcol = (p.C % 16) != 0;
+  auto kernel = dbcol ? tc_bwd_kernel<true> : tc_bwd_kernel<false>;
+  if (slope != nullptr) {
+    const int64_t row = static_cast<int64_t>(p.D) * kT;
+    st = p.stack_dy ? make_tmap_f16_boxes(&tm_s, slope, p.N, row, kBwTB, p.nqd)
+                    : make_tmap_f16(&tm_s, slope, p.N, row, kBwTB);
+    if (st != FEQL_OK) return st;
+    kernel = dbcol ? tc_bwd_kernel<true, true> : tc_bwd_kernel<false, true>;
+  }
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return FEQL_ERR_CUDA;
-  kernel<<<p.splits, kBwThreads, smem, stream>>>(tm_dy, tm_x, p);
+  kernel<<<p.splits, kBwThreads, smem, stream>>>(tm_dy, tm_x, tm_s, p);
   if (cudaGetLastError() != cudaSuccess) return FEQL_ERR_CUDA;
   // the split reduce as the kernel's programmatic dependent (see tc_dw.cuh)
   {
@@ -836,13 +848,13 @@ int feql_backward_dw(const void *x, const void *dy, void *dW, void *db, void *ws
     simt_dw_partial_kernel<__half><<<grid, kSimtThreads, 0, s>>>(
         static_cast<const __half *>(x), static_cast<const __half *>(dy), wsf, wsdb, N, C, D,
         q.split_len);
-    dw_reduce_kernel<__half><<<grid_for(red, 256, dev.sms), 256, 0, s>>>(
+    dw_reduce_kernel<__half><<<grid_for(red, 64, dev.sms), 64, 0, s>>>(
         wsf, wsdb, static_cast<__half *>(dW), static_cast<__half *>(db), q.splits, C, D);
   } else {
     simt_dw_partial_kernel<float><<<grid, kSimtThreads, 0, s>>>(
         static_cast<const float *>(x), static_cast<const float *>(dy), wsf, wsdb, N, C, D,
         q.split_len);
-    dw_reduce_kernel<float><<<grid_for(red, 256, dev.sms), 256, 0, s>>>(
+    dw_reduce_kernel<float><<<grid_for(red, 64, dev.sms), 64, 0, s>>>(
         wsf, wsdb, static_cast<float *>(dW), static_cast<float *>(db), q.splits, C, D);
   }
   return launch_status();
@@ -1007,13 +1019,13 @@ static int act_check(GroupKind G, int64_t N, int C, int D, int act, int dtype) {
 }
 
 static int forward_act(GroupKind G, const void *x, const void *What, const void *b, const void *res,
-                       void *y, void *z, int64_t N, int C, int D, int act, int dtype,
+                       void *y, void *slope, int64_t N, int C, int D, int act, int dtype,
                        feql_stream stream) {
   const int st = act_check(G, N, C, D, act, dtype);
   if (st != FEQL_OK) return st;
-  if (!aligned16(res) || !aligned16(z)) return FEQL_ERR_INVALID_ARG;
-  const Epilogue e = make_epilogue(act, res, z);
-  const Epilogue *ep = act == FEQL_ACT_NONE && res == nullptr && z == nullptr ? nullptr : &e;
+  if (!aligned16(res) || !aligned16(slope)) return FEQL_ERR_INVALID_ARG;
+  const Epilogue e = make_epilogue(act, res, slope);
+  const Epilogue *ep = act == FEQL_ACT_NONE && res == nullptr && slope == nullptr ? nullptr : &e;
   if (G.p4m) return g8_pass<Dihedral4>(x, What, b, y, N, C, D, stream, 0, ep);
   if (G.T == kT) return pass_common(x, What, b, y, N, C, D, dtype, stream, 0, ep);
   return ct_pass(G.T, x, What, b, y, N, C, D, dtype, stream, 0, ep);
@@ -1042,17 +1054,17 @@ static size_t backward_act_workspace_bytes(GroupKind G, int64_t N, int C, int D,
   return w.total > 16 ? w.total : 16;
 }
 
-static int backward_act(GroupKind G, const void *x, const void *dy, const void *z,
+static int backward_act(GroupKind G, const void *x, const void *dy, const void *slope,
                         const void *What, void *dx, void *dW, void *db, void *ws, size_t ws_bytes,
                         int64_t N, int C, int D, int act, int dtype, feql_stream stream) {
   int st = act_check(G, N, C, D, act, dtype);
   if (st != FEQL_OK) return st;
   if (ws == nullptr || (dx == nullptr && dW == nullptr) || (dW == nullptr && db != nullptr))
     return FEQL_ERR_INVALID_ARG;
-  if (N > 0 && (dy == nullptr || (act != FEQL_ACT_NONE && z == nullptr) ||
+  if (N > 0 && (dy == nullptr || (act != FEQL_ACT_NONE && slope == nullptr) ||
                 (dx != nullptr && What == nullptr) || (dW != nullptr && x == nullptr)))
     return FEQL_ERR_INVALID_ARG;
-  const void *all[] = {x, dy, z, What, dx, dW, db, ws};
+  const void *all[] = {x, dy, slope, What, dx, dW, db, ws};
   for (const void *p : all)
     if (!aligned16(p)) return FEQL_ERR_INVALID_ARG;
   DeviceInfo dev;
@@ -1062,18 +1074,26 @@ static int backward_act(GroupKind G, const void *x, const void *dy, const void *
   if (ws_bytes < w.total) return FEQL_ERR_INVALID_ARG;
   const void *dz = dy;
   if (act != FEQL_ACT_NONE && N > 0) {
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // where the layer's fused backward holds the slopes too, dz stays on chip
+    if (!G.p4m && G.T == kT && dx != nullptr && dW != nullptr && is_tc(resolve(dtype, C, D))) {
+      const WhatLayout L = make_what_layout(C, D, kWhatF16);
+      TcBwdParams p;
+      if (make_tc_bwd_plan(N, C, D, L, dev, p, true))
+        return launch_tc_bwd(p, x, dy, static_cast<const uint8_t *>(What) + L.off_dx,
+                             static_cast<__half *>(dx), static_cast<__half *>(dW),
+                             static_cast<__half *>(db), static_cast<float *>(ws), dev, s, slope);
+    }
     const int64_t n = N * D * G.T;
     void *to = static_cast<uint8_t *>(ws) + w.dz;
-    const Epilogue e = make_epilogue(act, nullptr, nullptr);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (is_half(dtype))
-      act_bwd_kernel<__half, 8><<<grid_for(n / 8 + 1, 256, dev.sms), 256, 0, s>>>(
-          static_cast<const __half *>(dy), static_cast<const __half *>(z),
-          static_cast<__half *>(to), n, e);
+      act_bwd_kernel<__half><<<grid_for(n / 8 + 1, 256, dev.sms), 256, 0, s>>>(
+          static_cast<const __half *>(dy), static_cast<const __half *>(slope),
+          static_cast<__half *>(to), n);
     else
-      act_bwd_kernel<float, 4><<<grid_for(n / 4 + 1, 256, dev.sms), 256, 0, s>>>(
-          static_cast<const float *>(dy), static_cast<const float *>(z), static_cast<float *>(to),
-          n, e);
+      act_bwd_kernel<float><<<grid_for(n / 4 + 1, 256, dev.sms), 256, 0, s>>>(
+          static_cast<const float *>(dy), static_cast<const float *>(slope),
+          static_cast<float *>(to), n);
     st = launch_status();
     if (st != FEQL_OK) return st;
     dz = to;
@@ -1091,52 +1111,52 @@ static int backward_act(GroupKind G, const void *x, const void *dy, const void *
 }
 
 int feql_forward_act(const void *x, const void *What, const void *b, const void *res, void *y,
-                     void *z, int64_t N, int C, int D, int act, int dtype, feql_stream stream) {
-  return forward_act({false, kT}, x, What, b, res, y, z, N, C, D, act, dtype, stream);
+                     void *slope, int64_t N, int C, int D, int act, int dtype, feql_stream stream) {
+  return forward_act({false, kT}, x, What, b, res, y, slope, N, C, D, act, dtype, stream);
 }
 
 size_t feql_backward_act_workspace_bytes(int64_t N, int C, int D, int act, int dtype) {
   return backward_act_workspace_bytes({false, kT}, N, C, D, act, dtype);
 }
 
-int feql_backward_act(const void *x, const void *dy, const void *z, const void *What, void *dx,
+int feql_backward_act(const void *x, const void *dy, const void *slope, const void *What, void *dx,
                       void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C, int D,
                       int act, int dtype, feql_stream stream) {
-  return backward_act({false, kT}, x, dy, z, What, dx, dW, db, ws, ws_bytes, N, C, D, act, dtype,
-                      stream);
+  return backward_act({false, kT}, x, dy, slope, What, dx, dW, db, ws, ws_bytes, N, C, D, act,
+                      dtype, stream);
 }
 
 int feql_ct_forward_act(int T, const void *x, const void *What, const void *b, const void *res,
-                        void *y, void *z, int64_t N, int C, int D, int act, int dtype,
+                        void *y, void *slope, int64_t N, int C, int D, int act, int dtype,
                         feql_stream stream) {
-  return forward_act({false, T}, x, What, b, res, y, z, N, C, D, act, dtype, stream);
+  return forward_act({false, T}, x, What, b, res, y, slope, N, C, D, act, dtype, stream);
 }
 
 size_t feql_ct_backward_act_workspace_bytes(int T, int64_t N, int C, int D, int act, int dtype) {
   return backward_act_workspace_bytes({false, T}, N, C, D, act, dtype);
 }
 
-int feql_ct_backward_act(int T, const void *x, const void *dy, const void *z, const void *What,
+int feql_ct_backward_act(int T, const void *x, const void *dy, const void *slope, const void *What,
                          void *dx, void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C,
                          int D, int act, int dtype, feql_stream stream) {
-  return backward_act({false, T}, x, dy, z, What, dx, dW, db, ws, ws_bytes, N, C, D, act, dtype,
+  return backward_act({false, T}, x, dy, slope, What, dx, dW, db, ws, ws_bytes, N, C, D, act, dtype,
                       stream);
 }
 
 int feql_p4m_forward_act(const void *x, const void *What, const void *b, const void *res, void *y,
-                         void *z, int64_t N, int C, int D, int act, int dtype,
+                         void *slope, int64_t N, int C, int D, int act, int dtype,
                          feql_stream stream) {
-  return forward_act({true, 8}, x, What, b, res, y, z, N, C, D, act, dtype, stream);
+  return forward_act({true, 8}, x, What, b, res, y, slope, N, C, D, act, dtype, stream);
 }
 
 size_t feql_p4m_backward_act_workspace_bytes(int64_t N, int C, int D, int act, int dtype) {
   return backward_act_workspace_bytes({true, 8}, N, C, D, act, dtype);
 }
 
-int feql_p4m_backward_act(const void *x, const void *dy, const void *z, const void *What, void *dx,
-                          void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C, int D,
+int feql_p4m_backward_act(const void *x, const void *dy, const void *slope, const void *What,
+                          void *dx, void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C, int D,
                           int act, int dtype, feql_stream stream) {
-  return backward_act({true, 8}, x, dy, z, What, dx, dW, db, ws, ws_bytes, N, C, D, act, dtype,
+  return backward_act({true, 8}, x, dy, slope, What, dx, dW, db, ws, ws_bytes, N, C, D, act, dtype,
                       stream);
 }
 

@@ -30,6 +30,17 @@ struct NormPlan {
   NormShape s;
 };
 
+// The variants of 16-byte packs per thread that keep out of local memory: eight
+// in the forward, four of fp16 in the backward, only where channels' parameters
+// and sums are shared by four values.
+constexpr bool norm_has(int V, int K, int A, bool half, bool bwd) {
+  const bool wide = V == (half ? 8 : 4);
+  if (!wide) return K == 2 || (K == 8 && !(bwd && V == 4 && A == 1));
+  if (K == 8) return !bwd && A == 4;
+  if (K == 4) return !(bwd && half && A == 1);
+  return K >= 1 && K <= 3;
+}
+
 // Packs: the widest of 16 bytes or less that divides a row, so that every row
 // starts on a pack.  Row groups: the (K, G) with the fewest idle slots; on
 // ties, four packs per thread (fewer shuffles per value, 64 bytes in flight).
@@ -42,18 +53,20 @@ NormPlan norm_plan(int64_t N, int C, int T, bool half, bool bwd) {
   while (F % q.V != 0) q.V /= 2;
   q.A = (T % 4 == 0 && q.V % 4 == 0) ? 4 : 1;
   q.s = {N, C, T, F, 0, F / q.V};
-  static const int wide_fwd[] = {4, 2, 3, 1, 8}, wide_bwd[] = {4, 2, 3, 1}, narrow_k[] = {2, 8};
-  const int *ks = q.V == wide ? (bwd ? wide_bwd : wide_fwd) : narrow_k;
-  const int nk = q.V == wide ? (bwd ? 4 : 5) : 2;
+  static const int wide_ks[] = {4, 2, 3, 1, 8}, narrow_ks[] = {8, 2};
+  const int *ks = q.V == wide ? wide_ks : narrow_ks;
+  const int nk = q.V == wide ? 5 : 2;
   q.in_regs = false;
   int best = 0;
   for (int i = 0; i < nk; ++i) {
+    if (!norm_has(q.V, ks[i], q.A, half, bwd)) continue;
     int G = 1;
     while (G * ks[i] < q.s.nchunk && G <= kNormMaxThreads) G *= 2;
     if (G > kNormMaxThreads) continue;
-    if (!q.in_regs || G * ks[i] < best) {
+    const int cost = G * ks[i] * (G > 32 ? 5 : 4);  // a group of several warps meets at barriers
+    if (!q.in_regs || cost < best) {
       q.in_regs = true;
-      best = G * ks[i];
+      best = cost;
       q.K = ks[i];
       q.s.G = G;
     }
@@ -63,11 +76,10 @@ NormPlan norm_plan(int64_t N, int C, int T, bool half, bool bwd) {
   return q;
 }
 
-// Blocks of the row loop: enough to fill the GPU; the backward's partial sums
-// are one row per block, so it takes half as many.
-int norm_blocks(const NormPlan &q, int sms, bool bwd) {
+// Blocks of the row loop: what the SMs hold at 64 registers a thread.
+int norm_blocks(const NormPlan &q, int sms) {
   const int64_t want = q.in_regs ? ceil_div(q.s.N, q.threads / q.s.G) : q.s.N;
-  const int64_t cap = static_cast<int64_t>(sms) * ((bwd ? 1024 : 2048) / q.threads);
+  const int64_t cap = static_cast<int64_t>(sms) * (1024 / q.threads);
   return static_cast<int>(want < cap ? want : cap);
 }
 
@@ -77,7 +89,8 @@ int64_t norm_long_splits(int64_t N) {
   return n < 32 ? n : 32;
 }
 
-#define FEQL_NORM_WIDE(X, Ty, V, A) X(Ty, V, 1, A) X(Ty, V, 2, A) X(Ty, V, 3, A) X(Ty, V, 4, A)
+#define FEQL_NORM_WIDE(X, Ty, V, A) \
+  X(Ty, V, 1, A) X(Ty, V, 2, A) X(Ty, V, 3, A) X(Ty, V, 4, A) X(Ty, V, 8, A)
 #define FEQL_NORM_NARROW(X, Ty, V, A) X(Ty, V, 2, A) X(Ty, V, 8, A)
 #define FEQL_NORM_HALF(X)                                                                \
   FEQL_NORM_WIDE(X, __half, 8, 1) FEQL_NORM_WIDE(X, __half, 8, 4)                        \
@@ -91,6 +104,7 @@ int norm_fwd_launch(const NormPlan &q, bool half, const void *x, const void *gam
                     const void *beta, void *y, float2 *stats, float eps, int grid,
                     cudaStream_t st) {
 #define FEQL_CASE(Ty, VV, KK, AA)                                                             \
+  if constexpr (norm_has(VV, KK, AA, sizeof(Ty) == 2, false))                                 \
   if (q.V == VV && q.K == KK && q.A == AA) {                                                  \
     norm_fwd_kernel<Ty, VV, KK, AA><<<grid, q.threads, 0, st>>>(                              \
         static_cast<const Ty *>(x), static_cast<const Ty *>(gamma),                           \
@@ -99,12 +113,8 @@ int norm_fwd_launch(const NormPlan &q, bool half, const void *x, const void *gam
   }
   if (half) {
     FEQL_NORM_HALF(FEQL_CASE)
-    FEQL_CASE(__half, 8, 8, 1)
-    FEQL_CASE(__half, 8, 8, 4)
   } else {
     FEQL_NORM_FLOAT(FEQL_CASE)
-    FEQL_CASE(float, 4, 8, 1)
-    FEQL_CASE(float, 4, 8, 4)
   }
 #undef FEQL_CASE
   return FEQL_ERR_UNSUPPORTED;
@@ -114,6 +124,7 @@ int norm_bwd_launch(const NormPlan &q, bool half, const void *x, const void *dy,
                     const void *gamma, const float2 *stats, void *dx, float *part, int grid,
                     cudaStream_t st) {
 #define FEQL_CASE(Ty, VV, KK, AA)                                                             \
+  if constexpr (norm_has(VV, KK, AA, sizeof(Ty) == 2, true))                                  \
   if (q.V == VV && q.K == KK && q.A == AA) {                                                  \
     norm_bwd_kernel<Ty, VV, KK, AA><<<grid, q.threads, 0, st>>>(                              \
         static_cast<const Ty *>(x), static_cast<const Ty *>(dy),                              \
@@ -145,10 +156,19 @@ int norm_bwd_long(const NormPlan &q, const void *x, const void *dy, const void *
 template <typename Ty>
 int norm_reduce(const float *part, void *dgamma, void *dbeta, int C, int m, int blocks,
                 cudaStream_t st) {
-  norm_reduce_kernel<Ty><<<static_cast<unsigned>(ceil_div(C, kNormRedCh)), kNormRedCh * 32, 0,
-                           st>>>(part, static_cast<Ty *>(dgamma), static_cast<Ty *>(dbeta), C, m,
-                                 blocks);
-  return launch_status();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(C, 32 / m)));
+  cfg.blockDim = dim3(32 * kNormRedLanes);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, norm_reduce_kernel<Ty>, part, static_cast<Ty *>(dgamma),
+                            static_cast<Ty *>(dbeta), C, m, blocks) == cudaSuccess
+             ? FEQL_OK
+             : FEQL_ERR_CUDA;
 }
 
 int norm_check(int64_t N, int C, int T, int dtype) {
@@ -337,7 +357,7 @@ int feql_norm_forward(const void *x, const void *gamma, const void *beta, void *
   if (st != FEQL_OK) return st;
   const bool half = is_half(dtype);
   const NormPlan q = norm_plan(N, C, T, half, false);
-  const int grid = norm_blocks(q, dev.sms, false);
+  const int grid = norm_blocks(q, dev.sms);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   float2 *sp = reinterpret_cast<float2 *>(stats);
   if (q.in_regs) return norm_fwd_launch(q, half, x, gamma, beta, y, sp, eps, grid, s);
@@ -357,7 +377,7 @@ size_t feql_norm_backward_workspace_bytes(int64_t N, int C, int T, int dtype) {
   DeviceInfo dev;
   if (device_info(&dev) != FEQL_OK) return 0;
   const NormPlan q = norm_plan(N, C, T, is_half(dtype), true);
-  const int64_t rows = q.in_regs ? norm_blocks(q, dev.sms, true) : norm_long_splits(N);
+  const int64_t rows = q.in_regs ? norm_blocks(q, dev.sms) : norm_long_splits(N);
   const size_t bytes = static_cast<size_t>(rows) * 2 * (q.s.F / (q.in_regs ? q.A : 1)) * 4;
   return bytes > 16 ? bytes : 16;
 }
@@ -381,7 +401,7 @@ int feql_norm_backward(const void *x, const void *dy, const float *stats, const 
   float *part = static_cast<float *>(ws);
   int rows = 0;  // partial rows to add
   if (N > 0) {
-    const int grid = norm_blocks(q, dev.sms, true);
+    const int grid = norm_blocks(q, dev.sms);
     rows = q.in_regs ? grid : static_cast<int>(norm_long_splits(N));
     if (q.in_regs)
       st = norm_bwd_launch(q, half, x, dy, gamma, sp, dx, part, grid, s);

@@ -633,7 +633,7 @@ struct G8FwdParams {
   int stages, stage_bytes, bias_floats;
   int out_box;         // one staging box: 32 rows x 8 channels x T fp16
   int nout;            // staging boxes per epilogue warp: 2, or 1 when that leaves room for a third stage
-  Epilogue ep;         // activation, residual, saved z (kernels with kEp)
+  Epilogue ep;         // activation, residual, saved slope (kernels with kEp)
 };
 
 struct G8Smem {
@@ -677,7 +677,7 @@ struct G8Units {
 // 18 warps over the 4 SM sub-partitions put 5 warps on two 16K-register slices:
 // 5 x 32 x 96 = 15,360 registers fit, 104 would not.
 // kEp != kEpNone: y = res + act(z) (act.cuh).  A lane holds whole fibres of its token row, so
-// it reads the residual and writes z directly, 16 bytes at a time; y goes through
+// it reads the residual and writes the slope directly, 16 bytes at a time; y goes through
 // the staging box as always.
 template <class Gp, int kEp = kEpNone>
 __global__ void __maxnreg__(96)
@@ -858,9 +858,9 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
           }
           if (d0 >= p.Do) continue;  // whole group is padding
           uint32_t hv[4][T / 2];  // fibres of channels d0 + 4h .. d0 + 4h + 3, packed fp16
-          // kEp: this lane's residual and z, 2 T words of 16-byte pieces: a piece
+          // kEp: this lane's residual and slopes, 2 T words of 16-byte pieces: a piece
           // is one channel's fibre (T = 8) or a third of four (T = 6, Do % 4 == 0)
-          uint32_t rw[2 * T], zw[2 * T];
+          uint32_t rw[2 * T], sw[2 * T];
           const int64_t row = static_cast<int64_t>(m) * kBM + quad * 32 + lane;
           const int64_t at = (row * p.Do + d0 + 4 * h) * T;
           if constexpr (kEp != kEpNone) {
@@ -887,16 +887,16 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
             for (int e = 0; e < T / 2; ++e) {
               float z0 = y[2 * e] + bv, z1 = y[2 * e + 1] + bv;
               if constexpr (kEp != kEpNone)
-                act_pair<kEp>(p.ep, z0, z1, rw[i * (T / 2) + e], zw[i * (T / 2) + e]);
+                act_pair<kEp>(p.ep, z0, z1, rw[i * (T / 2) + e], sw[i * (T / 2) + e]);
               hv[i][e] = pack_half2(z0, z1);
             }
           }
           if constexpr (kEp != kEpNone) {
 #pragma unroll
             for (int q = 0; q < T / 2; ++q)
-              if (p.ep.z != nullptr && row < p.N && d0 + 4 * h + (T == 8 ? q : 3) < p.Do)
-                *reinterpret_cast<uint4 *>(static_cast<__half *>(p.ep.z) + at + 8 * q) =
-                    make_uint4(zw[4 * q], zw[4 * q + 1], zw[4 * q + 2], zw[4 * q + 3]);
+              if (p.ep.slope != nullptr && row < p.N && d0 + 4 * h + (T == 8 ? q : 3) < p.Do)
+                *reinterpret_cast<uint4 *>(static_cast<__half *>(p.ep.slope) + at + 8 * q) =
+                    make_uint4(sw[4 * q], sw[4 * q + 1], sw[4 * q + 2], sw[4 * q + 3]);
           }
           Geo::put4(ob + lane * Geo::kRow, h, lane, hv);
         }

@@ -70,8 +70,18 @@ __device__ __forceinline__ void norm_params(const Ty *__restrict__ p, float dflt
   }
 }
 
+// Blocks of kNormMaxThreads per SM that the registers are shared out for: two (64
+// registers) where the packs in flight and the sums leave room for unpacking.
+constexpr int norm_blocks_fwd(int bytes_per_thread, int params) {
+  return bytes_per_thread / 4 + params < 40 ? 2 : 1;
+}
+constexpr int norm_blocks_bwd(int bytes_per_thread, int sums) {
+  return bytes_per_thread / 4 + sums <= 40 ? 2 : 1;
+}
+
 template <typename Ty, int V, int K, int A>
-__global__ void __launch_bounds__(kNormMaxThreads)
+__global__ void __launch_bounds__(kNormMaxThreads,
+                                  norm_blocks_fwd(K * V * sizeof(Ty), 2 * K * V / A))
 norm_fwd_kernel(const Ty *__restrict__ x, const Ty *__restrict__ gamma,
                 const Ty *__restrict__ beta, Ty *__restrict__ y, float2 *__restrict__ stats,
                 const NormShape s, float eps) {
@@ -104,6 +114,8 @@ norm_fwd_kernel(const Ty *__restrict__ x, const Ty *__restrict__ gamma,
       for (int j = 0; j < V; ++j) sum += f[j];
     }
     const float mu = norm_group_sum(sum, s.G, red) * inv;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k].renew();
     float sq = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -118,6 +130,8 @@ norm_fwd_kernel(const Ty *__restrict__ x, const Ty *__restrict__ gamma,
       }
     const float var = norm_group_sum(sq, s.G, red) * inv;
     const float r = 1.f / sqrtf(var + eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k].renew();
     if (!live) continue;
     if (stats != nullptr && lane == 0) stats[row] = make_float2(mu, r);
 #pragma unroll
@@ -140,7 +154,8 @@ norm_fwd_kernel(const Ty *__restrict__ x, const Ty *__restrict__ gamma,
 // part[block][2][F / A]: this block's sums of dy xh and dy over its rows and
 // over each A columns.
 template <typename Ty, int V, int K, int A>
-__global__ void __launch_bounds__(kNormMaxThreads)
+__global__ void __launch_bounds__(kNormMaxThreads,
+                                  norm_blocks_bwd(2 * K * V * sizeof(Ty), 2 * K * V / A))
 norm_bwd_kernel(const Ty *__restrict__ x, const Ty *__restrict__ dy, const Ty *__restrict__ gamma,
                 const float2 *__restrict__ stats, Ty *__restrict__ dx, float *__restrict__ part,
                 const NormShape s) {
@@ -190,6 +205,11 @@ norm_bwd_kernel(const Ty *__restrict__ x, const Ty *__restrict__ dy, const Ty *_
     }
     const float m1 = norm_group_sum(s1, s.G, red) * inv;
     const float m2 = norm_group_sum(s2, s.G, red) * inv;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      v[k].renew();
+      w[k].renew();
+    }
     if (!live) continue;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -258,35 +278,41 @@ norm_bwd_kernel(const Ty *__restrict__ x, const Ty *__restrict__ dy, const Ty *_
   }
 }
 
-// dgamma[c], dbeta[c] from the partials: 8 channels per block, 32 threads each,
-// in a fixed order.  m = T / A partial columns belong to a channel.
-constexpr int kNormRedCh = 8;
+// dgamma[c], dbeta[c] from the partials, in a fixed order: 32 partial columns
+// (m = T / A neighbours belong to a channel) by 32 row lanes per block.  Launched
+// as the programmatic dependent of the kernel that writes the partials.
+constexpr int kNormRedLanes = 32;
 template <typename Ty>
-__global__ void __launch_bounds__(kNormRedCh * 32)
+__global__ void __launch_bounds__(32 * kNormRedLanes)
 norm_reduce_kernel(const float *__restrict__ part, Ty *__restrict__ dgamma,
                    Ty *__restrict__ dbeta, int C, int m, int blocks) {
-  const int c = blockIdx.x * kNormRedCh + (threadIdx.x & (kNormRedCh - 1));
-  const int r = threadIdx.x / kNormRedCh;  // 0..31
+  __shared__ float sum[2][kNormRedLanes][33];
+  const int col = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const int per = 32 / m;  // channels per block
+  const int c0 = blockIdx.x * per;
   const int64_t nv = static_cast<int64_t>(C) * m;
+  const int64_t at = static_cast<int64_t>(c0) * m + col;
   float g = 0.f, b = 0.f;
-  if (c < C)
-    for (int i = r; i < blocks; i += 32)
-      for (int j = 0; j < m; ++j) {
-        g += part[2 * i * nv + static_cast<int64_t>(c) * m + j];
-        b += part[(2 * i + 1) * nv + static_cast<int64_t>(c) * m + j];
-      }
-  __shared__ float sg[32][kNormRedCh], sb[32][kNormRedCh];
-  sg[r][threadIdx.x & (kNormRedCh - 1)] = g;
-  sb[r][threadIdx.x & (kNormRedCh - 1)] = b;
-  __syncthreads();
-  if (r == 0 && c < C) {
-    g = b = 0.f;
-    for (int i = 0; i < 32; ++i) {
-      g += sg[i][threadIdx.x];
-      b += sb[i][threadIdx.x];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (col < per * m && at < nv) {
+#pragma unroll 4
+    for (int i = r; i < blocks; i += kNormRedLanes) {
+      g += part[2 * i * nv + at];
+      b += part[(2 * i + 1) * nv + at];
     }
-    if (dgamma != nullptr) dgamma[c] = narrow<Ty>(g);
-    if (dbeta != nullptr) dbeta[c] = narrow<Ty>(b);
+  }
+  sum[0][r][col] = g;
+  sum[1][r][col] = b;
+  __syncthreads();
+  if (r < 2) {  // warp 0: dgamma's columns, warp 1: dbeta's
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNormRedLanes; ++i) v += sum[r][i][col];
+    float t = v;
+    for (int j = 1; j < m; ++j) t += __shfl_down_sync(0xffffffffu, v, j);
+    const int c = c0 + col / m;
+    Ty *to = r == 0 ? dgamma : dbeta;
+    if (to != nullptr && col % m == 0 && col < per * m && c < C) to[c] = narrow<Ty>(t);
   }
 }
 

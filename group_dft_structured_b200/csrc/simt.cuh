@@ -150,14 +150,12 @@ simt_fwd_kernel(const T *__restrict__ in, const float *__restrict__ Wp, const T 
       }
       if constexpr (kEp != kEpNone) {
         const int64_t at = (n * Do + o) * kT;
-        float r[4] = {0.f, 0.f, 0.f, 0.f}, z[4];
+        float r[4] = {0.f, 0.f, 0.f, 0.f}, slope[4];
         if (ep.res != nullptr) Vec4<T>::load(static_cast<const T *>(ep.res) + at, r);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          z[t] = act_saved<kEp>(ep, y[t]);
-          y[t] = act_apply<kEp, sizeof(T) == 2>(ep, y[t], r[t]);
-        }
-        if (ep.z != nullptr) Vec4<T>::store(static_cast<T *>(ep.z) + at, z);
+        for (int t = 0; t < 4; ++t)
+          y[t] = act_value<kEp, sizeof(T) == 2>(ep, y[t], r[t], slope[t]);
+        if (ep.slope != nullptr) Vec4<T>::store(static_cast<T *>(ep.slope) + at, slope);
       }
       Vec4<T>::store(out + (n * Do + o) * kT, y);
     }
@@ -263,6 +261,7 @@ __global__ void dw_reduce_kernel(const float *__restrict__ ws, const float *__re
        e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     if (e < plane) {
       float g[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8  // loads of eight splits in flight; the sums stay in order
       for (int s = 0; s < splits; ++s) {
         const float *p = ws + static_cast<int64_t>(s) * 4 * plane + e;
 #pragma unroll
@@ -274,6 +273,7 @@ __global__ void dw_reduce_kernel(const float *__restrict__ ws, const float *__re
     } else if (db != nullptr) {
       const int d = static_cast<int>(e - plane);
       float s = 0.f;
+#pragma unroll 16
       for (int k = 0; k < splits; ++k) s += ws_db[static_cast<int64_t>(k) * D + d];
       db[d] = static_cast<T>(s);
     }

@@ -229,13 +229,14 @@ ct_simt_fwd_kernel(const Ty *__restrict__ in, const float *__restrict__ Wp,
       for (int t = 0; t < T; ++t) {
         float v = y[t] + bv;
         if constexpr (kEp != kEpNone) {
-          // not contracted with the inverse's last product: the same y whether z is saved or not
+          // not contracted with the inverse's last product: the same y in both forms
           v = __fadd_rn(y[t], bv);
           const int64_t at = (n * Do + o) * T + t;
-          if (ep.z != nullptr) static_cast<Ty *>(ep.z)[at] = ct_cast<Ty>(act_saved<kEp>(ep, v));
           const float r =
               ep.res != nullptr ? ct_load<Ty>(static_cast<const Ty *>(ep.res) + at) : 0.f;
-          v = act_apply<kEp, sizeof(Ty) == 2>(ep, v, r);
+          float slope;
+          v = act_value<kEp, sizeof(Ty) == 2>(ep, v, r, slope);
+          if (ep.slope != nullptr) static_cast<Ty *>(ep.slope)[at] = ct_cast<Ty>(slope);
         }
         dst[t] = ct_cast<Ty>(v);
       }
@@ -365,6 +366,7 @@ __global__ void ct_simt_dw_reduce_kernel(const float *__restrict__ ws, const flo
       float G[T], y[T];
 #pragma unroll
       for (int p = 0; p < T; ++p) G[p] = 0.f;
+#pragma unroll 4  // loads of four splits in flight; the sums stay in order
       for (int s = 0; s < splits; ++s)
 #pragma unroll
         for (int p = 0; p < T; ++p) G[p] += ws[(static_cast<int64_t>(s) * T + p) * plane + e];
@@ -374,6 +376,7 @@ __global__ void ct_simt_dw_reduce_kernel(const float *__restrict__ ws, const flo
     } else if (db != nullptr) {
       const int64_t d = e - plane;
       float s = 0.f;
+#pragma unroll 16
       for (int sp = 0; sp < splits; ++sp) s += ws_db[static_cast<int64_t>(sp) * D + d];
       db[d] = ct_cast<Ty>(s);
     }

@@ -44,6 +44,7 @@
 
 #include <cuda_fp16.h>
 
+#include "act.cuh"
 #include "plan.cuh"
 #include "rdft4.cuh"
 #include "sm100.cuh"
@@ -76,6 +77,7 @@ struct TcBwdParams {
   int ndx;             // dX accumulator buffers (1 or 2)
   int merged;          // dW bin 1 as two N = 2*CT MMAs (6*CT TMEM columns), see tc_dw.cuh
   int stack_dy, stack_x;  // 1: one 3-D load brings all of a stage's dy (x) boxes
+  int slope_bytes;     // slope boxes of a stage (kAct): one buffer of them
   float *ws;           // [splits][4][D][Cs]
   float *ws_db;        // [splits][D]
 };
@@ -89,16 +91,17 @@ __device__ __forceinline__ int bw_dy_row(int pp, int r) {
 }
 
 struct BwSmem {
-  int wres, stage0, bars, total;
+  int wres, stage0, sl, bars, total;
 };
 
 __host__ __device__ inline BwSmem tc_bwd_smem(const TcBwdParams &p) {
   BwSmem s;
   s.wres = 0;
   s.stage0 = p.wres_bytes;
-  s.bars = s.stage0 + p.stages * p.slots * kBwBox;
-  // full, tready, empty per stage; dxfull, dxempty x2; dwfull; wfull; tmem slot
-  s.total = s.bars + (3 * p.stages + 4 + 2) * 8 + 16;
+  s.sl = s.stage0 + p.stages * p.slots * kBwBox;
+  s.bars = s.sl + p.slope_bytes;
+  // full, tready, empty per stage; dxfull, dxempty x2; dwfull; wfull; tmem slot; sfull, sempty
+  s.total = s.bars + (3 * p.stages + 4 + 2) * 8 + 16 + 2 * 8;
   return s;
 }
 
@@ -110,10 +113,17 @@ __host__ __device__ inline BwSmem tc_bwd_smem(const TcBwdParams &p) {
 // bin-0 plane value to 1/4, so the dW bin-0 MMA produces
 //   G0[d][C] = sum_n (dY0[n,d] / 4) * (1/4) = db[d] / 16
 // in the padding column and db needs no accumulation in registers.
-template <bool kDbCol>
+//
+// kAct: the gradient through an activation, dz = dy slope (act.cuh), in place of dy.
+// A stage's slopes come by TMA into one buffer beside the stages' (the transform
+// reads it first, so it is free again while the stage's MMAs run), and the
+// transform multiplies its dy fibres before their rDFT: dz is rounded to fp16 as
+// the separate kernel rounds it, and never goes to memory.  401408 x 24 -> 96: 226 us
+// for the two kernels, BWD_ACT_US for this one.
+template <bool kDbCol, bool kAct = false>
 __global__ void __maxnreg__(80)
 tc_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x,
-              const TcBwdParams p) {
+              const __grid_constant__ CUtensorMap tm_s, const TcBwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -127,6 +137,7 @@ tc_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
   uint64_t *dwfull = dxempty + 2;
   uint64_t *wfull = dwfull + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(wfull + 1);
+  uint64_t *sfull = wfull + 3, *sempty = sfull + 1;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int split = blockIdx.x;
@@ -149,6 +160,8 @@ tc_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
     }
     mbar_init(dwfull, 1);
     mbar_init(wfull, 1);
+    mbar_init(sfull, 1);
+    mbar_init(sempty, kBwXfWarps);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -170,7 +183,7 @@ tc_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
         mbar_arrive_expect_tx(wfull, p.nqd * p.chunk_bytes);
         bulk_load(smem + L.wres, p.wt, p.nqd * p.chunk_bytes, wfull);
       }
-      int s = 0;
+      int s = 0, ns = 0;
       uint32_t ph = 0;
       for (int ch = 0; ch < nst; ++ch) {
         if (ok) ok = mbar_wait(&empty[s], ph ^ 1);
@@ -191,8 +204,23 @@ tc_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
               tma_load_2d(st + (p.nqd + q) * kBwBox, &tm_x, q * 16 * kT, row, &full[s]);
           }
         }
+        if constexpr (kAct) {
+          if (ok) ok = mbar_wait(sempty, (ch & 1) ^ 1);
+          if (ok) {
+            const int32_t row = static_cast<int32_t>(t_begin + static_cast<int64_t>(ch) * kBwTB);
+            mbar_arrive_expect_tx(sfull, p.nqd * kBwBox);
+            ++ns;
+            if (p.stack_dy) {
+              tma_load_3d(smem + L.sl, &tm_s, 0, row, 0, sfull);
+            } else {
+              for (int q = 0; q < p.nqd; ++q)
+                tma_load_2d(smem + L.sl + q * kBwBox, &tm_s, q * 16 * kT, row, sfull);
+            }
+          }
+        }
         if (++s == p.stages) { s = 0; ph ^= 1; }
       }
+      if (kAct && ns > 0) mbar_wait(sfull, (ns - 1) & 1);  // none left in flight
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
@@ -284,6 +312,9 @@ tc_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
     uint32_t ph = 0;
     for (int ch = 0; ch < nst; ++ch) {
       if (ok) ok = mbar_wait(&full[s], ph);
+      if constexpr (kAct) {
+        if (ok) ok = mbar_wait(sfull, ch & 1);
+      }
       uint8_t *st = smem + L.stage0 + s * p.slots * kBwBox;
       uint32_t pl[kPer][4][8];
 #pragma unroll
@@ -294,12 +325,23 @@ tc_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
           const uint8_t *src = st + b * kBwBox + r * 128;
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(src + ((q ^ (r & 7)) << 4));
+            uint4 v = *reinterpret_cast<const uint4 *>(src + ((q ^ (r & 7)) << 4));
+            if constexpr (kAct) {
+              if (b < p.nqd) {  // the same for a whole warp
+                const uint4 z = *reinterpret_cast<const uint4 *>(smem + L.sl + b * kBwBox + r * 128 +
+                                                                ((q ^ (r & 7)) << 4));
+                v = make_uint4(act_grad2(v.x, z.x), act_grad2(v.y, z.y), act_grad2(v.z, z.z),
+                               act_grad2(v.w, z.w));
+              }
+            }
             rdft4_pair_q(v, pl[k][0][q], pl[k][1][q], pl[k][2][q], pl[k][3][q]);
           }
         }
       }
       named_bar_sync(2, kBwXfWarps * 32);  // all rows read before the planes overwrite them
+      if constexpr (kAct) {
+        if (lane == 0 && ok) mbar_arrive(sempty);
+      }
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         const int e = t + k * kBwXfWarps * 32;

@@ -91,7 +91,7 @@ struct TcFwdParams {
   int bias_floats;      // nD * BD
   int res_ring;         // 1: the epilogue warps' residual rings are there
   void *out;            // [N][Do][4], fp16 (fp32 in split-TF32 mode)
-  Epilogue ep;          // activation, residual, saved z (kernels with kEp)
+  Epilogue ep;          // activation, residual, saved slope (kernels with kEp)
 };
 
 struct TcSmem {
@@ -159,8 +159,8 @@ struct TcUnits {
 // is dropped: Ootomo and Yokota's split-TF32 scheme), and the epilogue stores
 // fp32 rows.  Bins are not scaled (fp32 has the range).
 //
-// kEp != kEpNone: y = res + act(z) in the epilogue (act.cuh), the pre-activation
-// z stored beside y when the backward pass will want it.  An fp16 residual comes
+// kEp != kEpNone: y = res + act(z) in the epilogue (act.cuh), the slope act'(z)
+// stored beside y when the backward pass will want it.  An fp16 residual comes
 // by TMA: each epilogue warp loads the 32-row x 16-channel boxes (4 KB) of its
 // own column groups, in the order in which it will use them, into a private
 // ring of kResDepth slots, so the loads run kResDepth groups ahead (direct loads
@@ -510,13 +510,14 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
                     float4 q = make_float4(fmaf(0.5f, Yr, e), fmaf(-0.5f, Yi, o),
                                            fmaf(-0.5f, Yr, e), fmaf(0.5f, Yi, o));
                     if constexpr (kEp != kEpNone) {
-                      if (p.ep.z != nullptr)
-                        *reinterpret_cast<float4 *>(static_cast<float *>(p.ep.z) + at) = q;
                       const float4 r = rv[hf][rr][cc];
-                      q = make_float4(act_apply<kEp, false>(p.ep, q.x, r.x),
-                                      act_apply<kEp, false>(p.ep, q.y, r.y),
-                                      act_apply<kEp, false>(p.ep, q.z, r.z),
-                                      act_apply<kEp, false>(p.ep, q.w, r.w));
+                      float4 s;
+                      q = make_float4(act_value<kEp, false>(p.ep, q.x, r.x, s.x),
+                                      act_value<kEp, false>(p.ep, q.y, r.y, s.y),
+                                      act_value<kEp, false>(p.ep, q.z, r.z, s.z),
+                                      act_value<kEp, false>(p.ep, q.w, r.w, s.w));
+                      if (p.ep.slope != nullptr)
+                        *reinterpret_cast<float4 *>(static_cast<float *>(p.ep.slope) + at) = s;
                     }
                     *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = q;
                   }
@@ -531,7 +532,7 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
           for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {  // rows r0 and r0 + 8
-              uint32_t w[4], wz[4];
+              uint32_t w[4], ws[4];
               uint4 rv = {};
               if constexpr (kEp != kEpNone) {
                 const int r = (lane >> 2) + 16 * hf + 8 * rr;  // row of the box
@@ -553,17 +554,17 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
                 if constexpr (kEp != kEpNone) {
 #pragma unroll
                   for (int q = 0; q < 2; ++q)
-                    act_pair<kEp>(p.ep, v[2 * q], v[2 * q + 1], rw[2 * cc + q], wz[2 * cc + q]);
+                    act_pair<kEp>(p.ep, v[2 * q], v[2 * q + 1], rw[2 * cc + q], ws[2 * cc + q]);
                 }
                 w[2 * cc] = pack_half2(v[0], v[1]);
                 w[2 * cc + 1] = pack_half2(v[2], v[3]);
               }
               const int64_t row = row0 + 16 * hf + 8 * rr;
               if constexpr (kEp != kEpNone) {
-                if (p.ep.z != nullptr && row < p.N)
-                  *reinterpret_cast<uint4 *>(static_cast<__half *>(p.ep.z) + row * row_elems +
+                if (p.ep.slope != nullptr && row < p.N)
+                  *reinterpret_cast<uint4 *>(static_cast<__half *>(p.ep.slope) + row * row_elems +
                                              static_cast<int64_t>(d) * kT) =
-                      make_uint4(wz[0], wz[1], wz[2], wz[3]);
+                      make_uint4(ws[0], ws[1], ws[2], ws[3]);
               }
               if (row < p.N)
                 *reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + row * row_elems +

@@ -72,6 +72,16 @@ struct Pack {
     *reinterpret_cast<typename Word<V * sizeof(Ty)>::type *>(p) = w;
   }
   __device__ __forceinline__ void zero() { w = decltype(w){}; }
+
+  // Keeps the compiler from holding unpacked values (twice the registers for
+  // fp16) from here on: the next unpack() is a new one.
+  __device__ __forceinline__ void renew() {
+    if constexpr (sizeof(w) >= 4) {
+      uint32_t *p = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(w) / 4); ++i) asm volatile("" : "+r"(p[i]));
+    }
+  }
 };
 
 // fp32 vectors of V values, two to an instruction where V allows (sm_100's paired

@@ -5,6 +5,8 @@ the library.  No arithmetic happens here.
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (FEQL_ACT_NONE, FEQL_FP16, FEQL_FP16_SIMT, FEQL_FP32, feql_backward,
@@ -189,11 +191,15 @@ def mlp_forward(x: torch.Tensor, What: torch.Tensor, b1, b2, H: int, Co: int, mo
 # one device, which need not be the current one, and run on torch's current
 # stream of that device; what they return belongs to that stream.
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(t: torch.Tensor):
     """The device guard of a call on ``t``'s device."""
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"expected CUDA tensors (libfeql.so kernels), got one on {t.device}")
-    return torch.cuda.device(t.device)
+    return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
 def _mode(t: torch.Tensor) -> int:
@@ -204,20 +210,19 @@ def _mode(t: torch.Tensor) -> int:
     raise TypeError(f"expected float16 or float32 data, not {t.dtype}")
 
 
-def _take(t, name: str, shape, dtype, device):
+def _take(t, name: str, shape, dtype, index: int):
     """``t`` checked and dense, on a 16-byte boundary; None stays None."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    t = t.detach()
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if not t.is_contiguous():
-        t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+        t = t.detach().contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.detach().clone()
 
 
 # The layer with activation and residual in its epilogue.  ``act`` is one of
@@ -252,10 +257,11 @@ def _forward_act(calls, p4m, x, What, b, D, mode, act, res, save_z):
     if nbytes == 0:
         raise ValueError("unsupported (T, C, D, mode)")
     with _on(x):
-        x = _take(x, "x", x.shape, x.dtype, x.device)
-        What = _take(What, "What", (nbytes,), torch.uint8, x.device)
-        b = _take(b, "b", (D,), x.dtype, x.device)
-        res = _take(res, "res", (N, D, T), x.dtype, x.device)
+        at = x.get_device()
+        x = _take(x, "x", x.shape, x.dtype, at)
+        What = _take(What, "What", (nbytes,), torch.uint8, at)
+        b = _take(b, "b", (D,), x.dtype, at)
+        res = _take(res, "res", (N, D, T), x.dtype, at)
         y = torch.empty((N, D, T), dtype=x.dtype, device=x.device)
         z = torch.empty_like(y) if save_z and act != FEQL_ACT_NONE else None
         forward(T, x, What, b, res, y, z, N, C, D, act, mode)
@@ -272,11 +278,11 @@ def _backward_act(calls, p4m, x, dy, z, What, mode, act, with_dx, with_dw, with_
         raise ValueError("unsupported (T, C, D, mode)")
     dx = dW = db = None
     with _on(x):
-        dev = x.device
-        x = _take(x, "x", x.shape, x.dtype, dev)
-        dy = _take(dy, "dy", (N, D, T), x.dtype, dev)
-        z = _take(z, "z", (N, D, T), x.dtype, dev)
-        What = _take(What, "What", (nbytes,), torch.uint8, dev)
+        dev, at = x.device, x.get_device()
+        x = _take(x, "x", x.shape, x.dtype, at)
+        dy = _take(dy, "dy", (N, D, T), x.dtype, at)
+        z = _take(z, "z", (N, D, T), x.dtype, at)
+        What = _take(What, "What", (nbytes,), torch.uint8, at)
         ws = torch.empty(workspace(T, N, C, D, act, mode), dtype=torch.uint8, device=dev)
         if with_dx:
             dx = torch.empty_like(x)
@@ -291,9 +297,10 @@ def _backward_act(calls, p4m, x, dy, z, What, mode, act, with_dx, with_dw, with_
 
 def ct_forward_act(x: torch.Tensor, What: torch.Tensor, b, D: int, mode: int, act: int, res=None,
                    save_z: bool = False):
-    """y = res + act(z), z = the C_T layer of x plus b: (y, z).
+    """y = res + act(z), z = the C_T layer of x plus b: (y, saved z).
 
-    ``z`` is what ct_backward_act takes; None without ``save_z`` or activation.
+    The ``z`` returned is what ct_backward_act takes of it, the activation's slope
+    there; None without ``save_z`` or activation.
     """
     return _forward_act(_CYCLIC_CALLS, False, x, What, b, D, mode, act, res, save_z)
 
@@ -328,9 +335,10 @@ def norm_forward(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5,
     N, C, T = x.shape
     mode = _mode(x)
     with _on(x):
-        x = _take(x, "x", x.shape, x.dtype, x.device)
-        gamma = _take(gamma, "gamma", (C,), x.dtype, x.device)
-        beta = _take(beta, "beta", (C,), x.dtype, x.device)
+        at = x.get_device()
+        x = _take(x, "x", x.shape, x.dtype, at)
+        gamma = _take(gamma, "gamma", (C,), x.dtype, at)
+        beta = _take(beta, "beta", (C,), x.dtype, at)
         y = torch.empty_like(x)
         stats = (torch.empty((N, 2), dtype=torch.float32, device=x.device) if save_stats
                  else None)
@@ -346,10 +354,11 @@ def norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, gamma=
     N, C, T = x.shape
     mode = _mode(x)
     with _on(x):
-        x = _take(x, "x", x.shape, x.dtype, x.device)
-        dy = _take(dy, "dy", x.shape, x.dtype, x.device)
-        stats = _take(stats, "stats", (N, 2), torch.float32, x.device)
-        gamma = _take(gamma, "gamma", (C,), x.dtype, x.device)
+        at = x.get_device()
+        x = _take(x, "x", x.shape, x.dtype, at)
+        dy = _take(dy, "dy", x.shape, x.dtype, at)
+        stats = _take(stats, "stats", (N, 2), torch.float32, at)
+        gamma = _take(gamma, "gamma", (C,), x.dtype, at)
         dx = torch.empty_like(x)
         dgamma = dbeta = None
         if with_params:
@@ -393,11 +402,11 @@ def scan_forward(u: torch.Tensor, g: torch.Tensor, h0=None, offsets=None, save: 
     B, N, C, T, shared = _scan_sizes(u, g, offsets)
     mode = _mode(u)
     with _on(u):
-        dev = u.device
-        u = _take(u, "u", u.shape, u.dtype, dev)
-        g = _take(g, "g", g.shape, u.dtype, dev)
-        h0 = _take(h0, "h0", (B, C, T), torch.float32, dev)
-        offsets = _take(offsets, "offsets", (B + 1,), torch.int32, dev)
+        dev, at = u.device, u.get_device()
+        u = _take(u, "u", u.shape, u.dtype, at)
+        g = _take(g, "g", g.shape, u.dtype, at)
+        h0 = _take(h0, "h0", (B, C, T), torch.float32, at)
+        offsets = _take(offsets, "offsets", (B + 1,), torch.int32, at)
         h = torch.empty_like(u)
         hN = torch.empty((B, C, T), dtype=torch.float32, device=dev)
         nbytes = feql_scan_workspace_bytes(B, N, C, T, shared, offsets is not None, mode)
@@ -412,14 +421,14 @@ def scan_backward(dh: torch.Tensor, u: torch.Tensor, g: torch.Tensor, saved, dhN
     B, N, C, T, shared = _scan_sizes(u, g, offsets)
     mode = _mode(u)
     with _on(u):
-        dev = u.device
-        u = _take(u, "u", u.shape, u.dtype, dev)
-        g = _take(g, "g", g.shape, u.dtype, dev)
-        dh = _take(dh, "dh", u.shape, u.dtype, dev)
-        dhN = _take(dhN, "dhN", (B, C, T), torch.float32, dev)
-        offsets = _take(offsets, "offsets", (B + 1,), torch.int32, dev)
-        h = _take(saved[0], "h", u.shape, u.dtype, dev)
-        h0 = _take(saved[1], "h0", (B, C, T), torch.float32, dev)
+        dev, at = u.device, u.get_device()
+        u = _take(u, "u", u.shape, u.dtype, at)
+        g = _take(g, "g", g.shape, u.dtype, at)
+        dh = _take(dh, "dh", u.shape, u.dtype, at)
+        dhN = _take(dhN, "dhN", (B, C, T), torch.float32, at)
+        offsets = _take(offsets, "offsets", (B + 1,), torch.int32, at)
+        h = _take(saved[0], "h", u.shape, u.dtype, at)
+        h0 = _take(saved[1], "h0", (B, C, T), torch.float32, at)
         du, dg = torch.empty_like(u), torch.empty_like(g)
         dh0 = torch.empty((B, C, T), dtype=torch.float32, device=dev)
         nbytes = feql_scan_workspace_bytes(B, N, C, T, shared, offsets is not None, mode)
@@ -441,9 +450,10 @@ def scan_step(u: torch.Tensor, g: torch.Tensor, state: torch.Tensor) -> torch.Te
     with _on(u):
         if not state.is_contiguous() or state.data_ptr() % 16 != 0:
             raise ValueError("state is updated in place: it has to be dense and 16-byte aligned")
-        u = _take(u, "u", u.shape, u.dtype, u.device)
-        g = _take(g, "g", g.shape, u.dtype, u.device)
-        s = _take(state, "state", (B, C, T), torch.float32, u.device)
+        at = u.get_device()
+        u = _take(u, "u", u.shape, u.dtype, at)
+        g = _take(g, "g", g.shape, u.dtype, at)
+        s = _take(state, "state", (B, C, T), torch.float32, at)
         h = torch.empty_like(u)
         feql_scan_step(u, g, s, h, B, C, T, g.dim() < 3, mode)
     return h

@@ -101,7 +101,7 @@ class EqLinearFunction(torch.autograd.Function):
 class EqLinearActFunction(torch.autograd.Function):
     """y = res + act(z), z = EqLinear(x) + b on (N, C, T) tensors; the arguments of
     EqLinearFunction, ``res`` (or None) and one of FEQL_ACT_*.  Backward: dz =
-    dy act'(z) from the saved z, then dx, dW, db as asked for; dres = dy."""
+    dy act'(z) from the saved slopes, then dx, dW, db as asked for; dres = dy."""
 
     @staticmethod
     def forward(ctx, x, W, b, res, What, mode: int, group: str, act: int):

@@ -260,8 +260,8 @@ int feql_mlp_forward(const void *x, const void *What, const void *b1, const void
  * k0 = sqrt(2 / pi), k1 = 0.044715; SiLU is z sigma(z).  z is kept in fp32 from
  * the products to y (one rounding, y's).
  *   res : device [N][D][T] or NULL (no residual)
- *   z   : device [N][D][T] (written) for the backward pass, or NULL; a positive z
- *         that rounds to zero is saved as the least subnormal under ReLU
+ *   slope : device [N][D][T] (written), act'(z) in the data type, which the
+ *         backward pass takes; or NULL
  * The other arguments, groups, modes and errors are those of feql_forward,
  * feql_ct_forward and feql_p4m_forward. */
 typedef enum {
@@ -272,31 +272,31 @@ typedef enum {
 } feql_activation;
 
 int feql_forward_act(const void *x, const void *What, const void *b, const void *res, void *y,
-                     void *z, int64_t N, int C, int D, int act, int dtype, feql_stream stream);
+                     void *slope, int64_t N, int C, int D, int act, int dtype, feql_stream stream);
 int feql_ct_forward_act(int T, const void *x, const void *What, const void *b, const void *res,
-                        void *y, void *z, int64_t N, int C, int D, int act, int dtype,
+                        void *y, void *slope, int64_t N, int C, int D, int act, int dtype,
                         feql_stream stream);
 int feql_p4m_forward_act(const void *x, const void *What, const void *b, const void *res, void *y,
-                         void *z, int64_t N, int C, int D, int act, int dtype,
+                         void *slope, int64_t N, int C, int D, int act, int dtype,
                          feql_stream stream);
 
-/* Backward: dz = dy act'(z), then dx, dW and db of the layer for dz (the
+/* Backward: dz = dy slope, then dx, dW and db of the layer for dz (the
  * residual's gradient is dy itself).  dz is rounded to the data type.
- *   z  : as saved by the forward pass (NULL for FEQL_ACT_NONE)
+ *   slope : as saved by the forward pass (NULL for FEQL_ACT_NONE: dz = dy)
  *   dx : device [N][C][T] or NULL          dW : [D][C][T] or NULL
  *   db : [D] or NULL (NULL without dW); not both dx and dW NULL
  *   ws : ws_bytes >= feql_*_backward_act_workspace_bytes for these sizes (which
  *        includes room for dz) */
 size_t feql_backward_act_workspace_bytes(int64_t N, int C, int D, int act, int dtype);
-int feql_backward_act(const void *x, const void *dy, const void *z, const void *What, void *dx,
+int feql_backward_act(const void *x, const void *dy, const void *slope, const void *What, void *dx,
                       void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C, int D,
                       int act, int dtype, feql_stream stream);
 size_t feql_ct_backward_act_workspace_bytes(int T, int64_t N, int C, int D, int act, int dtype);
-int feql_ct_backward_act(int T, const void *x, const void *dy, const void *z, const void *What,
+int feql_ct_backward_act(int T, const void *x, const void *dy, const void *slope, const void *What,
                          void *dx, void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C,
                          int D, int act, int dtype, feql_stream stream);
 size_t feql_p4m_backward_act_workspace_bytes(int64_t N, int C, int D, int act, int dtype);
-int feql_p4m_backward_act(const void *x, const void *dy, const void *z, const void *What, void *dx,
+int feql_p4m_backward_act(const void *x, const void *dy, const void *slope, const void *What, void *dx,
                           void *dW, void *db, void *ws, size_t ws_bytes, int64_t N, int C, int D,
                           int act, int dtype, feql_stream stream);
 
