@@ -48,11 +48,19 @@ inline Epilogue make_epilogue(int act, const void *res, void *slope) {
 }
 
 // Variants of an epilogue: none (the layer alone); max(z, lo), which is ReLU or,
-// with lo = -inf, no activation; the sigmoid family.
-enum EpKind { kEpNone = 0, kEpMax = 1, kEpSigmoid = 2 };
+// with lo = -inf, no activation; the sigmoid family; each without and with its
+// slope on the tensor cores' fp16 path (elsewhere the slope is always at hand).
+enum EpKind { kEpNone = 0, kEpMax = 1, kEpSigmoid = 2, kEpMaxSlope = 3, kEpSigmoidSlope = 4 };
+
+__host__ __device__ constexpr bool ep_is_max(int kind) {
+  return kind == kEpMax || kind == kEpMaxSlope;
+}
+__host__ __device__ constexpr bool ep_has_slope(int kind) { return kind >= kEpMaxSlope; }
 
 inline int epilogue_kind(const Epilogue &e) {
-  return e.act == FEQL_ACT_GELU || e.act == FEQL_ACT_SILU ? kEpSigmoid : kEpMax;
+  const bool sig = e.act == FEQL_ACT_GELU || e.act == FEQL_ACT_SILU;
+  if (e.slope == nullptr) return sig ? kEpSigmoid : kEpMax;
+  return sig ? kEpSigmoidSlope : kEpMaxSlope;
 }
 
 // The larger of two, NaN if either is.
@@ -72,8 +80,8 @@ __device__ __forceinline__ float act_square(float z) { return fminf(z * z, 1e8f)
 // so, far below the outputs' rounding.
 template <int kKind, bool kFast>
 __device__ __forceinline__ float act_value(const Epilogue &e, float z, float res, float &slope) {
-  if constexpr (kKind == kEpMax) {
-    slope = z > e.lo ? 1.f : (z != z ? z : 0.f);
+  if constexpr (ep_is_max(kKind)) {
+    slope = z <= e.lo ? 0.f : 1.f;
     return max_nan(z, e.lo) + res;
   }
   const float z2 = act_square(z);
@@ -91,38 +99,39 @@ __device__ __forceinline__ float act_value(const Epilogue &e, float z, float res
   return fmaf(z, p, res);
 }
 
-// Two values of an fp16 epilogue, products and sums paired: z0, z1 become the
-// results, sw their packed slopes; rw: their residual (zeros where there is none).
+// act(z) and the slopes of two values in fp16's accuracy (the slopes only of
+// kinds that have them).
 template <int kKind>
-__device__ __forceinline__ void act_pair(const Epilogue &e, float &z0, float &z1, uint32_t rw,
-                                         uint32_t &sw) {
-  const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&rw));
-  float s[2];
-  if constexpr (kKind == kEpMax) {
-    z0 = act_value<kEpMax, true>(e, z0, r.x, s[0]);
-    z1 = act_value<kEpMax, true>(e, z1, r.y, s[1]);
-  } else {
-    const float z[2] = {z0, z1}, res[2] = {r.x, r.y}, one[2] = {1.f, 1.f};
-    const float ka[2] = {e.nka, e.nka}, kb[2] = {e.nkb, e.nkb};
-    const float ca[2] = {e.ka, e.ka}, cb[2] = {3.f * e.kb, 3.f * e.kb};
-    float z2[2], v[2], p[2], q[2], t[2], y[2];
+__device__ __forceinline__ void act_pair(const Epilogue &e, const float (&z)[2], float (&y)[2],
+                                         float (&s)[2]) {
+  if constexpr (ep_is_max(kKind)) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) z2[j] = act_square(z[j]);
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (ep_has_slope(kKind)) s[j] = z[j] <= e.lo ? 0.f : 1.f;
+      y[j] = max_nan(z[j], e.lo);
+    }
+  } else {
+    const float one[2] = {1.f, 1.f}, ka[2] = {e.nka, e.nka}, kb[2] = {e.nkb, e.nkb};
+    const float ca[2] = {e.ka, e.ka}, cb[2] = {3.f * e.kb, 3.f * e.kb};
+    // below -1e4 act and slope are 0, and the slope's cubic factor stays finite
+    // beside a p of zero; above, z is beyond fp16 before the factor overflows
+    float c[2] = {fmaxf(z[0], -1e4f), fmaxf(z[1], -1e4f)};
+    float z2[2], v[2], p[2];
+    vec_mul(z2, c, c);
     vec_fma(v, kb, z2, ka);
-    vec_mul(v, v, z);
+    vec_mul(v, v, c);
 #pragma unroll
     for (int j = 0; j < 2; ++j) p[j] = rcp_fast(1.f + ex2_fast(v[j]));
-    vec_sub(q, one, p);
-    vec_fma(t, cb, z2, ca);
-    vec_mul(t, t, z);
-    vec_mul(t, t, q);
-    vec_fma(s, p, t, p);
-    vec_fma(y, z, p, res);
-    z0 = y[0];
-    z1 = y[1];
+    vec_mul(y, c, p);
+    if constexpr (ep_has_slope(kKind)) {
+      float q[2], t[2];
+      vec_sub(q, one, p);
+      vec_fma(t, cb, z2, ca);
+      vec_mul(t, t, c);
+      vec_mul(t, t, q);
+      vec_fma(s, p, t, p);
+    }
   }
-  const __half2 h = __floats2half2_rn(s[0], s[1]);
-  sw = *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // dz = dy slope on a packed fp16 pair, rounded once.

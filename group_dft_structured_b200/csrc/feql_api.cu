@@ -190,15 +190,30 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
   st = tf32 ? make_tmap_f32(&tm_in, in, N, static_cast<int64_t>(P.Ci) * kT)
             : make_tmap_f16(&tm_in, in, N, static_cast<int64_t>(P.Ci) * kT);
   if (st != FEQL_OK) return st;
-  CUtensorMap tm_res = tm_in;  // residual boxes: 32 rows x 16 channels
-  if (p.res_ring) st = make_tmap_f16(&tm_res, p.ep.res, N, static_cast<int64_t>(P.Do) * kT, 32);
-  if (st != FEQL_OK) return st;
+  CUtensorMap tm_res = tm_in;
+  if (p.res_ring) {  // kResBox: 32 rows x 8 channels
+    st = make_tmap_f16(&tm_res, p.ep.res, N, static_cast<int64_t>(P.Do) * kT, 32, 8 * kT);
+    if (st != FEQL_OK) return st;
+  }
   auto kernel = tf32 ? tc_fourier_gemm_kernel<true> : tc_fourier_gemm_kernel<false>;
-  if (ep != nullptr && epilogue_kind(*ep) == kEpSigmoid)
-    kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpSigmoid>
-                  : tc_fourier_gemm_kernel<false, kEpSigmoid>;
-  else if (ep != nullptr)
-    kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpMax> : tc_fourier_gemm_kernel<false, kEpMax>;
+  if (ep != nullptr) {
+    switch (epilogue_kind(*ep)) {
+      case kEpMax:
+        kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpMax> : tc_fourier_gemm_kernel<false, kEpMax>;
+        break;
+      case kEpMaxSlope:
+        kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpMax>
+                      : tc_fourier_gemm_kernel<false, kEpMaxSlope>;
+        break;
+      case kEpSigmoid:
+        kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpSigmoid>
+                      : tc_fourier_gemm_kernel<false, kEpSigmoid>;
+        break;
+      default:
+        kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpSigmoid>
+                      : tc_fourier_gemm_kernel<false, kEpSigmoidSlope>;
+    }
+  }
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return FEQL_ERR_CUDA;
   kernel<<<grid, kTcThreads, smem, stream>>>(tm_in, tm_res, p);
@@ -213,8 +228,8 @@ int launch_simt_fwd(const void *in, const float *Wp, const void *bias, void *out
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(Do, kSimtTile)));
   if (grid.y > 65535) return FEQL_ERR_UNSUPPORTED;
   auto kernel = ep == nullptr ? simt_fwd_kernel<T>
-                : epilogue_kind(*ep) == kEpSigmoid ? simt_fwd_kernel<T, kEpSigmoid>
-                                                   : simt_fwd_kernel<T, kEpMax>;
+                : ep_is_max(epilogue_kind(*ep)) ? simt_fwd_kernel<T, kEpMax>
+                                                : simt_fwd_kernel<T, kEpSigmoid>;
   kernel<<<grid, kSimtThreads, 0, stream>>>(
       static_cast<const T *>(in), Wp, static_cast<const T *>(bias), static_cast<T *>(out), N, Ci,
       Do, ep != nullptr ? *ep : Epilogue{});
@@ -439,6 +454,8 @@ int launch_g8_fwd(const void *in, const uint8_t *wt, const G8Plan &P, const __ha
   p.acc_stride = T * p.BD;
   p.stage_bytes = g8_xchunk<T>() + static_cast<int>(align_up(p.chunk_bytes, 1024));
   p.out_box = 32 * 16 * T;
+  p.ep = ep != nullptr ? *ep : Epilogue{};
+  p.res_box = p.ep.res != nullptr ? p.out_box : 0;
   p.bias_floats = p.nD * p.BD;
   const int budget = dev.smem_optin - 1024;
   // two staging boxes per epilogue warp when a unit has few input chunks (its
@@ -447,11 +464,13 @@ int launch_g8_fwd(const void *in, const uint8_t *wt, const G8Plan &P, const __ha
   int fit[3] = {0, 0, 0};
   for (int nout = 1; nout <= kG8MaxOut; ++nout) {
     p.nout = nout;
+    p.slope_box = p.ep.slope != nullptr ? nout * p.out_box : 0;
     p.stages = 6;
     while (p.stages > 2 && g8_fwd_smem(p).total > budget) --p.stages;
     fit[nout] = g8_fwd_smem(p).total > budget ? 0 : p.stages;
   }
   p.nout = ((p.nK <= 2 && fit[2] >= 3) || fit[2] >= 4 || fit[2] >= fit[1]) ? 2 : 1;
+  p.slope_box = p.ep.slope != nullptr ? p.nout * p.out_box : 0;
   p.stages = fit[p.nout];
   if (p.stages == 0) return FEQL_ERR_UNSUPPORTED;
   CUtensorMap tm, tm_out;
@@ -459,16 +478,23 @@ int launch_g8_fwd(const void *in, const uint8_t *wt, const G8Plan &P, const __ha
   if (st != FEQL_OK) return st;
   st = make_tmap_f16(&tm_out, out, N, static_cast<int64_t>(P.Do) * T, 32, 8 * T);
   if (st != FEQL_OK) return st;
+  CUtensorMap tm_res = tm_out, tm_slope = tm_out;  // the same boxes of the other tensors
+  if (p.res_box != 0)
+    st = make_tmap_f16(&tm_res, p.ep.res, N, static_cast<int64_t>(P.Do) * T, 32, 8 * T);
+  if (st == FEQL_OK && p.slope_box != 0)
+    st = make_tmap_f16(&tm_slope, p.ep.slope, N, static_cast<int64_t>(P.Do) * T, 32, 8 * T);
+  if (st != FEQL_OK) return st;
   const int smem = g8_fwd_smem(p).total + 1024;
   auto kernel = ep == nullptr ? tc_g8_fwd_kernel<Gp>
-                : epilogue_kind(*ep) == kEpSigmoid ? tc_g8_fwd_kernel<Gp, kEpSigmoid>
-                                                   : tc_g8_fwd_kernel<Gp, kEpMax>;
-  p.ep = ep != nullptr ? *ep : Epilogue{};
+                : epilogue_kind(*ep) == kEpMax      ? tc_g8_fwd_kernel<Gp, kEpMax>
+                : epilogue_kind(*ep) == kEpMaxSlope ? tc_g8_fwd_kernel<Gp, kEpMaxSlope>
+                : epilogue_kind(*ep) == kEpSigmoid  ? tc_g8_fwd_kernel<Gp, kEpSigmoid>
+                                                    : tc_g8_fwd_kernel<Gp, kEpSigmoidSlope>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return FEQL_ERR_CUDA;
   const int grid = p.n_units < dev.sms ? p.n_units : dev.sms;
-  kernel<<<grid, kG8Threads, smem, stream>>>(tm, tm_out, p);
+  kernel<<<grid, kG8Threads, smem, stream>>>(tm, tm_out, tm_res, tm_slope, p);
   return launch_status();
 }
 

@@ -79,6 +79,17 @@ struct G8Geo<8> {
       *reinterpret_cast<uint4 *>(row + (((4 * h + i) ^ (r & 7)) << 4)) =
           make_uint4(f[i][0], f[i][1], f[i][2], f[i][3]);
   }
+  // The same back.
+  __device__ static void get4(const uint8_t *row, int h, int r, uint32_t (&f)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(row + (((4 * h + i) ^ (r & 7)) << 4));
+      f[i][0] = v.x;
+      f[i][1] = v.y;
+      f[i][2] = v.z;
+      f[i][3] = v.w;
+    }
+  }
   // One fibre to global memory (16-byte aligned).
   __device__ static void store(__half *dst, const uint32_t (&h)[4]) {
     *reinterpret_cast<uint4 *>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -118,6 +129,17 @@ struct G8Geo<6> {
     dst[0] = make_uint4(f[0][0], f[0][1], f[0][2], f[1][0]);
     dst[1] = make_uint4(f[1][1], f[1][2], f[2][0], f[2][1]);
     dst[2] = make_uint4(f[2][2], f[3][0], f[3][1], f[3][2]);
+  }
+  // The same back.
+  __device__ static void get4(const uint8_t *row, int h, int, uint32_t (&f)[4][3]) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(row + 48 * h);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint4 v = src[k];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[(4 * k + i) / 3][(4 * k + i) % 3] = w[i];
+    }
   }
   // (4-byte aligned: fibres start at multiples of 12 bytes)
   __device__ static void store(__half *dst, const uint32_t (&h)[3]) {
@@ -633,21 +655,24 @@ struct G8FwdParams {
   int stages, stage_bytes, bias_floats;
   int out_box;         // one staging box: 32 rows x 8 channels x T fp16
   int nout;            // staging boxes per epilogue warp: 2, or 1 when that leaves room for a third stage
+  int res_box, slope_box;  // bytes of a warp's residual box and of its slope boxes, or 0
   Epilogue ep;         // activation, residual, saved slope (kernels with kEp)
 };
 
 struct G8Smem {
-  int stage0, out0, bias, bars, total;
+  int stage0, out0, res0, slope0, bias, bars, total;
 };
 
 __host__ __device__ inline G8Smem g8_fwd_smem(const G8FwdParams &p) {
   G8Smem s;
   s.stage0 = 0;
   s.out0 = p.stages * p.stage_bytes;
-  s.bias = s.out0 + kG8EpiWarps * p.nout * p.out_box;
+  s.res0 = s.out0 + kG8EpiWarps * p.nout * p.out_box;
+  s.slope0 = s.res0 + kG8EpiWarps * p.res_box;
+  s.bias = s.slope0 + kG8EpiWarps * p.slope_box;
   s.bars = s.bias + static_cast<int>(align_up(p.bias_floats * 4, 16));
-  // full, tready, empty per stage; acc_full, acc_empty x2; final; tmem slot
-  s.total = s.bars + (3 * p.stages + 4 + 1) * 8 + 16;
+  // full, tready, empty per stage; acc_full, acc_empty x2; final; tmem slot; residual boxes
+  s.total = s.bars + (3 * p.stages + 4 + 1) * 8 + 16 + kG8EpiWarps * 8;
   return s;
 }
 
@@ -676,13 +701,15 @@ struct G8Units {
 
 // 18 warps over the 4 SM sub-partitions put 5 warps on two 16K-register slices:
 // 5 x 32 x 96 = 15,360 registers fit, 104 would not.
-// kEp != kEpNone: y = res + act(z) (act.cuh).  A lane holds whole fibres of its token row, so
-// it reads the residual and writes the slope directly, 16 bytes at a time; y goes through
-// the staging box as always.
+// kEp != kEpNone: y = res + act(z) (act.cuh).  Residual and slopes move as y does: the
+// residual by TMA into a box of each epilogue warp, its next one loaded as soon as
+// one has been read, the slopes through boxes beside y's (direct accesses, a row of
+// 128 bytes to a lane, took 65 us instead of 45 on 50000 x 12 -> 48, p4m).
 template <class Gp, int kEp = kEpNone>
 __global__ void __maxnreg__(96)
 tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
-                  const G8FwdParams p) {
+                 const __grid_constant__ CUtensorMap tm_res,
+                 const __grid_constant__ CUtensorMap tm_slope, const G8FwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -699,9 +726,11 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
   uint64_t *acc_empty = acc_full + 2;
   uint64_t *final_bar = acc_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(final_bar + 1);
+  uint64_t *res_full = final_bar + 3;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kG8EpiWarps; ++i) mbar_init(&res_full[i], 1);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&tready[s], 8);
@@ -820,6 +849,31 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
     int last_g = -1;  // this team's last 8-channel group of a unit
     for (int g = team; g < groups; g += 2) last_g = g;
     uint8_t *obase = smem + L.out0 + ew * p.nout * p.out_box;
+    uint8_t *sbase = smem + L.slope0 + ew * p.slope_box;
+    // residual boxes: the group that the next load is for
+    const bool ring = kEp != kEpNone && p.res_box != 0;
+    const uint8_t *rbox = smem + L.res0 + ew * p.res_box;
+    G8Units ahead(p);
+    int ahead_g = team;
+    uint32_t rph = 0;
+    bool flying = false;
+    auto issue_res = [&]() {
+      // on to a group with channels
+      while (ahead.valid && (ahead_g >= groups || ahead.j * p.BD + ahead_g * 8 >= p.Do)) {
+        ahead_g = team;
+        ahead.next();
+        if (team >= groups) return;  // this team has none at all
+      }
+      flying = ahead.valid;
+      if (!flying) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&res_full[ew], p.res_box);
+        tma_load_2d(smem + L.res0 + ew * p.res_box, &tm_res, (ahead.j * p.BD + ahead_g * 8) * T,
+                    ahead.m * kBM + quad * 32, &res_full[ew]);
+      }
+      ahead_g += 2;
+    };
+    if (ring) issue_res();
     int a = 0, oi = 0;
     uint32_t aph = 0;
     for (G8Units U(p); U.valid; U.next()) {
@@ -834,7 +888,13 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + a * p.acc_stride;
       for (int g = team; g < groups; g += 2) {
         const int d0 = j * p.BD + g * 8;
-        uint8_t *ob = obase + (p.nout == 2 ? (oi & 1) : 0) * p.out_box;
+        const int obi = p.nout == 2 ? (oi & 1) : 0;
+        uint8_t *ob = obase + obi * p.out_box, *sb = sbase + obi * p.out_box;
+        if (ring && d0 < p.Do && ok) {
+          ok = mbar_wait(&res_full[ew], rph);
+          rph ^= 1;
+          flying = false;
+        }
         if (d0 < p.Do) {
           if (lane == 0) {  // this box's last store has read it
             if (p.nout == 2)
@@ -858,24 +918,8 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
           }
           if (d0 >= p.Do) continue;  // whole group is padding
           uint32_t hv[4][T / 2];  // fibres of channels d0 + 4h .. d0 + 4h + 3, packed fp16
-          // kEp: this lane's residual and slopes, 2 T words of 16-byte pieces: a piece
-          // is one channel's fibre (T = 8) or a third of four (T = 6, Do % 4 == 0)
-          uint32_t rw[2 * T], sw[2 * T];
-          const int64_t row = static_cast<int64_t>(m) * kBM + quad * 32 + lane;
-          const int64_t at = (row * p.Do + d0 + 4 * h) * T;
-          if constexpr (kEp != kEpNone) {
-#pragma unroll
-            for (int q = 0; q < T / 2; ++q) {
-              uint4 v = {};
-              if (p.ep.res != nullptr && row < p.N && d0 + 4 * h + (T == 8 ? q : 3) < p.Do)
-                v = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.ep.res) + at +
-                                                     8 * q);
-              rw[4 * q] = v.x;
-              rw[4 * q + 1] = v.y;
-              rw[4 * q + 2] = v.z;
-              rw[4 * q + 3] = v.w;
-            }
-          }
+          uint32_t rw[4][T / 2] = {}, sw[4][T / 2];  // residual and slopes likewise
+          if (kEp != kEpNone && ring) Geo::get4(rbox + lane * Geo::kRow, h, lane, rw);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float F[T], y[T];
@@ -885,19 +929,19 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
             const float bv = sbias[d0 + 4 * h + i];
 #pragma unroll
             for (int e = 0; e < T / 2; ++e) {
-              float z0 = y[2 * e] + bv, z1 = y[2 * e + 1] + bv;
-              if constexpr (kEp != kEpNone)
-                act_pair<kEp>(p.ep, z0, z1, rw[i * (T / 2) + e], sw[i * (T / 2) + e]);
-              hv[i][e] = pack_half2(z0, z1);
+              float z[2] = {y[2 * e] + bv, y[2 * e + 1] + bv};
+              if constexpr (kEp != kEpNone) {
+                float sl[2] = {};
+                act_pair<kEp>(p.ep, z, z, sl);
+                const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&rw[i][e]));
+                z[0] += r.x;
+                z[1] += r.y;
+                sw[i][e] = pack_half2(sl[0], sl[1]);
+              }
+              hv[i][e] = pack_half2(z[0], z[1]);
             }
           }
-          if constexpr (kEp != kEpNone) {
-#pragma unroll
-            for (int q = 0; q < T / 2; ++q)
-              if (p.ep.slope != nullptr && row < p.N && d0 + 4 * h + (T == 8 ? q : 3) < p.Do)
-                *reinterpret_cast<uint4 *>(static_cast<__half *>(p.ep.slope) + at + 8 * q) =
-                    make_uint4(sw[4 * q], sw[4 * q + 1], sw[4 * q + 2], sw[4 * q + 3]);
-          }
+          if constexpr (ep_has_slope(kEp)) Geo::put4(sb + lane * Geo::kRow, h, lane, sw);
           Geo::put4(ob + lane * Geo::kRow, h, lane, hv);
         }
         if (d0 >= p.Do) continue;
@@ -905,13 +949,16 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
         __syncwarp();
         if (lane == 0) {  // the store clips rows past N and channels past Do
           tma_store_2d(&tm_out, d0 * T, m * kBM + quad * 32, ob);
+          if (ep_has_slope(kEp)) tma_store_2d(&tm_slope, d0 * T, m * kBM + quad * 32, sb);
           bulk_commit();
         }
         ++oi;
+        if (ring && ok) issue_res();  // every lane has read the box (the barrier above)
       }
       if (++a == p.nacc) { a = 0; aph ^= 1; }
     }
     if (lane == 0) bulk_wait<0>();
+    if (ring && flying) mbar_wait(&res_full[ew], rph);  // (gave up: none left in flight)
   }
 
   tc_fence_before();

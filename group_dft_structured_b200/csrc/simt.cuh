@@ -261,11 +261,20 @@ __global__ void dw_reduce_kernel(const float *__restrict__ ws, const float *__re
        e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     if (e < plane) {
       float g[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8  // loads of eight splits in flight; the sums stay in order
-      for (int s = 0; s < splits; ++s) {
+      // eight splits' values in flight; the sums stay in order
+      for (int s = 0; s < splits; s += 8) {
         const float *p = ws + static_cast<int64_t>(s) * 4 * plane + e;
+        float v[8][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) g[k] += p[k * plane];
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[i][k] = s + i < splits ? __ldg(p + (4ll * i + k) * plane) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (s + i < splits) g[k] += v[i][k];
       }
       float w[4];
       irdft4(g[0], g[1], g[2], g[3], w);
@@ -273,8 +282,15 @@ __global__ void dw_reduce_kernel(const float *__restrict__ ws, const float *__re
     } else if (db != nullptr) {
       const int d = static_cast<int>(e - plane);
       float s = 0.f;
-#pragma unroll 16
-      for (int k = 0; k < splits; ++k) s += ws_db[static_cast<int64_t>(k) * D + d];
+      for (int k = 0; k < splits; k += 16) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[i] = k + i < splits ? __ldg(ws_db + static_cast<int64_t>(k + i) * D + d) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (k + i < splits) s += v[i];
+      }
       db[d] = static_cast<T>(s);
     }
   }

@@ -27,8 +27,8 @@ int ct_simt_pass_launch(const void *in, const float *Wp, const void *bias, void 
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(Do, kCtTile)));
   if (grid.y > 65535) return FEQL_ERR_UNSUPPORTED;
   auto kernel = ep == nullptr ? ct_simt_fwd_kernel<T, Ty>
-                : epilogue_kind(*ep) == kEpSigmoid ? ct_simt_fwd_kernel<T, Ty, kEpSigmoid>
-                                                   : ct_simt_fwd_kernel<T, Ty, kEpMax>;
+                : ep_is_max(epilogue_kind(*ep)) ? ct_simt_fwd_kernel<T, Ty, kEpMax>
+                                                : ct_simt_fwd_kernel<T, Ty, kEpSigmoid>;
   kernel<<<grid, kCtThreads, 0, s>>>(static_cast<const Ty *>(in), Wp,
                                      static_cast<const Ty *>(bias), static_cast<Ty *>(out), N, Ci,
                                      Do, ep != nullptr ? *ep : Epilogue{});

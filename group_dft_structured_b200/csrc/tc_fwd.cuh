@@ -63,17 +63,24 @@ constexpr bool kSkipFirstRelease = false;
 constexpr int kTcWarps = 20;
 constexpr int kTcThreads = kTcWarps * 32;
 constexpr int kTcEpi0 = 12;                       // first epilogue warp
+constexpr int kEpTeams = 3;                       // epilogue teams of the kEp kernels
+constexpr int kEpFirst = 8;                       // their first warp (warps 8 .. 19)
 
 // Transform ordinal (0..4*kTeams-1) of warp w, or -1 when w is not a transform warp.
 __device__ __forceinline__ int tc_xf_ordinal(int w) {
   if (w < 2 || w >= kTcEpi0 || w == 5 || w == 9) return -1;
   return w - 2 - (w > 5) - (w > 9);
 }
+
+// The same for the kEp kernels' one transform team: warps 2, 3, 4 and 6.
+__device__ __forceinline__ int tc_ep_xf_ordinal(int w) {
+  return w < 2 || w > 6 || w == 5 ? -1 : w - 2 - (w > 5);
+}
 constexpr int kXChunkBytes = kBM * kCK * kT * 2;  // 16 KB: 128 rows x 128 B
 constexpr int kPlaneBytes = kBM * kCK * 2;        // 4 KB: 128 rows x 32 B
 constexpr int kTmemCols = 512;
-constexpr int kResDepth = 2;                      // residual boxes in flight per epilogue warp
-constexpr int kResBox = 32 * 128;                 // 4 KB: 32 rows x 16 channels x 4 fp16
+constexpr int kResDepth = 3;                      // residual boxes in flight per epilogue warp
+constexpr int kResBox = 32 * 64;                  // 2 KB: 32 rows x 8 channels x 4 fp16
 
 struct TcFwdParams {
   const uint8_t *wt;    // weight chunks of this direction
@@ -104,11 +111,11 @@ __host__ __device__ inline TcSmem tc_fwd_smem(const TcFwdParams &p) {
   s.wres = 0;
   s.stage0 = p.resident ? p.wres_bytes : 0;
   s.res = s.stage0 + p.stages * p.stage_bytes;
-  s.bias = s.res + (p.res_ring ? 4 * kTeams * kResDepth * kResBox : 0);
+  s.bias = s.res + (p.res_ring ? 4 * kEpTeams * kResDepth * kResBox : 0);
   s.bars = s.bias + static_cast<int>(align_up(p.bias_floats * 4, 16));
   // full, tready, empty per stage; acc_full, acc_empty per acc buffer; final; wfull; tmem
   // slot; residual boxes
-  s.total = s.bars + (3 * p.stages + 2 * 2 + 2) * 8 + 16 + 4 * kTeams * kResDepth * 8;
+  s.total = s.bars + (3 * p.stages + 2 * 2 + 2) * 8 + 16 + 4 * kEpTeams * kResDepth * 8;
   return s;
 }
 
@@ -160,12 +167,17 @@ struct TcUnits {
 // fp32 rows.  Bins are not scaled (fp32 has the range).
 //
 // kEp != kEpNone: y = res + act(z) in the epilogue (act.cuh), the slope act'(z)
-// stored beside y when the backward pass will want it.  An fp16 residual comes
-// by TMA: each epilogue warp loads the 32-row x 16-channel boxes (4 KB) of its
-// own column groups, in the order in which it will use them, into a private
-// ring of kResDepth slots, so the loads run kResDepth groups ahead (direct loads
-// in the group that uses them cost an HBM latency each: 123 us instead of
-// 78 us on 65536 x 192 -> 192).
+// stored beside y when the backward pass will want it.  The epilogue then has the
+// most work (some 13 instructions per value with an activation and its slope, on
+// two or three warps per SM sub-partition), so the warps are dealt out anew: one
+// transform team and three epilogue teams, which share every tile's 8-channel
+// blocks (401408 x 24 -> 96 with GELU and slopes: 199 us with two and two, 172 us
+// so; two and three need 24 warps of 80 registers, which spill: 210 us).  An fp16
+// residual comes by TMA: each epilogue warp loads the 32-row x 8-channel boxes
+// (2 KB) of its own blocks, in the order in which it will use them, into a private
+// ring of kResDepth slots, so the loads run kResDepth blocks ahead (direct loads in
+// the block that uses them cost an HBM
+// latency each: 123 us instead of 78 us on 65536 x 192 -> 192).
 template <bool kTF32, int kEp = kEpNone>
 __global__ void __maxnreg__(96)
 tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
@@ -190,7 +202,7 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
 
   if (threadIdx.x == 0) {
     if (kEp != kEpNone)
-      for (int i = 0; i < 4 * kTeams * kResDepth; ++i) mbar_init(&res_full[i], 1);
+      for (int i = 0; i < 4 * kEpTeams * kResDepth; ++i) mbar_init(&res_full[i], 1);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&tready[s], 4);
@@ -198,7 +210,8 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], p.nacc == 1 ? 4 * kTeams : 4);  // single buffer: all teams release
+      // all teams release a single buffer, and any buffer of the kEp kernels
+      mbar_init(&acc_empty[a], kEp != kEpNone ? 4 * kEpTeams : (p.nacc == 1 ? 4 * kTeams : 4));
     }
     mbar_init(final_bar, 1);
     mbar_init(wfull, 1);
@@ -320,17 +333,18 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
       mma_commit(final_bar);
       mbar_wait(final_bar, 0);
     }
-  } else if (tc_xf_ordinal(warp) >= 0) {
+  } else if ((kEp != kEpNone ? tc_ep_xf_ordinal(warp) : tc_xf_ordinal(warp)) >= 0) {
     // ---------------------------------------------------------- transform
     // kTeams teams of 4 warps take alternate chunks of the ring.
-    const int xo = tc_xf_ordinal(warp);
+    constexpr int kXfTeams = kEp != kEpNone ? 1 : kTeams;
+    const int xo = kEp != kEpNone ? tc_ep_xf_ordinal(warp) : tc_xf_ordinal(warp);
     const int team = xo / 4;
     const int r = (xo % 4) * 32 + lane;  // row of the chunk (token within the tile)
     int s = 0, c = 0;
     uint32_t ph = 0;
     for (TcUnits U(p); U.valid; U.next()) {
       for (int kc = 0; kc < p.nK; ++kc, ++c) {
-        if (c % kTeams != team) {
+        if (c % kXfTeams != team) {
           if (++s == p.stages) { s = 0; ph ^= 1; }
           continue;
         }
@@ -389,7 +403,175 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
         if (++s == p.stages) { s = 0; ph ^= 1; }
       }
     }
-  } else if (warp >= kTcEpi0) {
+  } else if (kEp != kEpNone && warp >= kEpFirst) {
+    // ------------------------------ epilogue with activation and residual
+    // As below, but all teams share every tile: team t takes the 8-channel
+    // blocks t, t + kEpTeams, ...
+    const int ew = warp - kEpFirst, eteam = ew / 4;
+    const int quad = warp & 3;
+    const int blocks = p.BD / 8;
+    const int last = eteam < blocks ? eteam + (blocks - 1 - eteam) / kEpTeams * kEpTeams : -1;
+    const int tcp = 2 * (lane & 3);
+    const int64_t row_elems = static_cast<int64_t>(p.Do) * kT;
+    // the residual ring: the block that the next load is for, slots issued and used
+    const bool ring = !kTF32 && p.res_ring && last >= 0;
+    uint8_t *rbox = smem + L.res + ew * kResDepth * kResBox;
+    uint64_t *rbar = res_full + ew * kResDepth;
+    TcUnits ahead(p);
+    int ahead_b = eteam, islot = 0, uslot = 0, flying = 0;
+    uint32_t uph = 0;
+    auto issue_res = [&]() {
+      if (!ahead.valid) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&rbar[islot], kResBox);
+        tma_load_2d(rbox + islot * kResBox, &tm_res, (ahead.j * p.BD + ahead_b * 8) * kT,
+                    ahead.m * kBM + quad * 32, &rbar[islot]);
+      }
+      ++flying;
+      if (++islot == kResDepth) islot = 0;
+      ahead_b += kEpTeams;
+      if (ahead_b > last) {
+        ahead_b = eteam;
+        ahead.next();
+      }
+    };
+    if (ring) {
+      if (lane == 0) tma_prefetch_desc(&tm_res);
+      for (int i = 0; i < kResDepth; ++i) issue_res();
+    }
+    int a = 0;
+    uint32_t aph = 0;
+    for (TcUnits U(p); U.valid; U.next()) {
+      const int m = U.m, j = U.j;
+      if (ok) ok = mbar_wait(&acc_full[a], aph);
+      tc_fence_after();
+      if (last < 0) {  // this team reads nothing of the tile
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&acc_empty[a]);
+      }
+      const uint32_t tl = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + a * p.acc_stride;
+      const int64_t row0 = static_cast<int64_t>(m) * kBM + quad * 32 + (lane >> 2);
+      for (int blk = eteam; blk < blocks; blk += kEpTeams) {
+        const int c = blk * 8;
+        const int d = j * p.BD + c + tcp;  // this thread's first output channel
+        uint32_t y0[2][4], y2[2][4], yr[2][4], yi[2][4];
+        float4 rv[2][2][2];  // fp32 residual, loaded while the accumulators are awaited
+        if constexpr (kTF32) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int hf = i >> 2, rr = (i >> 1) & 1, cc = i & 1;
+            const int64_t row = row0 + 16 * hf + 8 * rr;
+            rv[hf][rr][cc] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p.ep.res != nullptr && row < p.N && d + cc < p.Do)
+              rv[hf][rr][cc] = *reinterpret_cast<const float4 *>(
+                  static_cast<const float *>(p.ep.res) + row * row_elems +
+                  static_cast<int64_t>(d + cc) * kT);
+          }
+        }
+        __syncwarp();  // the TMEM loads are warp-collective
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t col = tl + (static_cast<uint32_t>(16 * hf) << 16) + c;
+          tmem_ld16x256(col, y0[hf]);
+          tmem_ld16x256(col + p.BD, y2[hf]);
+          tmem_ld16x256(col + 2 * p.BD, yr[hf]);
+          tmem_ld16x256(col + 3 * p.BD, yi[hf]);
+        }
+        tmem_ld_wait();
+        if (blk == last) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&acc_empty[a]);
+        }
+        if (ring && ok) ok = mbar_wait(&rbar[uslot], uph);
+        const uint8_t *rslot = rbox + uslot * kResBox + lane * 16;  // + 512 per 8 rows
+        if constexpr (kTF32) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int hf = i >> 2, rr = (i >> 1) & 1, cc = i & 1, k = 2 * rr + cc;
+            const int64_t row = row0 + 16 * hf + 8 * rr;
+            const float Y0 = __uint_as_float(y0[hf][k]), Y2 = __uint_as_float(y2[hf][k]);
+            const float Yr = __uint_as_float(yr[hf][k]), Yi = __uint_as_float(yi[hf][k]);
+            if (row < p.N && d + cc < p.Do) {
+              const float bv = sbias[d + cc];
+              const float e = fmaf(0.25f, Y0 + Y2, bv), o = fmaf(0.25f, Y0 - Y2, bv);
+              const int64_t at = row * row_elems + static_cast<int64_t>(d + cc) * kT;
+              const float4 r = rv[hf][rr][cc];
+              float4 s, q;
+              q.x = act_value<kEp, false>(p.ep, fmaf(0.5f, Yr, e), r.x, s.x);
+              q.y = act_value<kEp, false>(p.ep, fmaf(-0.5f, Yi, o), r.y, s.y);
+              q.z = act_value<kEp, false>(p.ep, fmaf(-0.5f, Yr, e), r.z, s.z);
+              q.w = act_value<kEp, false>(p.ep, fmaf(0.5f, Yi, o), r.w, s.w);
+              if (p.ep.slope != nullptr)
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.ep.slope) + at) = s;
+              *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = q;
+            }
+          }
+        } else {
+          // Do is even: a thread's channel pair is whole or padding
+          const bool pair = d + 2 <= p.Do;
+          const float bv[2] = {pair ? sbias[d] : 0.f, pair ? sbias[d + 1] : 0.f};
+          const float k4[2] = {4.f, 4.f}, k8[2] = {8.f, 8.f}, n8[2] = {-8.f, -8.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int hf = i >> 1, rr = i & 1;
+            const int64_t row = row0 + 16 * hf + 8 * rr;
+            float Y0[2], Y2[2], Yr[2], Yi[2], e[2], o[2], v[4][2], s[4][2];
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              Y0[cc] = __uint_as_float(y0[hf][2 * rr + cc]);
+              Y2[cc] = __uint_as_float(y2[hf][2 * rr + cc]);
+              Yr[cc] = __uint_as_float(yr[hf][2 * rr + cc]);
+              Yi[cc] = __uint_as_float(yi[hf][2 * rr + cc]);
+            }
+            // planes and weights are both stored divided by 4 (Y = 16 * acc)
+            vec_add(e, Y0, Y2);
+            vec_sub(o, Y0, Y2);
+            vec_fma(e, k4, e, bv);
+            vec_fma(o, k4, o, bv);
+            vec_fma(v[0], k8, Yr, e);
+            vec_fma(v[1], n8, Yi, o);
+            vec_fma(v[2], n8, Yr, e);
+            vec_fma(v[3], k8, Yi, o);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) act_pair<kEp>(p.ep, v[t], v[t], s[t]);
+            if (ring) {
+              const uint4 r4 = *reinterpret_cast<const uint4 *>(rslot + (2 * hf + rr) * 512);
+              const float2 a0 = __half22float2(as_h2(r4.x)), a1 = __half22float2(as_h2(r4.y));
+              const float2 c0 = __half22float2(as_h2(r4.z)), c1 = __half22float2(as_h2(r4.w));
+              const float r[4][2] = {{a0.x, c0.x}, {a0.y, c0.y}, {a1.x, c1.x}, {a1.y, c1.y}};
+#pragma unroll
+              for (int t = 0; t < 4; ++t) vec_add(v[t], v[t], r[t]);
+            }
+            if (pair && row < p.N) {
+              const int64_t at = row * row_elems + static_cast<int64_t>(d) * kT;
+              if (ep_has_slope(kEp))
+                *reinterpret_cast<uint4 *>(static_cast<__half *>(p.ep.slope) + at) =
+                    make_uint4(pack_half2(s[0][0], s[1][0]), pack_half2(s[2][0], s[3][0]),
+                               pack_half2(s[0][1], s[1][1]), pack_half2(s[2][1], s[3][1]));
+              *reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + at) =
+                  make_uint4(pack_half2(v[0][0], v[1][0]), pack_half2(v[2][0], v[3][0]),
+                             pack_half2(v[0][1], v[1][1]), pack_half2(v[2][1], v[3][1]));
+            }
+          }
+        }
+        if (ring) {
+          --flying;
+          if (++uslot == kResDepth) { uslot = 0; uph ^= 1; }
+          __syncwarp();  // every lane has read the slot that the next load overwrites
+          if (ok) issue_res();
+        }
+      }
+      if (++a == p.nacc) { a = 0; aph ^= 1; }
+    }
+    // a warp that gave up waiting still has loads of its own in flight
+    if (ring && !ok)
+      for (; flying > 0; --flying) {
+        mbar_wait(&rbar[uslot], uph);
+        if (++uslot == kResDepth) { uslot = 0; uph ^= 1; }
+      }
+  } else if (kEp == kEpNone && warp >= kTcEpi0) {
     // ----------------------------------------------------------- epilogue
     // kTeams teams of 4 warps.  With double-buffered accumulators each team
     // owns one TMEM buffer (alternate tiles); with a single buffer the teams
@@ -407,33 +589,6 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
     int last_g = -1;
     for (int g = g0; g < groups; g += gstep) last_g = g;
     int it = 0;
-    // the residual ring: the group that the next load is for, slots issued and used
-    const bool ring = kEp != kEpNone && !kTF32 && p.res_ring && last_g >= 0;
-    uint8_t *rbox = smem + L.res + ew * kResDepth * kResBox;
-    uint64_t *rbar = res_full + ew * kResDepth;
-    TcUnits ahead(p);
-    int ahead_g = g0, issued = 0, used = 0;
-    if (!split && eteam == 1 && ahead.valid) ahead.next();  // this team takes the odd units
-    auto issue_res = [&]() {
-      if (!ahead.valid) return;
-      if (lane == 0) {
-        const int s = issued % kResDepth;
-        mbar_arrive_expect_tx(&rbar[s], kResBox);
-        tma_load_2d(rbox + s * kResBox, &tm_res, (ahead.j * p.BD + ahead_g * 16) * kT,
-                    ahead.m * kBM + quad * 32, &rbar[s]);
-      }
-      ++issued;
-      ahead_g += gstep;
-      if (ahead_g > last_g) {
-        ahead_g = g0;
-        ahead.next();
-        if (!split && ahead.valid) ahead.next();
-      }
-    };
-    if (ring) {
-      if (lane == 0) tma_prefetch_desc(&tm_res);
-      for (int i = 0; i < kResDepth; ++i) issue_res();
-    }
     for (TcUnits U(p); U.valid; U.next(), ++it) {
       const int m = U.m, j = U.j;
       if (!split && it % kTeams != eteam) continue;
@@ -454,26 +609,10 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
       const int64_t row0 = static_cast<int64_t>(m) * kBM + quad * 32 + (lane >> 2);
       const int64_t row_elems = static_cast<int64_t>(p.Do) * kT;
       for (int g = g0; g < groups; g += gstep) {
-        const uint8_t *rslot = rbox + (used % kResDepth) * kResBox;
-        if (ring && ok) ok = mbar_wait(&rbar[used % kResDepth], (used / kResDepth) & 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int c = g * 16 + h * 8;
           uint32_t y0[2][4], y2[2][4], yr[2][4], yi[2][4];
-          float4 rv[2][2][2];  // fp32 residual, loaded while the accumulators are awaited
-          if constexpr (kEp != kEpNone && kTF32) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int hf = i >> 2, rr = (i >> 1) & 1, cc = i & 1;
-              const int64_t row = row0 + 16 * hf + 8 * rr;
-              const int d = j * p.BD + c + tcp + cc;
-              rv[hf][rr][cc] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (p.ep.res != nullptr && row < p.N && d < p.Do)
-                rv[hf][rr][cc] = *reinterpret_cast<const float4 *>(
-                    static_cast<const float *>(p.ep.res) + row * row_elems +
-                    static_cast<int64_t>(d) * kT);
-            }
-          }
           __syncwarp();  // the TMEM loads are warp-collective
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -505,22 +644,11 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
                   const float Yr = __uint_as_float(yr[hf][i]), Yi = __uint_as_float(yi[hf][i]);
                   const float bv = d + cc < p.Do ? sbias[d + cc] : 0.f;
                   const float e = fmaf(0.25f, Y0 + Y2, bv), o = fmaf(0.25f, Y0 - Y2, bv);
-                  if (row < p.N && d + cc < p.Do) {
-                    const int64_t at = row * row_elems + static_cast<int64_t>(d + cc) * kT;
-                    float4 q = make_float4(fmaf(0.5f, Yr, e), fmaf(-0.5f, Yi, o),
-                                           fmaf(-0.5f, Yr, e), fmaf(0.5f, Yi, o));
-                    if constexpr (kEp != kEpNone) {
-                      const float4 r = rv[hf][rr][cc];
-                      float4 s;
-                      q = make_float4(act_value<kEp, false>(p.ep, q.x, r.x, s.x),
-                                      act_value<kEp, false>(p.ep, q.y, r.y, s.y),
-                                      act_value<kEp, false>(p.ep, q.z, r.z, s.z),
-                                      act_value<kEp, false>(p.ep, q.w, r.w, s.w));
-                      if (p.ep.slope != nullptr)
-                        *reinterpret_cast<float4 *>(static_cast<float *>(p.ep.slope) + at) = s;
-                    }
-                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = q;
-                  }
+                  if (row < p.N && d + cc < p.Do)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * row_elems +
+                                                static_cast<int64_t>(d + cc) * kT) =
+                        make_float4(fmaf(0.5f, Yr, e), fmaf(-0.5f, Yi, o), fmaf(-0.5f, Yr, e),
+                                    fmaf(0.5f, Yi, o));
                 }
               }
             }
@@ -532,15 +660,7 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
           for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {  // rows r0 and r0 + 8
-              uint32_t w[4], ws[4];
-              uint4 rv = {};
-              if constexpr (kEp != kEpNone) {
-                const int r = (lane >> 2) + 16 * hf + 8 * rr;  // row of the box
-                if (ring)
-                  rv = *reinterpret_cast<const uint4 *>(
-                      rslot + r * 128 + (((4 * h + (lane & 3)) ^ (r & 7)) << 4));
-              }
-              const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
+              uint32_t w[4];
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
                 const int i = 2 * rr + cc;
@@ -549,23 +669,10 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
                 const float bv = cc ? b1 : b0;
                 // planes and weights are both stored divided by 4 (Y = 16 * acc)
                 const float e = fmaf(4.f, Y0 + Y2, bv), o = fmaf(4.f, Y0 - Y2, bv);
-                float v[4] = {fmaf(8.f, Yr, e), fmaf(-8.f, Yi, o), fmaf(-8.f, Yr, e),
-                              fmaf(8.f, Yi, o)};
-                if constexpr (kEp != kEpNone) {
-#pragma unroll
-                  for (int q = 0; q < 2; ++q)
-                    act_pair<kEp>(p.ep, v[2 * q], v[2 * q + 1], rw[2 * cc + q], ws[2 * cc + q]);
-                }
-                w[2 * cc] = pack_half2(v[0], v[1]);
-                w[2 * cc + 1] = pack_half2(v[2], v[3]);
+                w[2 * cc] = pack_half2(fmaf(8.f, Yr, e), fmaf(-8.f, Yi, o));
+                w[2 * cc + 1] = pack_half2(fmaf(-8.f, Yr, e), fmaf(8.f, Yi, o));
               }
               const int64_t row = row0 + 16 * hf + 8 * rr;
-              if constexpr (kEp != kEpNone) {
-                if (p.ep.slope != nullptr && row < p.N)
-                  *reinterpret_cast<uint4 *>(static_cast<__half *>(p.ep.slope) + row * row_elems +
-                                             static_cast<int64_t>(d) * kT) =
-                      make_uint4(ws[0], ws[1], ws[2], ws[3]);
-              }
               if (row < p.N)
                 *reinterpret_cast<uint4 *>(static_cast<__half *>(p.out) + row * row_elems +
                                            static_cast<int64_t>(d) * kT) =
@@ -573,16 +680,8 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
             }
           }
         }
-        if (ring) {
-          ++used;
-          __syncwarp();  // every lane has read the slot that the next load overwrites
-          if (ok) issue_res();
-        }
       }
     }
-    // a warp that gave up waiting still has loads of its own in flight
-    if (ring && !ok)
-      for (; used < issued; ++used) mbar_wait(&rbar[used % kResDepth], (used / kResDepth) & 1);
   }
 
   tc_fence_before();

@@ -84,60 +84,29 @@ struct Pack {
   }
 };
 
-// fp32 vectors of V values, two to an instruction where V allows (sm_100's paired
-// fp32 pipe): the same roundings as one by one.
+// fp32 vectors of V values.  (The paired fp32 instructions were measured: fewer issue
+// slots, no time won, 104 against 99 us in the recurrence's backward and 351 against
+// 328 us in the layer's training step through GELU.)
 template <int V>
 __device__ __forceinline__ void vec_fma(float (&d)[V], const float (&a)[V], const float (&b)[V],
                                         const float (&c)[V]) {
-  if constexpr (V % 2 == 0) {
 #pragma unroll
-    for (int j = 0; j < V; j += 2)
-      asm("{.reg .b64 a, b, c, d;\n\t"
-          "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-          "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
-          : "=f"(d[j]), "=f"(d[j + 1])
-          : "f"(a[j]), "f"(a[j + 1]), "f"(b[j]), "f"(b[j + 1]), "f"(c[j]), "f"(c[j + 1]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] = fmaf(a[j], b[j], c[j]);
-  }
+  for (int j = 0; j < V; ++j) d[j] = fmaf(a[j], b[j], c[j]);
 }
 template <int V>
 __device__ __forceinline__ void vec_mul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
-  if constexpr (V % 2 == 0) {
 #pragma unroll
-    for (int j = 0; j < V; j += 2)
-      asm("{.reg .b64 a, b, d;\n\t"
-          "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-          "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
-          : "=f"(d[j]), "=f"(d[j + 1])
-          : "f"(a[j]), "f"(a[j + 1]), "f"(b[j]), "f"(b[j + 1]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] = a[j] * b[j];
-  }
+  for (int j = 0; j < V; ++j) d[j] = a[j] * b[j];
 }
 template <int V>
 __device__ __forceinline__ void vec_add(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
-  if constexpr (V % 2 == 0) {
 #pragma unroll
-    for (int j = 0; j < V; j += 2)
-      asm("{.reg .b64 a, b, d;\n\t"
-          "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-          "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
-          : "=f"(d[j]), "=f"(d[j + 1])
-          : "f"(a[j]), "f"(a[j + 1]), "f"(b[j]), "f"(b[j + 1]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] = a[j] + b[j];
-  }
+  for (int j = 0; j < V; ++j) d[j] = a[j] + b[j];
 }
 template <int V>
 __device__ __forceinline__ void vec_sub(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
-  float n[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) n[j] = -1.f;
-  vec_fma(d, b, n, a);
+  for (int j = 0; j < V; ++j) d[j] = a[j] - b[j];
 }
 // Gate values of a row spread over its V features: themselves, or the one.
 template <int V, int GV>
