@@ -122,14 +122,17 @@ __device__ __forceinline__ void act_pair(const Epilogue &e, const float (&z)[2],
     vec_mul(v, v, c);
 #pragma unroll
     for (int j = 0; j < 2; ++j) p[j] = rcp_fast(1.f + ex2_fast(v[j]));
-    vec_mul(y, c, p);
+    // (not contracted with the residual's sum: the same y with and without slopes; z is
+    // read no more, y may be its place)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) y[j] = __fmul_rn(c[j], p[j]);
     if constexpr (ep_has_slope(kKind)) {
+      // p + z p (1 - p) v'(z), and z p is y
       float q[2], t[2];
       vec_sub(q, one, p);
       vec_fma(t, cb, z2, ca);
-      vec_mul(t, t, c);
-      vec_mul(t, t, q);
-      vec_fma(s, p, t, p);
+      vec_mul(t, t, y);
+      vec_fma(s, t, q, p);
     }
   }
 }

@@ -1105,7 +1105,9 @@ static int backward_act(GroupKind G, const void *x, const void *dy, const void *
     if (!G.p4m && G.T == kT && dx != nullptr && dW != nullptr && is_tc(resolve(dtype, C, D))) {
       const WhatLayout L = make_what_layout(C, D, kWhatF16);
       TcBwdParams p;
-      if (make_tc_bwd_plan(N, C, D, L, dev, p, true))
+      // (the regular dW workspace covers the fused plan, as in feql_backward)
+      if (make_tc_bwd_plan(N, C, D, L, dev, p, true) &&
+          w.dw >= static_cast<size_t>(p.splits) * (4ull * p.D * p.Cs + p.D) * 4)
         return launch_tc_bwd(p, x, dy, static_cast<const uint8_t *>(What) + L.off_dx,
                              static_cast<__half *>(dx), static_cast<__half *>(dW),
                              static_cast<__half *>(db), static_cast<float *>(ws), dev, s, slope);

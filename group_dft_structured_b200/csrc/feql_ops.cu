@@ -187,7 +187,7 @@ struct ScanPlan {
 // Rows per thread: what keeps the values in use within 128 registers, so that
 // two blocks of 256 threads share an SM.
 constexpr int scan_rows_fwd(bool half, int V) { return V == 4 && !half ? 4 : 8; }
-constexpr int scan_rows_bwd(int V) { return V == 4 ? 4 : 8; }
+constexpr int scan_rows_bwd(bool half, int V) { return half ? (V == 4 ? 4 : 8) : 8 / V; }
 
 // A thread's features are V neighbours: 4, or fewer where a row (or, for
 // shared gates, a channel) is not a multiple of 4.  One warp per block walks
@@ -224,7 +224,7 @@ ScanPlan scan_plan(int B, int64_t N, int C, int T, bool shared, bool packed, boo
   q.s.ntiles = static_cast<int>(ceil_div(F, q.s.FT));
   const int64_t units = static_cast<int64_t>(B) * q.s.ntiles;
   const int64_t avg = B > 0 ? ceil_div(N, B) : 0;
-  const int warp_rows = 32 / q.TX * (bwd ? scan_rows_bwd(q.V) : scan_rows_fwd(half, q.V));
+  const int warp_rows = 32 / q.TX * (bwd ? scan_rows_bwd(half, q.V) : scan_rows_fwd(half, q.V));
   q.NW = (units >= 16ll * sms || avg <= 64) ? 1 : 8;
   const int tile = q.NW * warp_rows;
   q.s.seg_rows = 0;
@@ -293,7 +293,7 @@ int scan_fwd_run(const ScanPlan &q, const Ty *u, const Ty *g, const float *h0, T
 template <typename Ty, int V, int TX, int NW, bool kShared>
 int scan_bwd_run(const ScanPlan &q, const Ty *dh, const Ty *u, const Ty *g, const Ty *h,
                  const float *h0, const float *dhN, Ty *du, Ty *dg, float *dh0, cudaStream_t st) {
-  constexpr int R = scan_rows_bwd(V);
+  constexpr int R = scan_rows_bwd(sizeof(Ty) == 2, V);
   const int bad = scan_maps<Ty, V, TX, kShared, true>(q, dh, g, st);
   if (bad != FEQL_OK) return bad;
   return scan_launch(scan_bwd_kernel<Ty, V, TX, R, NW, kShared>, q,

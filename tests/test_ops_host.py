@@ -63,6 +63,37 @@ def test_scan_refusals(lib):
     assert s(None, None, None, None, 0, 4, 4, 0, FP16, None) == F.FEQL_OK
 
 
+def test_activation_refusals(lib):
+    GELU = F.FEQL_ACT_GELU
+    f = lib.feql_forward_act
+    assert f(P, P, None, None, P, None, 8, 4, 4, -1, FP16, None) == INV
+    assert f(P, P, None, None, P, None, 8, 4, 4, 4, FP16, None) == INV
+    assert f(P, P, None, None, P, None, -1, 4, 4, GELU, FP16, None) == INV
+    assert f(P, P, None, P + 8, P, None, 8, 4, 4, GELU, FP16, None) == INV
+    assert f(P, P, None, None, P, P + 8, 8, 4, 4, GELU, FP16, None) == INV
+    assert f(None, P, None, None, P, None, 8, 4, 4, GELU, FP16, None) == INV
+    assert f(P, P, None, None, P, None, 8, 3, 4, GELU, FP16, None) == UNS
+    assert f(None, None, None, None, None, None, 0, 4, 4, GELU, FP16, None) == F.FEQL_OK
+    c = lib.feql_ct_forward_act
+    assert c(17, P, P, None, None, P, None, 8, 4, 4, GELU, FP16, None) == UNS
+    assert c(8, P, P, None, None, P, None, 8, 4, 4, 9, FP16, None) == INV
+    assert c(3, P, None, None, None, P, None, 8, 4, 4, GELU, FP32, None) == INV
+    m = lib.feql_p4m_forward_act
+    assert m(P, P, None, None, P, None, 8, 4, 4, GELU, FP32, None) == UNS
+    b = lib.feql_backward_act
+    big = 1 << 40
+    assert b(P, P, None, P, P, P, P, P, big, 8, 4, 4, GELU, FP16, None) == INV   # no slopes
+    assert b(P, P, P, P, None, None, None, P, big, 8, 4, 4, GELU, FP16, None) == INV
+    assert b(P, P, P, P, P, None, P, P, big, 8, 4, 4, GELU, FP16, None) == INV   # db without dW
+    assert b(P, P, P, None, P, P, P, P, big, 8, 4, 4, GELU, FP16, None) == INV
+    assert b(None, P, P, P, P, P, P, P, big, 8, 4, 4, GELU, FP16, None) == INV
+    assert b(P, P, P, P, P, P, P, None, big, 8, 4, 4, GELU, FP16, None) == INV
+    assert b(P, P, P + 2, P, P, P, P, P, big, 8, 4, 4, GELU, FP16, None) == INV
+    assert b(P, P, P, P, P, P, P, P, big, 8, 4, 5, GELU, FP16, None) == UNS
+    assert lib.feql_backward_act_workspace_bytes(8, 4, 4, 7, FP16) == 0
+    assert lib.feql_p4m_backward_act_workspace_bytes(8, 4, 4, GELU, FP32) == 0
+
+
 def test_layer_functions_refuse_cpu_tensors_and_wrong_shapes():
     x = torch.zeros(3, 4, 4, dtype=torch.float16)
     with pytest.raises(ValueError):
