@@ -10,6 +10,7 @@
 
 #include "act.cuh"
 #include "plan.cuh"
+#include "split_sum.cuh"
 #include "wfft.cuh"
 
 namespace feql {
@@ -254,45 +255,24 @@ simt_dw_partial_kernel(const T *__restrict__ x, const T *__restrict__ dy, float 
 // Deterministic reduction over splits (fixed order), inverse rDFT, cast:
 //   dW[d][c][u] = (G0 + (-1)^u G2)/4 + Re(G1 i^u)/2,  db[d] = sum of partials.
 template <typename T>
-__global__ void dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db,
-                                 T *__restrict__ dW, T *__restrict__ db, int splits, int C, int D) {
-  const int64_t plane = static_cast<int64_t>(D) * C;
-  for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < plane + D;
-       e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    if (e < plane) {
-      float g[4] = {0.f, 0.f, 0.f, 0.f};
-      // eight splits' values in flight; the sums stay in order
-      for (int s = 0; s < splits; s += 8) {
-        const float *p = ws + static_cast<int64_t>(s) * 4 * plane + e;
-        float v[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            v[i][k] = s + i < splits ? __ldg(p + (4ll * i + k) * plane) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (s + i < splits) g[k] += v[i][k];
-      }
+__global__ void __launch_bounds__(kSumThreads)
+dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db, T *__restrict__ dW,
+                 T *__restrict__ db, int splits, int C, int D) {
+  __shared__ float buf[kSumLines][kSumOut];
+  const int64_t plane = static_cast<int64_t>(D) * C, blocks_w = (plane + kSumOut - 1) / kSumOut;
+  const int lane = threadIdx.x % kSumOut;
+  if (blockIdx.x < blocks_w) {
+    const int64_t e = blockIdx.x * static_cast<int64_t>(kSumOut) + lane;
+    split_sums<kT>(ws, plane, e, splits, buf);
+    if (threadIdx.x < kSumOut && e < plane) {
       float w[4];
-      irdft4(g[0], g[1], g[2], g[3], w);
+      irdft4(buf[0][lane], buf[1][lane], buf[2][lane], buf[3][lane], w);
       Vec4<T>::store(dW + e * kT, w);
-    } else if (db != nullptr) {
-      const int d = static_cast<int>(e - plane);
-      float s = 0.f;
-      for (int k = 0; k < splits; k += 16) {
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          v[i] = k + i < splits ? __ldg(ws_db + static_cast<int64_t>(k + i) * D + d) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (k + i < splits) s += v[i];
-      }
-      db[d] = static_cast<T>(s);
     }
+  } else if (db != nullptr) {
+    const int64_t d = (blockIdx.x - blocks_w) * static_cast<int64_t>(kSumOut) + lane;
+    split_sums<1>(ws_db, D, d, splits, buf);
+    if (threadIdx.x < kSumOut && d < D) db[d] = static_cast<T>(buf[0][lane]);
   }
 }
 

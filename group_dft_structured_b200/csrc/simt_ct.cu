@@ -48,7 +48,7 @@ int ct_simt_dw_launch(const void *x, const void *dy, void *dW, void *db, float *
         static_cast<const Ty *>(x), static_cast<const Ty *>(dy), ws, ws_db, N, C, D, p.split_len,
         p.tiles_d, p.tiles_c);
   }
-  ct_simt_dw_reduce_kernel<T, Ty><<<grid_for(static_cast<int64_t>(D) * C + D, 64, sms), 64, 0, s>>>(
+  ct_simt_dw_reduce_kernel<T, Ty><<<split_sum_blocks(C, D), kSumThreads, 0, s>>>(
       ws, ws_db, static_cast<Ty *>(dW), static_cast<Ty *>(db), p.splits, C, D);
   return launch_status();
 }

@@ -24,6 +24,7 @@
 #include "act.cuh"
 #include "plan.cuh"
 #include "simt_ct_host.cuh"
+#include "split_sum.cuh"
 
 namespace feql {
 
@@ -353,33 +354,30 @@ ct_simt_dw_kernel(const Ty *__restrict__ x, const Ty *__restrict__ dy, float *__
 
 // Fixed-order sum of the split partials, then dW[d][c][:] = irDFT(G[d][c]) and db.
 template <int T, typename Ty>
-__global__ void ct_simt_dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db,
-                                         Ty *__restrict__ dW, Ty *__restrict__ db, int splits,
-                                         int C, int D) {
+__global__ void __launch_bounds__(kSumThreads)
+ct_simt_dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db,
+                         Ty *__restrict__ dW, Ty *__restrict__ db, int splits, int C, int D) {
   __shared__ float cs[CtBins<T>::kBins][T], sn[CtBins<T>::kBins][T];
+  __shared__ float buf[kSumLines][kSumOut];
   ct_twiddles<T>(cs, sn);
   __syncthreads();
-  const int64_t plane = static_cast<int64_t>(D) * C;
-  for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < plane + D;
-       e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    if (e < plane) {
+  const int64_t plane = static_cast<int64_t>(D) * C, blocks_w = (plane + kSumOut - 1) / kSumOut;
+  const int lane = threadIdx.x % kSumOut;
+  if (blockIdx.x < blocks_w) {
+    const int64_t e = blockIdx.x * static_cast<int64_t>(kSumOut) + lane;
+    split_sums<T>(ws, plane, e, splits, buf);
+    if (threadIdx.x < kSumOut && e < plane) {
       float G[T], y[T];
 #pragma unroll
-      for (int p = 0; p < T; ++p) G[p] = 0.f;
-#pragma unroll 4  // loads of four splits in flight; the sums stay in order
-      for (int s = 0; s < splits; ++s)
-#pragma unroll
-        for (int p = 0; p < T; ++p) G[p] += ws[(static_cast<int64_t>(s) * T + p) * plane + e];
+      for (int p = 0; p < T; ++p) G[p] = buf[p][lane];
       ct_inverse<T>(G, cs, sn, y);
 #pragma unroll
       for (int t = 0; t < T; ++t) dW[e * T + t] = ct_cast<Ty>(y[t]);
-    } else if (db != nullptr) {
-      const int64_t d = e - plane;
-      float s = 0.f;
-#pragma unroll 16
-      for (int sp = 0; sp < splits; ++sp) s += ws_db[static_cast<int64_t>(sp) * D + d];
-      db[d] = ct_cast<Ty>(s);
     }
+  } else if (db != nullptr) {
+    const int64_t d = (blockIdx.x - blocks_w) * static_cast<int64_t>(kSumOut) + lane;
+    split_sums<1>(ws_db, D, d, splits, buf);
+    if (threadIdx.x < kSumOut && d < D) db[d] = ct_cast<Ty>(buf[0][lane]);
   }
 }
 

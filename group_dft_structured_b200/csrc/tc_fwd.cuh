@@ -89,6 +89,7 @@ struct TcFwdParams {
   int Ci, Do, BD, nD, nK, chunk_bytes;
   int nM;               // token tiles: ceil(N / 128)
   int n_units;          // nM * nD
+  int share;            // CTAs of a unit, each with part of the epilogue's blocks (kEp kernels)
   int nacc, acc_stride; // accumulator buffers in TMEM and their column stride
   int resident;         // 1: the CTA's weight slice is loaded once (fixed D tile per CTA)
   int wres_bytes;       // resident weight buffer: nK * chunk_bytes (1 KB aligned)
@@ -130,16 +131,18 @@ struct TcUnits {
   int dm, dj, nD, nM;
   bool valid;
   __device__ __forceinline__ explicit TcUnits(const TcFwdParams &p) : nD(p.nD), nM(p.nM) {
-    m = static_cast<int>(blockIdx.x) / p.nD;
-    j = static_cast<int>(blockIdx.x) % p.nD;
+    const int cta = static_cast<int>(blockIdx.x) / p.share;
+    const int ctas = static_cast<int>(gridDim.x) / p.share;
+    m = cta / p.nD;
+    j = cta % p.nD;
     if (p.resident) {
-      const int g = static_cast<int>(gridDim.x) / p.nD;
+      const int g = ctas / p.nD;
       dm = g;
       dj = 0;
-      valid = static_cast<int>(blockIdx.x) < g * p.nD && m < nM;
+      valid = cta < g * p.nD && m < nM;
     } else {
-      dm = static_cast<int>(gridDim.x) / p.nD;
-      dj = static_cast<int>(gridDim.x) % p.nD;
+      dm = ctas / p.nD;
+      dj = ctas % p.nD;
       valid = m < nM;
     }
   }
@@ -406,11 +409,12 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
   } else if (kEp != kEpNone && warp >= kEpFirst) {
     // ------------------------------ epilogue with activation and residual
     // As below, but all teams share every tile: team t takes the 8-channel
-    // blocks t, t + kEpTeams, ...
-    const int ew = warp - kEpFirst, eteam = ew / 4;
+    // blocks t, t + bstep, ... (teams counted through the CTAs of the unit)
+    const int ew = warp - kEpFirst, bstep = kEpTeams * p.share;
+    const int eteam = ew / 4 + kEpTeams * (static_cast<int>(blockIdx.x) % p.share);
     const int quad = warp & 3;
     const int blocks = p.BD / 8;
-    const int last = eteam < blocks ? eteam + (blocks - 1 - eteam) / kEpTeams * kEpTeams : -1;
+    const int last = eteam < blocks ? eteam + (blocks - 1 - eteam) / bstep * bstep : -1;
     const int tcp = 2 * (lane & 3);
     const int64_t row_elems = static_cast<int64_t>(p.Do) * kT;
     // the residual ring: the block that the next load is for, slots issued and used
@@ -429,7 +433,7 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
       }
       ++flying;
       if (++islot == kResDepth) islot = 0;
-      ahead_b += kEpTeams;
+      ahead_b += bstep;
       if (ahead_b > last) {
         ahead_b = eteam;
         ahead.next();
@@ -452,7 +456,7 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
       }
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + a * p.acc_stride;
       const int64_t row0 = static_cast<int64_t>(m) * kBM + quad * 32 + (lane >> 2);
-      for (int blk = eteam; blk < blocks; blk += kEpTeams) {
+      for (int blk = eteam; blk < blocks; blk += bstep) {
         const int c = blk * 8;
         const int d = j * p.BD + c + tcp;  // this thread's first output channel
         uint32_t y0[2][4], y2[2][4], yr[2][4], yi[2][4];
