@@ -195,8 +195,8 @@ constexpr int scan_rows_bwd(bool half, int V) { return half ? (V == 4 ? 4 : 8) :
 // the GPU with warps or the sequences are short; else eight warps share a
 // tile of rows.  (Six warps and 96 registers, for three blocks per SM, were
 // measured: no faster, 105 against 104 us on the 384 units of 128 x 3136 x 24 x 4
-// backward, of which 296 blocks of eight run at a time.)  Then sequences are cut into segments where whole ones would
-// leave SMs idle: dense sequences when not every SM gets a unit, packed ones
+// backward, of which 296 blocks of eight run at a time; 99 us by now.)  Then
+// sequences are cut into segments where whole ones would leave SMs idle: dense sequences when not every SM gets a unit, packed ones
 // (whose longest the host does not know) always, in segments of an even share
 // for two blocks (16 of one warp) per SM, two (16) tiles at least.
 ScanPlan scan_plan(int B, int64_t N, int C, int T, bool shared, bool packed, bool half, bool bwd,

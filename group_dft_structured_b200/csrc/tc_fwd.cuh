@@ -179,8 +179,8 @@ struct TcUnits {
 // residual comes by TMA: each epilogue warp loads the 32-row x 8-channel boxes
 // (2 KB) of its own blocks, in the order in which it will use them, into a private
 // ring of kResDepth slots, so the loads run kResDepth blocks ahead (direct loads in
-// the block that uses them cost an HBM
-// latency each: 123 us instead of 78 us on 65536 x 192 -> 192).
+// the block that uses them cost an HBM latency each: 123 us instead of 78 with two
+// teams on 65536 x 192 -> 192; 85 us with three, 3.6 TB/s).
 template <bool kTF32, int kEp = kEpNone>
 __global__ void __maxnreg__(96)
 tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
