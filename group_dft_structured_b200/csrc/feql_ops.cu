@@ -194,11 +194,11 @@ constexpr int scan_rows_bwd(bool half, int V) { return half ? (V == 4 ? 4 : 8) :
 // a sequence by itself when there are enough (sequence, tile) units to fill
 // the GPU with warps or the sequences are short; else eight warps share a
 // tile of rows.  (Six warps and 96 registers, for three blocks per SM, were
-// measured: no faster, 105 against 104 us on the 384 units of 128 x 3136 x 24 x 4
-// backward, of which 296 blocks of eight run at a time; 99 us by now.)  Then
-// sequences are cut into segments where whole ones would leave SMs idle: dense sequences when not every SM gets a unit, packed ones
-// (whose longest the host does not know) always, in segments of an even share
-// for two blocks (16 of one warp) per SM, two (16) tiles at least.
+// measured: no faster, 105 against 104 us on 128 x 3136 x 24 x 4 backward.)  Then
+// sequences are cut into segments where whole ones would leave SMs idle: dense
+// sequences when not every SM gets a unit, packed ones (whose longest the host
+// does not know) always, in segments of an even share for two blocks (16 of one
+// warp) per SM, two (16) tiles at least.
 ScanPlan scan_plan(int B, int64_t N, int C, int T, bool shared, bool packed, bool half, bool bwd,
                    int sms) {
   ScanPlan q;
@@ -235,7 +235,28 @@ ScanPlan scan_plan(int B, int64_t N, int C, int T, bool shared, bool packed, boo
     const int64_t rows = share > least ? share : least;
     if (rows < (packed ? N : q.s.L)) q.s.seg_rows = rows;
   }
-  q.s.slots = q.s.seg_rows == 0 ? B : N / q.s.seg_rows + B;
+  q.s.whole = 0;
+  q.s.per = 1;
+  // Dense sequences that fill the GPU once or twice and then less than half of it:
+  // those of the last round are cut (128 x 3136 x 24 x 4 backward, 384 units of which
+  // 296 run at a time: 91 us, 99 with whole ones; all of them cut 105, since the maps
+  // read all of dh and g).
+  const int64_t cap = static_cast<int64_t>(sms) * scan_blocks(8, !bwd && sh && q.V > 1);
+  if (!packed && q.NW == 8 && units > cap && units < 3 * cap) {
+    const int64_t whole = units / cap * cap / q.s.ntiles, rest = (B - whole) * q.s.ntiles;
+    if (rest > 0 && 2 * rest <= cap) {
+      const int64_t part = ceil_div(ceil_div(q.s.L, cap / rest), tile) * tile;
+      const int64_t rows = part > 2 * tile ? part : 2 * tile;
+      if (rows < q.s.L) {
+        q.s.seg_rows = rows;
+        q.s.whole = static_cast<int>(whole);
+      }
+    }
+  }
+  if (!packed && q.s.seg_rows != 0) q.s.per = static_cast<int>(ceil_div(q.s.L, q.s.seg_rows));
+  q.s.slots = q.s.seg_rows == 0 ? B
+              : packed          ? N / q.s.seg_rows + B
+                                : q.s.whole + static_cast<int64_t>(B - q.s.whole) * q.s.per;
   q.s.maps = nullptr;
   return q;
 }
@@ -269,7 +290,7 @@ int scan_launch(void (*kernel)(Args...), const ScanPlan &q, int smem, cudaStream
 template <typename Ty, int V, int TX, bool kShared, bool kRev>
 int scan_maps(const ScanPlan &q, const Ty *x, const Ty *g, cudaStream_t st) {
   if (q.s.seg_rows == 0) return FEQL_OK;
-  const unsigned grid = static_cast<unsigned>(q.s.slots * q.s.ntiles);
+  const unsigned grid = static_cast<unsigned>((q.s.slots - q.s.whole) * q.s.ntiles);
   scan_maps_kernel<Ty, V, TX, 8, kShared, kRev><<<grid, 256, 0, st>>>(x, g, q.s);
   return launch_status();
 }

@@ -19,8 +19,9 @@
 // copying thread reads (no barrier), so loads never wait for the joins.  Every
 // value is read once and written once.  States, products and sums are fp32.
 //
-// Where whole sequences are too few or too uneven to fill the GPU, their rows
-// are cut into segments of seg_rows, a block to each: a first kernel reads u and
+// Where whole sequences are too few or too uneven to fill the GPU, or their last
+// round fills less than half of it, rows are cut into segments of seg_rows (of the
+// last round's sequences, in the last case), a block to each: a first kernel reads u and
 // g and reduces each segment to its affine map, and the main kernel's block of a
 // segment starts from the maps before it.  That reads the inputs twice, the
 // second time partly from L2, for as many more blocks.  (Sequences of one
@@ -30,10 +31,10 @@
 // moves dg by at most half a step of h against (h - u), less than dg's own
 // rounding.  Recomputing h from saved tile states was tried: it saves one of six
 // streams but scans every tile twice, 118 us against 104 on 128 x 3136 x 24 x 4
-// with channel gates (99 by now).
+// with channel gates (91 by now).
 //
 // Measured, fp16: 128 x 3136 x 24 x 4 with channel gates, forward 44 us (173 MB,
-// 3.9 TB/s) and backward 99 us (405 MB, 4.1 TB/s); one sequence of 65536 x 96 x 4,
+// 3.9 TB/s) and backward 91 us (405 MB, 4.4 TB/s); one sequence of 65536 x 96 x 4,
 // 29 us for the maps and 34 for the scan (151 MB, 252 with the second reading).
 // DRAM is 40 % busy and the instructions issue on 50 to 65 % of the cycles: the
 // converts, the joins and the walk over the rows bound it, not the loads.
@@ -60,7 +61,8 @@ struct ScanShape {
   int FT;              // features per tile
   int ntiles;
   int64_t seg_rows;    // rows of a segment (a multiple of the tiles), 0: sequences are whole
-  int64_t slots;       // segment slots: N / seg_rows + B, or B
+  int64_t slots;       // segment slots: N / seg_rows + B, dense whole + (B - whole) per
+  int whole, per;      // dense: the first sequences stay whole, the others' segments
   float *maps;         // [slots][ntiles][2][TX V] affine maps of the segments
 };
 
@@ -84,7 +86,8 @@ __device__ __forceinline__ void scan_rows(const ScanShape &p, int b, int64_t &s,
 // Which sequence a slot belongs to: the last b whose first slot is not behind it,
 // by a search over the offsets, 32 candidates a round (the whole warp calls).
 __device__ __forceinline__ int scan_slot_owner(const ScanShape &p, int64_t slot) {
-  if (p.seg_rows == 0) return static_cast<int>(slot);
+  if (p.seg_rows == 0 || slot < p.whole) return static_cast<int>(slot);
+  if (p.offsets == nullptr) return p.whole + static_cast<int>(slot - p.whole) / p.per;
   int lo = 0, hi = p.B;  // the owner is in [lo, hi)
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
@@ -365,11 +368,11 @@ struct ScanPlace {
   bool live;                  // this thread's features exist
   bool work;                  // the slot holds a segment
   int64_t s, e, len, r0, r1;  // rows of the sequence; the segment's within it
-  __device__ __forceinline__ explicit ScanPlace(const ScanShape &p) {
+  __device__ __forceinline__ explicit ScanPlace(const ScanShape &p, int first = 0) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     tx = lane % TX;
     ty = warp * (32 / TX) + lane / TX;
-    slot = blockIdx.x / p.ntiles;
+    slot = first + blockIdx.x / p.ntiles;
     tile = blockIdx.x % p.ntiles;
     f = tile * p.FT + tx * V;
     live = tx * V < p.FT && f < p.F;
@@ -382,8 +385,9 @@ struct ScanPlace {
     nseg = 1;
     r0 = 0;
     r1 = len;
-    if (p.seg_rows != 0) {
-      seg = static_cast<int>(slot - (s / p.seg_rows + b));
+    if (p.seg_rows != 0 && slot >= p.whole) {
+      seg = static_cast<int>(p.offsets == nullptr ? (slot - p.whole) % p.per
+                                                  : slot - (s / p.seg_rows + b));
       nseg = static_cast<int>((len + p.seg_rows - 1) / p.seg_rows);
       if (nseg < 1) nseg = 1;
       r0 = seg * p.seg_rows;
@@ -398,16 +402,19 @@ struct ScanPlace {
 };
 
 // kRev: the gradient's maps c -> A c + B, B from dh; else the states', B from u.
-// Each row group walks its share of the segment's rows by itself, eight at a
-// time with the next eight on their way, and the groups join once at the end.
+// Each row group walks its share of the segment's rows by itself, R at a time
+// with the next R on their way, and the groups join once at the end.
 template <typename Ty, int V, int TX, int NW, bool kShared, bool kRev>
 __global__ void __launch_bounds__(NW * 32, 2)
 scan_maps_kernel(const Ty *__restrict__ x, const Ty *__restrict__ g, const ScanShape p) {
   constexpr int GV = kShared ? 1 : V;
-  constexpr int TY = NW * 32 / TX, R = V == 4 && sizeof(Ty) == 4 ? 4 : 8;
+  constexpr int TY = NW * 32 / TX, R = 4;
   using J = ScanJoin<V, TX, NW, GV, kRev>;
   __shared__ __align__(16) typename J::Smem sm;
-  const ScanPlace<V, TX, NW, kShared> at(p);
+  // the main kernel's blocks may start: those of whole sequences run, the others
+  // bring their first tile and wait
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const ScanPlace<V, TX, NW, kShared> at(p, p.whole);
   // (the same for a whole block; a sequence's last segment in scan order has no use)
   if (!at.work || at.seg == (kRev ? 0 : at.nseg - 1)) return;
   const int64_t rows = at.r1 - at.r0;
@@ -423,32 +430,25 @@ scan_maps_kernel(const Ty *__restrict__ x, const Ty *__restrict__ g, const ScanS
   const int64_t first = at.s + (kRev ? l1 - 1 : l0);
   const Ty *px = x + first * p.F + at.f, *pg = g + first * p.FG + at.gf;
   const int sx = kRev ? -p.F : p.F, sg = kRev ? -p.FG : p.FG;
-  Pack<Ty, V> rx[R], nx[R];
-  Pack<Ty, GV> rg[R], ng[R];
-  auto fetch = [&](int64_t k) {
+  Pack<Ty, V> rx[2][R];
+  Pack<Ty, GV> rg[2][R];
+  auto fetch = [&](int h, auto rows) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (k + r < n) {
-        nx[r].load(px + static_cast<int64_t>(r) * sx);
-        ng[r].load(pg + static_cast<int64_t>(r) * sg);
+      if (rows.has(r)) {
+        rx[h][r].load(px + static_cast<int64_t>(r) * sx);
+        rg[h][r].load(pg + static_cast<int64_t>(r) * sg);
       }
     px += static_cast<int64_t>(R) * sx;
     pg += static_cast<int64_t>(R) * sg;
   };
-  fetch(0);
-  for (int64_t k = 0; k < n; k += R) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      rx[r] = nx[r];
-      rg[r] = ng[r];
-    }
-    fetch(k + R);
+  auto walk = [&](int h, auto rows) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (k + r < n) {
+      if (rows.has(r)) {
         float xv[V], gv[GV], a[GV], na[GV], av[V], nav[V];
-        rx[r].unpack(xv);
-        rg[r].unpack(gv);
+        rx[h][r].unpack(xv);
+        rg[h][r].unpack(gv);
 #pragma unroll
         for (int j = 0; j < GV; ++j) sigmoid_pair<sizeof(Ty) == 2>(gv[j], a[j], na[j]);
         spread(av, a);
@@ -462,6 +462,25 @@ scan_maps_kernel(const Ty *__restrict__ x, const Ty *__restrict__ g, const ScanS
         }
         vec_mul(A, A, a);
       }
+  };
+  auto some = [&](int64_t k) {
+    return ScanRows<false>{k >= n ? 0 : n - k < R ? static_cast<int>(n - k) : R};
+  };
+  const ScanRows<true> all{R};
+  fetch(0, some(0));
+  fetch(1, some(R));
+  int64_t k = 0;
+  for (; k + 4 * R <= n; k += 2 * R) {  // nothing to check
+    walk(0, all);
+    fetch(0, all);
+    walk(1, all);
+    fetch(1, all);
+  }
+  for (; k < n; k += 2 * R) {
+    walk(0, some(k));
+    fetch(0, some(k + 2 * R));
+    walk(1, some(k + R));
+    fetch(1, some(k + 3 * R));
   }
   // joined: the map's constant part is where a zero state goes, its factor the product
   J join;
@@ -573,7 +592,7 @@ scan_fwd_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, const float 
   }
   float carry[V] = {};
   if (h0 != nullptr) load_state<V>(h0 + static_cast<int64_t>(at.b) * p.F + at.f, carry);
-  scan_wait_maps(p);
+  if (at.slot >= p.whole) scan_wait_maps(p);
   scan_enter<false>(p, at, carry);
   Ty *ph = h + row * p.F + at.f;
   auto tile = [&](int i, auto rows_of) {
@@ -707,7 +726,7 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
   const int64_t state = static_cast<int64_t>(at.b) * p.F + at.f;
   if (dhN != nullptr) load_state<V>(dhN + state, carry);
   if (top && h0 != nullptr) load_state<V>(h0 + state, start);
-  scan_wait_maps(p);
+  if (at.slot >= p.whole) scan_wait_maps(p);
   scan_enter<true>(p, at, carry);
   Ty *pdu = du + row * p.F + at.f, *pdg = dg + row * p.FG + at.gf;
   auto tile = [&](int i, auto rows_of) {

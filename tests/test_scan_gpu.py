@@ -299,3 +299,31 @@ def test_refusals():
         L.scan_step(u[:, 0], u[:, 0], state)
     with pytest.raises(TypeError):
         L.scan_step(u[:, 0], u[:, 0], torch.zeros(2, 6, 4, device="cuda").half())
+
+
+@pytest.mark.parametrize("dt", [np.float16, np.float32])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("B,L_", [(306, 530), (452, 261), (600, 300), (620, 2001)])
+def test_last_round_of_sequences_cut(B, L_, shared, dt):
+    """More sequences than run at a time: those of a short last round are cut."""
+    C, T, K = 8, 4, 4  # K sequences, repeated
+    u, g, dh, h0, dhN = inputs(K * L_, K, C, T, shared, dt)
+
+    def tiled(v, per):
+        v = v.reshape(K, per, *v.shape[1:]) if per else v
+        return cuda(np.concatenate([v] * (B // K + 1))[:B])
+
+    h, hN, saved = L.scan_forward(tiled(u, L_), tiled(g, L_), tiled(h0, 0))
+    # backward may cut others than forward does: both kinds read the first one's h
+    of = torch.arange(B, device="cuda") % K
+    saved = (saved[0][:K][of], saved[1])
+    du, dg, dh0 = L.scan_backward(tiled(dh, L_), tiled(u, L_), tiled(g, L_), saved, tiled(dhN, 0))
+    out = (h, hN, du, dg, dh0)
+    ends = [list(range(K)), [B - K + (k - B) % K for k in range(K)]]  # first and last of each
+    like = (u, h0, u, g, h0)
+    for pick in ends:
+        check(u, g, dh, h0, dhN, [i * L_ for i in range(K + 1)],
+              [t[pick].reshape(v.shape) for t, v in zip(out, like)])
+    for t in out:  # whole or cut alike: the bits of one or of the other
+        same = [(t == t[pick][of]).flatten(1).all(1) for pick in ends]
+        assert bool((same[0] | same[1]).all())
