@@ -523,8 +523,8 @@ __device__ __forceinline__ void scan_enter(const ScanShape &p,
   }
 }
 
-// Before the first use of the maps: their kernel has finished.  Every block
-// waits, so that the grid never ends before it.
+// Before the first use of the maps: their kernel has finished.  Every block of a
+// cut sequence waits, and there are some, so the grid never ends before it.
 __device__ __forceinline__ void scan_wait_maps(const ScanShape &p) {
   if (p.seg_rows != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -456,4 +456,6 @@ def scan_step(u: torch.Tensor, g: torch.Tensor, state: torch.Tensor) -> torch.Te
         s = _take(state, "state", (B, C, T), torch.float32, at)
         h = torch.empty_like(u)
         feql_scan_step(u, g, s, h, B, C, T, g.dim() < 3, mode)
+        if not state.is_inference():  # a graph that saved the state sees the change
+            torch.autograd.graph.increment_version(state)
     return h

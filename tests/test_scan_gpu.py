@@ -178,6 +178,23 @@ def test_step(B, C, T, shared, dt):
     check(u, g, u, h0, None, off, (h, state, None, None, None))
 
 
+def test_step_shows_in_the_state_version():
+    """A graph that saved the state refuses to go on with the changed one."""
+    from group_dft_structured_b200.module import EqScan
+    scan = EqScan(8, 4)
+    u = torch.randn(2, 5, 32, device="cuda").half().requires_grad_()
+    gate = torch.randn(2, 5, 8, device="cuda").half()
+    state = torch.zeros(2, 32, device="cuda")
+    h, _ = scan(u, gate, state)
+    scan.step(u.detach()[:, 0], gate[:, 0], state)
+    with pytest.raises(RuntimeError, match="inplace"):
+        h.float().sum().backward()
+    with torch.inference_mode():
+        held = torch.zeros(2, 32, device="cuda")
+        scan.step(u.detach()[:, 0], gate[:, 0], held)
+    assert torch.equal(held, state)
+
+
 def test_steps_continue_a_scan():
     u, g, _, h0, _ = inputs(2 * 40, 2, 24, 4, False, np.float16)
     U_, G_ = cuda(u).view(2, 40, 24, 4), cuda(g).view(2, 40, 24, 4)
