@@ -51,7 +51,8 @@ NormPlan norm_plan(int64_t N, int C, int T, bool half, bool bwd) {
   q.V = half ? 8 : 4;
   const int wide = q.V;
   while (F % q.V != 0) q.V /= 2;
-  q.A = (T % 4 == 0 && q.V % 4 == 0) ? 4 : 1;
+  // neighbours that share a channel's parameters and sums
+  q.A = T % 4 == 0 && q.V % 4 == 0 ? 4 : (T % 2 == 0 && q.V % 2 == 0 ? 2 : 1);
   q.s = {N, C, T, F, 0, F / q.V};
   static const int wide_ks[] = {4, 2, 3, 1, 8}, narrow_ks[] = {8, 2};
   const int *ks = q.V == wide ? wide_ks : narrow_ks;
@@ -93,12 +94,17 @@ int64_t norm_long_splits(int64_t N) {
   X(Ty, V, 1, A) X(Ty, V, 2, A) X(Ty, V, 3, A) X(Ty, V, 4, A) X(Ty, V, 8, A)
 #define FEQL_NORM_NARROW(X, Ty, V, A) X(Ty, V, 2, A) X(Ty, V, 8, A)
 #define FEQL_NORM_HALF(X)                                                                \
-  FEQL_NORM_WIDE(X, __half, 8, 1) FEQL_NORM_WIDE(X, __half, 8, 4)                        \
-  FEQL_NORM_NARROW(X, __half, 4, 1) FEQL_NORM_NARROW(X, __half, 4, 4)                    \
-  FEQL_NORM_NARROW(X, __half, 2, 1) FEQL_NORM_NARROW(X, __half, 1, 1)
+  FEQL_NORM_WIDE(X, __half, 8, 1) FEQL_NORM_WIDE(X, __half, 8, 2)                        \
+  FEQL_NORM_WIDE(X, __half, 8, 4)                                                        \
+  FEQL_NORM_NARROW(X, __half, 4, 1) FEQL_NORM_NARROW(X, __half, 4, 2)                    \
+  FEQL_NORM_NARROW(X, __half, 4, 4)                                                      \
+  FEQL_NORM_NARROW(X, __half, 2, 1) FEQL_NORM_NARROW(X, __half, 2, 2)                    \
+  FEQL_NORM_NARROW(X, __half, 1, 1)
 #define FEQL_NORM_FLOAT(X)                                                               \
-  FEQL_NORM_WIDE(X, float, 4, 1) FEQL_NORM_WIDE(X, float, 4, 4)                          \
-  FEQL_NORM_NARROW(X, float, 2, 1) FEQL_NORM_NARROW(X, float, 1, 1)
+  FEQL_NORM_WIDE(X, float, 4, 1) FEQL_NORM_WIDE(X, float, 4, 2)                          \
+  FEQL_NORM_WIDE(X, float, 4, 4)                                                         \
+  FEQL_NORM_NARROW(X, float, 2, 1) FEQL_NORM_NARROW(X, float, 2, 2)                      \
+  FEQL_NORM_NARROW(X, float, 1, 1)
 
 int norm_fwd_launch(const NormPlan &q, bool half, const void *x, const void *gamma,
                     const void *beta, void *y, float2 *stats, float eps, int grid,

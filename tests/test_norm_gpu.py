@@ -106,6 +106,15 @@ def test_parity(N, C, T, dt):
 
 
 @pytest.mark.parametrize("dt", [np.float16, np.float32])
+@pytest.mark.parametrize("N,C,T", [(40, 4, 6), (333, 12, 10), (21, 340, 6), (50, 64, 2), (9, 96, 14),
+                                   (6, 2731, 6), (17, 30, 6), (800, 2, 6), (11, 1540, 2)])
+def test_pairs_of_a_channel(N, C, T, dt):
+    """T even but no multiple of four: parameters and sums are shared by two."""
+    x, dy, gamma, beta = inputs(N, C, T, dt)
+    check(x, dy, gamma, beta, *run(x, dy, gamma, beta))
+
+
+@pytest.mark.parametrize("dt", [np.float16, np.float32])
 def test_parity_without_affine_and_many_rows(dt):
     x, dy, _, _ = inputs(40000, 6, 4, dt)
     check(x, dy, None, None, *run(x, dy, None, None))
