@@ -127,18 +127,19 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_raw_stream = None
+_raw_stream = _device = None  # torch's, once they are needed
 
 
 def _current_stream() -> int:
     """torch's current stream of the current device as a raw cudaStream_t."""
-    global _raw_stream
-    import torch
-    if _raw_stream is None:
+    global _raw_stream, _device
+    if _device is None:
+        import torch
         # without the Stream object in between, where torch offers it
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return _raw_stream(torch.cuda.current_device())
+        _device = torch.cuda.current_device
+    return _raw_stream(_device())
 
 
 def _stream(s):

@@ -220,9 +220,30 @@ def _take(t, name: str, shape, dtype, index: int):
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    return _dense(t)
+
+
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """``t``, or a dense copy on a 16-byte boundary."""
     if not t.is_contiguous():
         t = t.detach().contiguous()
     return t if t.data_ptr() % 16 == 0 else t.detach().clone()
+
+
+_sizes: dict = {}
+
+
+def _bytes(query, index: int, *args) -> int:
+    """query(*args) on device ``index``, asked once per sizes; 0 (refused) is asked anew."""
+    key = (query, index, args)
+    n = _sizes.get(key)
+    if n is None:
+        n = query(*args)
+        if n:
+            if len(_sizes) >= 4096:
+                _sizes.clear()
+            _sizes[key] = n
+    return n
 
 
 # The layer with activation and residual in its epilogue.  ``act`` is one of
@@ -253,16 +274,16 @@ def _layer_input(x: torch.Tensor, mode: int, p4m: bool):
 
 def _forward_act(calls, p4m, x, What, b, D, mode, act, res, save_z):
     N, C, T = _layer_input(x, mode, p4m)
-    nbytes, forward = calls[0](T, C, D, mode), calls[1]
+    nbytes, forward = _bytes(calls[0], -1, T, C, D, mode), calls[1]
     if nbytes == 0:
         raise ValueError("unsupported (T, C, D, mode)")
     with _on(x):
         at = x.get_device()
-        x = _take(x, "x", x.shape, x.dtype, at)
+        x = _dense(x)
         What = _take(What, "What", (nbytes,), torch.uint8, at)
         b = _take(b, "b", (D,), x.dtype, at)
         res = _take(res, "res", (N, D, T), x.dtype, at)
-        y = torch.empty((N, D, T), dtype=x.dtype, device=x.device)
+        y = x.new_empty((N, D, T))
         z = torch.empty_like(y) if save_z and act != FEQL_ACT_NONE else None
         forward(T, x, What, b, res, y, z, N, C, D, act, mode)
     return y, z
@@ -273,25 +294,26 @@ def _backward_act(calls, p4m, x, dy, z, What, mode, act, with_dx, with_dw, with_
     if dy.dim() != 3:
         raise ValueError(f"dy has shape {tuple(dy.shape)}, expected (N, D, T)")
     D = dy.shape[1]
-    nbytes, workspace, backward = calls[0](T, C, D, mode), calls[2], calls[3]
+    nbytes, workspace, backward = _bytes(calls[0], -1, T, C, D, mode), calls[2], calls[3]
     if nbytes == 0:
         raise ValueError("unsupported (T, C, D, mode)")
     dx = dW = db = None
     with _on(x):
-        dev, at = x.device, x.get_device()
-        x = _take(x, "x", x.shape, x.dtype, at)
+        at = x.get_device()
+        x = _dense(x)
         dy = _take(dy, "dy", (N, D, T), x.dtype, at)
         z = _take(z, "z", (N, D, T), x.dtype, at)
         What = _take(What, "What", (nbytes,), torch.uint8, at)
-        ws = torch.empty(workspace(T, N, C, D, act, mode), dtype=torch.uint8, device=dev)
+        ws_bytes = _bytes(workspace, at, T, N, C, D, act, mode)
+        ws = x.new_empty(ws_bytes, dtype=torch.uint8)
         if with_dx:
             dx = torch.empty_like(x)
         if with_dw or with_db:
-            dW = torch.empty((D, C, T), dtype=x.dtype, device=dev)
+            dW = x.new_empty((D, C, T))
         if with_db:
-            db = torch.empty((D,), dtype=x.dtype, device=dev)
+            db = x.new_empty(D)
         if with_dx or dW is not None:
-            backward(T, x, dy, z, What, dx, dW, db, ws, ws.numel(), N, C, D, act, mode)
+            backward(T, x, dy, z, What, dx, dW, db, ws, ws_bytes, N, C, D, act, mode)
     return dx, (dW if with_dw else None), db
 
 
@@ -336,12 +358,11 @@ def norm_forward(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5,
     mode = _mode(x)
     with _on(x):
         at = x.get_device()
-        x = _take(x, "x", x.shape, x.dtype, at)
+        x = _dense(x)
         gamma = _take(gamma, "gamma", (C,), x.dtype, at)
         beta = _take(beta, "beta", (C,), x.dtype, at)
         y = torch.empty_like(x)
-        stats = (torch.empty((N, 2), dtype=torch.float32, device=x.device) if save_stats
-                 else None)
+        stats = x.new_empty((N, 2), dtype=torch.float32) if save_stats else None
         feql_norm_forward(x, gamma, beta, y, stats, N, C, T, eps, mode)
     return y, stats
 
@@ -355,18 +376,17 @@ def norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, gamma=
     mode = _mode(x)
     with _on(x):
         at = x.get_device()
-        x = _take(x, "x", x.shape, x.dtype, at)
+        x = _dense(x)
         dy = _take(dy, "dy", x.shape, x.dtype, at)
         stats = _take(stats, "stats", (N, 2), torch.float32, at)
         gamma = _take(gamma, "gamma", (C,), x.dtype, at)
         dx = torch.empty_like(x)
         dgamma = dbeta = None
         if with_params:
-            dgamma = torch.empty((C,), dtype=x.dtype, device=x.device)
-            dbeta = torch.empty((C,), dtype=x.dtype, device=x.device)
-        nbytes = feql_norm_backward_workspace_bytes(N, C, T, mode)
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
-        feql_norm_backward(x, dy, stats, gamma, dx, dgamma, dbeta, ws, ws.numel(), N, C, T, mode)
+            dgamma, dbeta = x.new_empty(C), x.new_empty(C)
+        nbytes = max(_bytes(feql_norm_backward_workspace_bytes, at, N, C, T, mode), 16)
+        ws = x.new_empty(nbytes, dtype=torch.uint8)
+        feql_norm_backward(x, dy, stats, gamma, dx, dgamma, dbeta, ws, nbytes, N, C, T, mode)
     return dx, dgamma, dbeta
 
 
@@ -402,16 +422,17 @@ def scan_forward(u: torch.Tensor, g: torch.Tensor, h0=None, offsets=None, save: 
     B, N, C, T, shared = _scan_sizes(u, g, offsets)
     mode = _mode(u)
     with _on(u):
-        dev, at = u.device, u.get_device()
-        u = _take(u, "u", u.shape, u.dtype, at)
+        at = u.get_device()
+        u = _dense(u)
         g = _take(g, "g", g.shape, u.dtype, at)
         h0 = _take(h0, "h0", (B, C, T), torch.float32, at)
         offsets = _take(offsets, "offsets", (B + 1,), torch.int32, at)
         h = torch.empty_like(u)
-        hN = torch.empty((B, C, T), dtype=torch.float32, device=dev)
-        nbytes = feql_scan_workspace_bytes(B, N, C, T, shared, offsets is not None, mode)
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        feql_scan_forward(u, g, h0, offsets, h, hN, ws, ws.numel(), B, N, C, T, shared, mode)
+        hN = u.new_empty((B, C, T), dtype=torch.float32)
+        nbytes = max(_bytes(feql_scan_workspace_bytes, at, B, N, C, T, shared,
+                            offsets is not None, mode), 16)
+        ws = u.new_empty(nbytes, dtype=torch.uint8)
+        feql_scan_forward(u, g, h0, offsets, h, hN, ws, nbytes, B, N, C, T, shared, mode)
     return h, hN, ((h, h0) if save else None)
 
 
@@ -421,8 +442,8 @@ def scan_backward(dh: torch.Tensor, u: torch.Tensor, g: torch.Tensor, saved, dhN
     B, N, C, T, shared = _scan_sizes(u, g, offsets)
     mode = _mode(u)
     with _on(u):
-        dev, at = u.device, u.get_device()
-        u = _take(u, "u", u.shape, u.dtype, at)
+        at = u.get_device()
+        u = _dense(u)
         g = _take(g, "g", g.shape, u.dtype, at)
         dh = _take(dh, "dh", u.shape, u.dtype, at)
         dhN = _take(dhN, "dhN", (B, C, T), torch.float32, at)
@@ -430,10 +451,11 @@ def scan_backward(dh: torch.Tensor, u: torch.Tensor, g: torch.Tensor, saved, dhN
         h = _take(saved[0], "h", u.shape, u.dtype, at)
         h0 = _take(saved[1], "h0", (B, C, T), torch.float32, at)
         du, dg = torch.empty_like(u), torch.empty_like(g)
-        dh0 = torch.empty((B, C, T), dtype=torch.float32, device=dev)
-        nbytes = feql_scan_workspace_bytes(B, N, C, T, shared, offsets is not None, mode)
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        feql_scan_backward(dh, u, g, h, h0, dhN, offsets, du, dg, dh0, ws, ws.numel(), B, N, C, T,
+        dh0 = u.new_empty((B, C, T), dtype=torch.float32)
+        nbytes = max(_bytes(feql_scan_workspace_bytes, at, B, N, C, T, shared,
+                            offsets is not None, mode), 16)
+        ws = u.new_empty(nbytes, dtype=torch.uint8)
+        feql_scan_backward(dh, u, g, h, h0, dhN, offsets, du, dg, dh0, ws, nbytes, B, N, C, T,
                            shared, mode)
     return du, dg, dh0
 
@@ -451,7 +473,7 @@ def scan_step(u: torch.Tensor, g: torch.Tensor, state: torch.Tensor) -> torch.Te
         if not state.is_contiguous() or state.data_ptr() % 16 != 0:
             raise ValueError("state is updated in place: it has to be dense and 16-byte aligned")
         at = u.get_device()
-        u = _take(u, "u", u.shape, u.dtype, at)
+        u = _dense(u)
         g = _take(g, "g", g.shape, u.dtype, at)
         s = _take(state, "state", (B, C, T), torch.float32, at)
         h = torch.empty_like(u)
