@@ -70,8 +70,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// A z that is no number must show in y and in the slope (an overflowed x, a diverged
+// W: a loss scaler looks for it), and so must z = -inf, as 0 times infinity does.
+
 // z^2 up to 1e8: from |z| = 1e4 on p is 0 or 1 and the slope's cubic factor must
-// stay finite beside a 1 - p or p of zero.
+// stay finite beside a 1 - p or p of zero.  (A NaN comes back in the product with z.)
 __device__ __forceinline__ float act_square(float z) { return fminf(z * z, 1e8f); }
 
 // y = res + act(z) and slope = act'(z) of one value.  In the sigmoid family exp(-v)
@@ -92,9 +95,10 @@ __device__ __forceinline__ float act_value(const Epilogue &e, float z, float res
   } else {
     sigmoid_pair<false>(z * fmaf(e.kb, z2, e.ka), p, q);
   }
-  // (|z| beyond 1e31 would overflow beside a p or q of zero: those cases are set)
+  // (|z| beyond 1e31 would overflow beside a p or q of zero: those cases are set;
+  // z - z is 0, or NaN for a z of -inf)
   const float t = z * fmaf(3.f * e.kb, z2, e.ka) * q;
-  slope = p > 0.f ? fmaf(p, t, p) : 0.f;
+  slope = p <= 0.f ? z - z : fmaf(p, t, p);
   if (!kFast && !(q > 0.f)) slope = p;
   return fmaf(z, p, res);
 }
@@ -115,7 +119,7 @@ __device__ __forceinline__ void act_pair(const Epilogue &e, const float (&z)[2],
     const float ca[2] = {e.ka, e.ka}, cb[2] = {3.f * e.kb, 3.f * e.kb};
     // below -1e4 act and slope are 0, and the slope's cubic factor stays finite
     // beside a p of zero; above, z is beyond fp16 before the factor overflows
-    float c[2] = {fmaxf(z[0], -1e4f), fmaxf(z[1], -1e4f)};
+    const float c[2] = {max_nan(z[0], -1e4f), max_nan(z[1], -1e4f)};
     float z2[2], v[2], p[2];
     vec_mul(z2, c, c);
     vec_fma(v, kb, z2, ka);
@@ -123,9 +127,9 @@ __device__ __forceinline__ void act_pair(const Epilogue &e, const float (&z)[2],
 #pragma unroll
     for (int j = 0; j < 2; ++j) p[j] = rcp_fast(1.f + ex2_fast(v[j]));
     // (not contracted with the residual's sum: the same y with and without slopes; z is
-    // read no more, y may be its place)
+    // read no more, y may be its place.  z and not c: -inf times 0 is no number)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) y[j] = __fmul_rn(c[j], p[j]);
+    for (int j = 0; j < 2; ++j) y[j] = __fmul_rn(z[j], p[j]);
     if constexpr (ep_has_slope(kKind)) {
       // p + z p (1 - p) v'(z), and z p is y
       float q[2], t[2];
