@@ -96,7 +96,9 @@ _SIGNATURES = {
                                 _VP]),
     "feql_scan_workspace_bytes": (_SZ, [_I64, _I64, _I, _I, _I, _I, _I]),
     "feql_scan_forward": (_I, [_VP] * 7 + [_SZ, _I64, _I64, _I, _I, _I, _I, _VP]),
+    "feql_scan_forward_diff": (_I, [_VP] * 8 + [_SZ, _I64, _I64, _I, _I, _I, _I, _VP]),
     "feql_scan_backward": (_I, [_VP] * 11 + [_SZ, _I64, _I64, _I, _I, _I, _I, _VP]),
+    "feql_scan_backward_diff": (_I, [_VP] * 9 + [_SZ, _I64, _I64, _I, _I, _I, _I, _VP]),
     "feql_scan_step": (_I, [_VP, _VP, _VP, _VP, _I64, _I, _I, _I, _I, _VP]),
     "feql_device_status": (_I, [_VP]),
     "feql_status_string": (ctypes.c_char_p, [_I]),
@@ -366,12 +368,28 @@ def feql_scan_forward(u, g, h0, offsets, h, hN, ws, ws_bytes: int, B: int, N: in
                                     _stream(stream)), "feql_scan_forward")
 
 
+def feql_scan_forward_diff(u, g, h0, offsets, h, hN, diff, ws, ws_bytes: int, B: int, N: int,
+                           C: int, T: int, shared: bool, dtype: int, stream=None) -> None:
+    _check(load().feql_scan_forward_diff(_ptr(u), _ptr(g), _ptr(h0), _ptr(offsets), _ptr(h),
+                                         _ptr(hN), _ptr(diff), _ptr(ws), ws_bytes, B, N, C, T,
+                                         int(shared), dtype, _stream(stream)),
+           "feql_scan_forward_diff")
+
+
 def feql_scan_backward(dh, u, g, h, h0, dhN, offsets, du, dg, dh0, ws, ws_bytes: int, B: int,
                        N: int, C: int, T: int, shared: bool, dtype: int, stream=None) -> None:
     _check(load().feql_scan_backward(_ptr(dh), _ptr(u), _ptr(g), _ptr(h), _ptr(h0), _ptr(dhN),
                                      _ptr(offsets), _ptr(du), _ptr(dg), _ptr(dh0), _ptr(ws),
                                      ws_bytes, B, N, C, T, int(shared), dtype,
                                      _stream(stream)), "feql_scan_backward")
+
+
+def feql_scan_backward_diff(dh, g, diff, dhN, offsets, du, dg, dh0, ws, ws_bytes: int, B: int,
+                            N: int, C: int, T: int, shared: bool, dtype: int, stream=None) -> None:
+    _check(load().feql_scan_backward_diff(_ptr(dh), _ptr(g), _ptr(diff), _ptr(dhN), _ptr(offsets),
+                                          _ptr(du), _ptr(dg), _ptr(dh0), _ptr(ws), ws_bytes, B, N,
+                                          C, T, int(shared), dtype, _stream(stream)),
+           "feql_scan_backward_diff")
 
 
 def feql_scan_step(u, g, state, h, B: int, C: int, T: int, shared: bool, dtype: int,

@@ -309,34 +309,39 @@ int scan_maps(const ScanPlan &q, const Ty *x, const Ty *g, cudaStream_t st) {
 
 template <typename Ty, int V, int TX, int NW, bool kShared>
 int scan_fwd_run(const ScanPlan &q, const Ty *u, const Ty *g, const float *h0, Ty *h, float *hN,
-                 cudaStream_t st) {
+                 float *diff, cudaStream_t st) {
   constexpr int R = scan_rows_fwd(sizeof(Ty) == 2, V);
   const int bad = scan_maps<Ty, V, TX, kShared, false>(q, u, g, st);
   if (bad != FEQL_OK) return bad;
-  return scan_launch(scan_fwd_kernel<Ty, V, TX, R, NW, kShared>, q,
-                     scan_feed_bytes<Ty, V, R, NW, kShared>(1), st, u, g, h0, h, hN, q.s);
+  auto kernel = scan_fwd_kernel<Ty, V, TX, R, NW, kShared, false>;
+  if constexpr (sizeof(Ty) == 2)
+    if (diff != nullptr) kernel = scan_fwd_kernel<Ty, V, TX, R, NW, kShared, true>;
+  return scan_launch(kernel, q, scan_feed_bytes<Ty, V, R, NW, kShared>(1, false), st, u, g, h0, h,
+                     hN, diff, q.s);
 }
 
 template <typename Ty, int V, int TX, int NW, bool kShared>
 int scan_bwd_run(const ScanPlan &q, const Ty *dh, const Ty *u, const Ty *g, const Ty *h,
-                 const float *h0, const float *dhN, Ty *du, Ty *dg, float *dh0, cudaStream_t st) {
+                 const float *h0, const float *diff, const float *dhN, Ty *du, Ty *dg, float *dh0,
+                 cudaStream_t st) {
   constexpr int R = scan_rows_bwd(sizeof(Ty) == 2, V);
+  constexpr bool kDiff = sizeof(Ty) == 2;
   const int bad = scan_maps<Ty, V, TX, kShared, true>(q, dh, g, st);
   if (bad != FEQL_OK) return bad;
-  return scan_launch(scan_bwd_kernel<Ty, V, TX, R, NW, kShared>, q,
-                     scan_feed_bytes<Ty, V, R, NW, kShared>(3), st, dh, u, g, h, h0, dhN, du, dg,
-                     dh0, q.s);
+  return scan_launch(scan_bwd_kernel<Ty, V, TX, R, NW, kShared, kDiff>, q,
+                     scan_feed_bytes<Ty, V, R, NW, kShared>(kDiff ? 1 : 3, kDiff), st, dh, u, g, h,
+                     h0, diff, dhN, du, dg, dh0, q.s);
 }
 
 template <typename Ty>
 int scan_fwd(const ScanPlan &q, const void *u, const void *g, const float *h0, void *h, float *hN,
-             cudaStream_t st) {
+             float *diff, cudaStream_t st) {
   const bool sh = q.s.FG != q.s.F;
 #define FEQL_CASE(T_, VV, XX, NWW, SH)                                               \
   if (q.V == VV && q.TX == XX && q.NW == NWW && sh == SH)                            \
     return scan_fwd_run<T_, VV, XX, NWW, SH>(q, static_cast<const T_ *>(u),          \
                                              static_cast<const T_ *>(g), h0,         \
-                                             static_cast<T_ *>(h), hN, st);
+                                             static_cast<T_ *>(h), hN, diff, st);
   FEQL_SCAN_CASES(FEQL_CASE, Ty)
 #undef FEQL_CASE
   return FEQL_ERR_UNSUPPORTED;
@@ -344,14 +349,15 @@ int scan_fwd(const ScanPlan &q, const void *u, const void *g, const float *h0, v
 
 template <typename Ty>
 int scan_bwd(const ScanPlan &q, const void *dh, const void *u, const void *g, const void *h,
-             const float *h0, const float *dhN, void *du, void *dg, float *dh0, cudaStream_t st) {
+             const float *h0, const float *diff, const float *dhN, void *du, void *dg, float *dh0,
+             cudaStream_t st) {
   const bool sh = q.s.FG != q.s.F;
 #define FEQL_CASE(T_, VV, XX, NWW, SH)                                                          \
   if (q.V == VV && q.TX == XX && q.NW == NWW && sh == SH)                                       \
     return scan_bwd_run<T_, VV, XX, NWW, SH>(                                                   \
         q, static_cast<const T_ *>(dh), static_cast<const T_ *>(u), static_cast<const T_ *>(g), \
-        static_cast<const T_ *>(h), h0, dhN, static_cast<T_ *>(du), static_cast<T_ *>(dg), dh0, \
-        st);
+        static_cast<const T_ *>(h), h0, diff, dhN, static_cast<T_ *>(du),                       \
+        static_cast<T_ *>(dg), dh0, st);
   FEQL_SCAN_CASES(FEQL_CASE, Ty)
 #undef FEQL_CASE
   return FEQL_ERR_UNSUPPORTED;
@@ -474,9 +480,9 @@ static int scan_prepare(int64_t B, int64_t N, int C, int T, int shared, int dtyp
   return FEQL_OK;
 }
 
-int feql_scan_forward(const void *u, const void *g, const float *h0, const int32_t *offsets,
-                      void *h, float *hN, void *ws, size_t ws_bytes, int64_t B, int64_t N, int C,
-                      int T, int shared, int dtype, feql_stream stream) {
+static int scan_forward(const void *u, const void *g, const float *h0, const int32_t *offsets,
+                        void *h, float *hN, float *diff, void *ws, size_t ws_bytes, int64_t B,
+                        int64_t N, int C, int T, int shared, int dtype, feql_stream stream) {
   const int bad = scan_check(B, N, C, T, dtype, offsets != nullptr);
   if (bad != FEQL_OK) return bad;
   if (!ok_ptr(u, N > 0) || !ok_ptr(g, N > 0) || !ok_ptr(h, N > 0) || !ok_ptr(h0, false) ||
@@ -487,8 +493,24 @@ int feql_scan_forward(const void *u, const void *g, const float *h0, const int32
   const int st = scan_prepare(B, N, C, T, shared, dtype, offsets, false, ws, ws_bytes, &q);
   if (st != FEQL_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return is_half(dtype) ? scan_fwd<__half>(q, u, g, h0, h, hN, s)
-                        : scan_fwd<float>(q, u, g, h0, h, hN, s);
+  return is_half(dtype) ? scan_fwd<__half>(q, u, g, h0, h, hN, diff, s)
+                        : scan_fwd<float>(q, u, g, h0, h, hN, nullptr, s);
+}
+
+int feql_scan_forward(const void *u, const void *g, const float *h0, const int32_t *offsets,
+                      void *h, float *hN, void *ws, size_t ws_bytes, int64_t B, int64_t N, int C,
+                      int T, int shared, int dtype, feql_stream stream) {
+  return scan_forward(u, g, h0, offsets, h, hN, nullptr, ws, ws_bytes, B, N, C, T, shared, dtype,
+                      stream);
+}
+
+int feql_scan_forward_diff(const void *u, const void *g, const float *h0, const int32_t *offsets,
+                           void *h, float *hN, float *diff, void *ws, size_t ws_bytes, int64_t B,
+                           int64_t N, int C, int T, int shared, int dtype, feql_stream stream) {
+  if (!valid_dtype(dtype) || !ok_ptr(diff, N > 0)) return FEQL_ERR_INVALID_ARG;
+  if (!is_half(dtype)) return FEQL_ERR_UNSUPPORTED;
+  return scan_forward(u, g, h0, offsets, h, hN, diff, ws, ws_bytes, B, N, C, T, shared, dtype,
+                      stream);
 }
 
 int feql_scan_backward(const void *dh, const void *u, const void *g, const void *h,
@@ -501,13 +523,32 @@ int feql_scan_backward(const void *dh, const void *u, const void *g, const void 
       !ok_ptr(du, N > 0) || !ok_ptr(dg, N > 0) || !ok_ptr(h0, false) || !ok_ptr(dhN, false) ||
       !ok_ptr(dh0, false) || !ok_ptr(offsets, false) || !ok_ptr(ws, false))
     return FEQL_ERR_INVALID_ARG;
+  if (is_half(dtype)) return FEQL_ERR_UNSUPPORTED;
   if (B == 0) return FEQL_OK;
   ScanPlan q;
   const int st = scan_prepare(B, N, C, T, shared, dtype, offsets, true, ws, ws_bytes, &q);
   if (st != FEQL_OK) return st;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return is_half(dtype) ? scan_bwd<__half>(q, dh, u, g, h, h0, dhN, du, dg, dh0, s)
-                        : scan_bwd<float>(q, dh, u, g, h, h0, dhN, du, dg, dh0, s);
+  return scan_bwd<float>(q, dh, u, g, h, h0, nullptr, dhN, du, dg, dh0,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+int feql_scan_backward_diff(const void *dh, const void *g, const float *diff, const float *dhN,
+                            const int32_t *offsets, void *du, void *dg, float *dh0, void *ws,
+                            size_t ws_bytes, int64_t B, int64_t N, int C, int T, int shared,
+                            int dtype, feql_stream stream) {
+  const int bad = scan_check(B, N, C, T, dtype, offsets != nullptr);
+  if (bad != FEQL_OK) return bad;
+  if (!ok_ptr(dh, N > 0) || !ok_ptr(g, N > 0) || !ok_ptr(diff, N > 0) || !ok_ptr(du, N > 0) ||
+      !ok_ptr(dg, N > 0) || !ok_ptr(dhN, false) || !ok_ptr(dh0, false) ||
+      !ok_ptr(offsets, false) || !ok_ptr(ws, false))
+    return FEQL_ERR_INVALID_ARG;
+  if (!is_half(dtype)) return FEQL_ERR_UNSUPPORTED;
+  if (B == 0) return FEQL_OK;
+  ScanPlan q;
+  const int st = scan_prepare(B, N, C, T, shared, dtype, offsets, true, ws, ws_bytes, &q);
+  if (st != FEQL_OK) return st;
+  return scan_bwd<__half>(q, dh, nullptr, g, nullptr, nullptr, diff, dhN, du, dg, dh0,
+                          reinterpret_cast<cudaStream_t>(stream));
 }
 
 int feql_scan_step(const void *u, const void *g, float *state, void *h, int64_t B, int C, int T,

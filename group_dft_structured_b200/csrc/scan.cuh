@@ -27,11 +27,13 @@
 // second time partly from L2, for as many more blocks.  (Sequences of one
 // segment have no map and cost nothing more.)
 //
-// The backward pass needs h_{l-1} and reads the forward's h: in fp16 its rounding
-// moves dg by at most half a step of h against (h - u), less than dg's own
-// rounding.  Recomputing h from saved tile states was tried: it saves one of six
-// streams but scans every tile twice, 118 us against 104 on 128 x 3136 x 24 x 4
-// with channel gates (91 by now).
+// The backward pass needs h_{l-1} - u_l.  With fp32 data it reads the forward's h and
+// u.  The h of fp16 data is rounded, which moves dg by half a step of h against h - u,
+// without bound where they are close (slowly varying features), so the forward of a
+// training step writes the difference of its fp32 states in fp32 (kDiff), and the
+// backward reads that in the place of u and h: the same bytes there, 4 a value more in
+// the forward.  (16 bits of the difference were not enough: their rounding adds to
+// dg's own, where the bound is one.)
 //
 // Measured, fp16: 128 x 3136 x 24 x 4 with channel gates, forward 44 us (173 MB,
 // 3.9 TB/s) and backward 91 us (405 MB, 4.4 TB/s); one sequence of 65536 x 96 x 4,
@@ -209,11 +211,12 @@ struct ScanFeed<Ty, V, R, NT, false> {
 template <typename Ty, int V>
 constexpr bool scan_async() { return V * sizeof(Ty) >= 4; }
 
-// Shared memory of the feeds: u (and h, dh), and g unless it is shared over the
-// group axis (a two-byte gate per row and channel comes by registers).
+// Shared memory of the feeds: u (or dh with u and h, or with diff), and g unless it is
+// shared over the group axis (a two-byte gate per row and channel comes by registers).
 template <typename Ty, int V, int R, int NW, bool kShared>
-constexpr int scan_feed_bytes(int streams) {
-  return (streams + (kShared ? 0 : 1)) * ScanFeed<Ty, V, R, NW * 32, scan_async<Ty, V>()>::kBytes;
+constexpr int scan_feed_bytes(int streams, bool diff) {
+  return (streams + (kShared ? 0 : 1)) * ScanFeed<Ty, V, R, NW * 32, scan_async<Ty, V>()>::kBytes +
+         (diff ? ScanFeed<float, V, R, NW * 32, true>::kBytes : 0);
 }
 
 __device__ __forceinline__ void async_commit() {
@@ -544,10 +547,12 @@ __device__ __forceinline__ void scan_row_gates(Feed &fg, int r, bool there, floa
   }
 }
 
-template <typename Ty, int V, int TX, int R, int NW, bool kShared>
+// kDiff: writes h_{l-1} - u_l too.
+template <typename Ty, int V, int TX, int R, int NW, bool kShared, bool kDiff>
 __global__ void __launch_bounds__(NW * 32, scan_blocks(NW, kShared && V > 1))
 scan_fwd_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, const float *__restrict__ h0,
-                Ty *__restrict__ h, float *__restrict__ hN, const ScanShape p) {
+                Ty *__restrict__ h, float *__restrict__ hN, float *__restrict__ diff,
+                const ScanShape p) {
   constexpr int GV = kShared ? 1 : V;
   constexpr int TY = NW * 32 / TX, RT = TY * R, NT = NW * 32;
   constexpr bool kAsync = scan_async<Ty, V>(), kLean = kShared && V > 1;
@@ -595,6 +600,7 @@ scan_fwd_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, const float 
   if (at.slot >= p.whole) scan_wait_maps(p);
   scan_enter<false>(p, at, carry);
   Ty *ph = h + row * p.F + at.f;
+  float *pq = kDiff ? diff + row * p.F + at.f : nullptr;
   auto tile = [&](int i, auto rows_of) {
     // the map of the thread's rows: a gate per channel is kept and u read again
     // for the second walk, a gate per value the local states and products
@@ -614,6 +620,9 @@ scan_fwd_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, const float 
     if (NW > 1) __syncthreads();
     join.join(sm, i & 1, i == 0, carry, in);
     if (!at.live) return;
+    float before[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) before[j] = in[j];
 #pragma unroll
     for (int r = 0; r < R; ++r)
       if (rows_of.has(r)) {
@@ -621,6 +630,11 @@ scan_fwd_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, const float 
         if constexpr (kLean) {
           float uv[V], av[V], nav[V];
           fu.get(r, uv);
+          if constexpr (kDiff) {
+            float q[V];
+            vec_sub(q, in, uv);
+            store_state<V>(pq + static_cast<int64_t>(r) * p.F, q);
+          }
           spread(av, a[r]);
           spread(nav, na[r]);
           vec_mul(uv, nav, uv);
@@ -631,13 +645,21 @@ scan_fwd_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, const float 
           float pv[V];
           spread(pv, P[kLean ? 0 : r]);
           vec_fma(o, pv, in, hl[kLean ? 0 : r]);
+          if constexpr (kDiff) {
+            float uv[V];
+            fu.get(r, uv);
+            vec_sub(uv, before, uv);
+            store_state<V>(pq + static_cast<int64_t>(r) * p.F, uv);
+#pragma unroll
+            for (int j = 0; j < V; ++j) before[j] = o[j];
+          }
         }
         Pack<Ty, V> k;
         k.pack(o);
         k.store(ph + static_cast<int64_t>(r) * p.F);
       }
   };
-  for (int i = 0; i < steps; ++i, ph += du) {
+  for (int i = 0; i < steps; ++i, ph += du, pq += kDiff ? du : 0) {
     async_wait_tile<kStages>();
     fu.take(i % kStages);
     fg.take(i % kStages);
@@ -652,13 +674,15 @@ scan_fwd_kernel(const Ty *__restrict__ u, const Ty *__restrict__ g, const float 
   scan_zero_rest<Ty, V, TY>(p, at.b, at.seg, at.nseg, at.ty, at.s, at.e, h, p.F, at.f, at.live);
 }
 
-// h: the forward's output; the state before the first row of a sequence is h0.
-template <typename Ty, int V, int TX, int R, int NW, bool kShared>
+// diff: h_{l-1} - u_l as the forward wrote it (kDiff); else from u and h, the forward's
+// output, where the state before the first row of a sequence is h0.
+template <typename Ty, int V, int TX, int R, int NW, bool kShared, bool kDiff>
 __global__ void __launch_bounds__(NW * 32, scan_blocks(NW, false))
 scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *__restrict__ g,
                 const Ty *__restrict__ h, const float *__restrict__ h0,
-                const float *__restrict__ dhN, Ty *__restrict__ du, Ty *__restrict__ dg,
-                float *__restrict__ dh0, const ScanShape p) {
+                const float *__restrict__ diff, const float *__restrict__ dhN,
+                Ty *__restrict__ du, Ty *__restrict__ dg, float *__restrict__ dh0,
+                const ScanShape p) {
   constexpr int GV = kShared ? 1 : V;
   constexpr int TY = NW * 32 / TX, RT = TY * R, NT = NW * 32;
   constexpr bool kAsync = scan_async<Ty, V>();
@@ -666,11 +690,17 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
   extern __shared__ __align__(16) uint8_t feeds[];
   __shared__ __align__(16) typename J::Smem sm;
   ScanFeed<Ty, V, R, NT, kAsync> fu, fd, fh;
+  ScanFeed<float, V, R, NT, true> fq;
   ScanFeed<Ty, GV, R, NT, kAsync && !kShared> fg;
-  fu.init(feeds);
-  fd.init(feeds + fu.kBytes);
-  fh.init(feeds + 2 * fu.kBytes);
-  fg.init(feeds + 3 * fu.kBytes);
+  fd.init(feeds);
+  if constexpr (kDiff) {
+    fq.init(feeds + fd.kBytes);
+    fg.init(feeds + fd.kBytes + fq.kBytes);
+  } else {
+    fu.init(feeds + fd.kBytes);
+    fh.init(feeds + 2 * fd.kBytes);
+    fg.init(feeds + 3 * fd.kBytes);
+  }
   const ScanPlace<V, TX, NW, kShared> at(p);
   if (!at.work) {
     scan_wait_maps(p);
@@ -681,9 +711,11 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
   const int part = steps - static_cast<int>(rows / RT);  // 1: the first step's tile lacks rows
   // step i takes tile steps - 1 - i: the tiles run from the segment's end
   const int64_t row = at.s + at.r0 + static_cast<int64_t>(steps - 1) * RT + at.ty * R;
-  const Ty *pu = u + row * p.F + at.f, *pd = dh + row * p.F + at.f;
+  const Ty *pd = dh + row * p.F + at.f;
+  const float *pq = kDiff ? diff + row * p.F + at.f : nullptr;
   // the rows before; before the sequence's first row stands h0
-  const Ty *ph = h + (row - 1) * p.F + at.f;
+  const Ty *pu = kDiff ? nullptr : u + row * p.F + at.f;
+  const Ty *ph = kDiff ? nullptr : h + (row - 1) * p.F + at.f;
   const bool top = at.seg == 0 && at.ty == 0;
   const Ty *pg = g + row * p.FG + at.gf;
   const int64_t step = static_cast<int64_t>(RT) * p.F, gstep = static_cast<int64_t>(RT) * p.FG;
@@ -695,21 +727,25 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
     if (i < steps) {
       const int st = i % kStages;
       const bool none = top && i == steps - 1;
-      if (i < part) {
-        const ScanRows<false> n{have()};
-        fu.issue(st, pu, p.F, n);
+      auto rows_of = [&](auto n) {
         fd.issue(st, pd, p.F, n);
-        fh.issue(st, ph, p.F, n, none);
-      } else {
-        const ScanRows<true> n{R};
-        fu.issue(st, pu, p.F, n);
-        fd.issue(st, pd, p.F, n);
-        fh.issue(st, ph, p.F, n, none);
-      }
+        if constexpr (kDiff) {
+          fq.issue(st, pq, p.F, n);
+        } else {
+          fu.issue(st, pu, p.F, n);
+          fh.issue(st, ph, p.F, n, none);
+        }
+      };
+      if (i < part) rows_of(ScanRows<false>{have()});
+      else rows_of(ScanRows<true>{R});
     }
-    pu -= step;
     pd -= step;
-    ph -= step;
+    if constexpr (kDiff) {
+      pq -= step;
+    } else {
+      pu -= step;
+      ph -= step;
+    }
   };
   auto issue_g = [&](int i) {
     if (i < part) fg.issue(i % kStages, pg, p.FG, ScanRows<false>{have()});
@@ -718,14 +754,14 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    if (i < fu.kAhead) issue_x(i);
+    if (i < fd.kAhead) issue_x(i);
     if (i < fg.kAhead) issue_g(i);
     async_commit();
   }
   float carry[V] = {}, start[V] = {};
   const int64_t state = static_cast<int64_t>(at.b) * p.F + at.f;
   if (dhN != nullptr) load_state<V>(dhN + state, carry);
-  if (top && h0 != nullptr) load_state<V>(h0 + state, start);
+  if (!kDiff && top && h0 != nullptr) load_state<V>(h0 + state, start);
   if (at.slot >= p.whole) scan_wait_maps(p);
   scan_enter<true>(p, at, carry);
   Ty *pdu = du + row * p.F + at.f, *pdg = dg + row * p.FG + at.gf;
@@ -751,23 +787,28 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
     join.join(sm, i & 1, i == 0, carry, cin);
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      float uv[V] = {}, before[V] = {}, o[V], gg[V], av[V], nav[V], og[GV];
-      if (rows_of.has(r)) {
-        fu.get(r, uv);
-        fh.get(r, before);
-      }
-      if (r == 0 && top && i == steps - 1) {
+      float off[V] = {}, o[V], gg[V], av[V], nav[V], og[GV];  // off: h_{l-1} - u_l
+      if constexpr (kDiff) {
+        if (rows_of.has(r)) fq.get(r, off);
+      } else {
+        float uv[V] = {};
+        if (rows_of.has(r)) {
+          fu.get(r, uv);
+          fh.get(r, off);
+        }
+        if (r == 0 && top && i == steps - 1) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) before[j] = start[j];
+          for (int j = 0; j < V; ++j) off[j] = start[j];
+        }
+        vec_sub(off, off, uv);
       }
       spread(av, a[r]);
       spread(nav, na[r]);
       vec_add(d[r], d[r], cin);  // delta
       vec_mul(o, nav, d[r]);
       vec_mul(cin, av, d[r]);
-      vec_sub(before, before, uv);
       if constexpr (kShared) {
-        vec_mul(gg, d[r], before);
+        vec_mul(gg, d[r], off);
         float gsum = gg[0];
 #pragma unroll
         for (int j = 1; j < V; ++j) gsum += gg[j];
@@ -777,7 +818,7 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
         for (int k = 1; k < p.m; ++k) sum += __shfl_down_sync(0xffffffffu, gsum, k);
         og[0] = sum;
       } else {
-        vec_mul(gg, o, before);
+        vec_mul(gg, o, off);
         vec_mul(gg, gg, av);
 #pragma unroll
         for (int j = 0; j < V; ++j) og[GV == 1 ? 0 : j] = gg[j];
@@ -794,11 +835,15 @@ scan_bwd_kernel(const Ty *__restrict__ dh, const Ty *__restrict__ u, const Ty *_
   };
   for (int i = 0; i < steps; ++i, pdu -= step, pdg -= gstep) {
     async_wait_tile<kStages>();
-    fu.take(i % kStages);
     fd.take(i % kStages);
-    fh.take(i % kStages);
+    if constexpr (kDiff) {
+      fq.take(i % kStages);
+    } else {
+      fu.take(i % kStages);
+      fh.take(i % kStages);
+    }
     fg.take(i % kStages);
-    issue_x(i + fu.kAhead);
+    issue_x(i + fd.kAhead);
     issue_g(i + fg.kAhead);
     async_commit();
     if (i < part) tile(i, ScanRows<false>{have()});

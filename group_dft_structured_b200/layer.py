@@ -19,8 +19,8 @@ from . import (FEQL_ACT_NONE, FEQL_FP16, FEQL_FP16_SIMT, FEQL_FP32, feql_backwar
                feql_p4m_backward_act, feql_p4m_backward_act_workspace_bytes, feql_p4m_backward_dw,
                feql_p4m_backward_dw_workspace_bytes, feql_p4m_backward_dx, feql_p4m_forward,
                feql_p4m_forward_act, feql_p4m_weight_fft, feql_p4m_weight_fft_bytes,
-               feql_scan_backward, feql_scan_forward, feql_scan_step,
-               feql_scan_workspace_bytes,
+               feql_scan_backward, feql_scan_backward_diff, feql_scan_forward,
+               feql_scan_forward_diff, feql_scan_step, feql_scan_workspace_bytes,
                feql_weight_fft, feql_weight_fft_bytes)
 
 
@@ -416,8 +416,9 @@ def scan_forward(u: torch.Tensor, g: torch.Tensor, h0=None, offsets=None, save: 
     Dense: u (B, L, C, T).  Packed: u (N, C, T) and ``offsets`` (B + 1,) int32,
     sequence b in rows offsets[b]..offsets[b + 1].  g has u's shape, or lacks its
     last axis (one gate per channel).  h0 and hN are (B, C, T) fp32 states;
-    ``saved`` is what scan_backward takes (h and h0, which it reads; None without
-    ``save``).
+    ``saved`` is what scan_backward takes: (h, h0), which it reads, for fp32 data, and
+    for fp16 data, whose h is rounded, (h_{l-1} - u_l in fp32, None); None without
+    ``save``.
     """
     B, N, C, T, shared = _scan_sizes(u, g, offsets)
     mode = _mode(u)
@@ -432,31 +433,44 @@ def scan_forward(u: torch.Tensor, g: torch.Tensor, h0=None, offsets=None, save: 
         nbytes = max(_bytes(feql_scan_workspace_bytes, at, B, N, C, T, shared,
                             offsets is not None, mode), 16)
         ws = u.new_empty(nbytes, dtype=torch.uint8)
+        if save and mode == FEQL_FP16:
+            diff = torch.empty_like(u, dtype=torch.float32)
+            feql_scan_forward_diff(u, g, h0, offsets, h, hN, diff, ws, nbytes, B, N, C, T, shared,
+                                   mode)
+            return h, hN, (diff, None)
         feql_scan_forward(u, g, h0, offsets, h, hN, ws, nbytes, B, N, C, T, shared, mode)
     return h, hN, ((h, h0) if save else None)
 
 
-def scan_backward(dh: torch.Tensor, u: torch.Tensor, g: torch.Tensor, saved, dhN=None,
-                  offsets=None):
-    """du, dg, dh0 of scan_forward on the same u, g and offsets."""
-    B, N, C, T, shared = _scan_sizes(u, g, offsets)
-    mode = _mode(u)
-    with _on(u):
-        at = u.get_device()
-        u = _dense(u)
-        g = _take(g, "g", g.shape, u.dtype, at)
-        dh = _take(dh, "dh", u.shape, u.dtype, at)
+def scan_backward(dh: torch.Tensor, u, g: torch.Tensor, saved, dhN=None, offsets=None):
+    """du, dg, dh0 of scan_forward on the same u, g and offsets.
+
+    ``u`` is not read for fp16 data, and may be None there.
+    """
+    like = dh if u is None else u
+    B, N, C, T, shared = _scan_sizes(like, g, offsets)
+    mode = _mode(like)
+    with _on(like):
+        at = like.get_device()
+        g = _take(g, "g", g.shape, like.dtype, at)
+        dh = _take(dh, "dh", like.shape, like.dtype, at)
         dhN = _take(dhN, "dhN", (B, C, T), torch.float32, at)
         offsets = _take(offsets, "offsets", (B + 1,), torch.int32, at)
-        h = _take(saved[0], "h", u.shape, u.dtype, at)
-        h0 = _take(saved[1], "h0", (B, C, T), torch.float32, at)
-        du, dg = torch.empty_like(u), torch.empty_like(g)
-        dh0 = u.new_empty((B, C, T), dtype=torch.float32)
+        kept = _take(saved[0], "saved", like.shape, torch.float32, at)
+        du, dg = torch.empty_like(dh), torch.empty_like(g)
+        dh0 = dh.new_empty((B, C, T), dtype=torch.float32)
         nbytes = max(_bytes(feql_scan_workspace_bytes, at, B, N, C, T, shared,
                             offsets is not None, mode), 16)
-        ws = u.new_empty(nbytes, dtype=torch.uint8)
-        feql_scan_backward(dh, u, g, h, h0, dhN, offsets, du, dg, dh0, ws, nbytes, B, N, C, T,
-                           shared, mode)
+        ws = dh.new_empty(nbytes, dtype=torch.uint8)
+        if mode == FEQL_FP16:
+            feql_scan_backward_diff(dh, g, kept, dhN, offsets, du, dg, dh0, ws, nbytes, B, N, C, T,
+                                    shared, mode)
+        else:
+            if u is None:
+                raise ValueError("u is read for fp32 data")
+            h0 = _take(saved[1], "h0", (B, C, T), torch.float32, at)
+            feql_scan_backward(dh, _dense(u), g, kept, h0, dhN, offsets, du, dg, dh0, ws, nbytes,
+                               B, N, C, T, shared, mode)
     return du, dg, dh0
 
 

@@ -309,18 +309,21 @@ class EqScanFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, u, g, h0, offsets):
-        h, hN, _ = _L.scan_forward(u, g, h0, offsets, save=False)
-        ctx.save_for_backward(u, g, h, h0, offsets)
+        h, hN, saved = _L.scan_forward(u, g, h0, offsets, save=any(ctx.needs_input_grad[:3]))
+        if saved is not None:
+            # fp16 data: the backward pass reads neither u nor h0 (kept all the same, so that
+            # a state that step() changes in between is refused in both types)
+            ctx.save_for_backward(u if u.dtype == torch.float32 else None, g, saved[0], h0, offsets)
         ctx.set_materialize_grads(False)
         return h, hN
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dh, dhN):
-        u, g, h, h0, offsets = ctx.saved_tensors
+        u, g, kept, h0, offsets = ctx.saved_tensors
         if dh is None:
-            dh = torch.zeros_like(u)
-        du, dg, dh0 = _L.scan_backward(dh, u, g, (h, h0), dhN, offsets)
+            dh = torch.zeros(kept.shape, dtype=g.dtype, device=g.device)
+        du, dg, dh0 = _L.scan_backward(dh, u, g, (kept, h0), dhN, offsets)
         need = ctx.needs_input_grad
         return (du if need[0] else None, dg if need[1] else None, dh0 if need[2] else None, None)
 

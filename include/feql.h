@@ -345,23 +345,39 @@ int feql_norm_backward(const void *x, const void *dy, const float *stats, const 
  *           after the last rows (h0 for an empty sequence), or NULL
  *   ws    : device scratch of ws_bytes >= feql_scan_workspace_bytes(...) (packed: 1
  *           with offsets, else 0), here and in the backward pass
- * States are fp32 throughout. */
+ * States are fp32 throughout; h is their rounding to the data type. */
 size_t feql_scan_workspace_bytes(int64_t B, int64_t N, int C, int T, int shared, int packed,
                                  int dtype);
 int feql_scan_forward(const void *u, const void *g, const float *h0, const int32_t *offsets,
                       void *h, float *hN, void *ws, size_t ws_bytes, int64_t B, int64_t N, int C,
                       int T, int shared, int dtype, feql_stream stream);
 
+/* The forward pass of a training step on fp16 data (others FEQL_ERR_UNSUPPORTED): the same
+ * results, and what the backward pass takes of the states,
+ *   diff : device fp32 [N][C][T] (written), h_{l-1} - u_l from the fp32 states (rows of no
+ *          sequence are left as they are) */
+int feql_scan_forward_diff(const void *u, const void *g, const float *h0, const int32_t *offsets,
+                           void *h, float *hN, float *diff, void *ws, size_t ws_bytes, int64_t B,
+                           int64_t N, int C, int T, int shared, int dtype, feql_stream stream);
+
 /* Gradients of <dh, h> + <dhN, hN>:
  *   delta_l = dh_l + a_{l+1} delta_{l+1} (+ dhN at the last row),
  *   du = (1 - a) delta,  dg = delta (h_{l-1} - u) a (1 - a) (summed over T for
  *   shared gates),  dh0 = a_0 delta_0 (dhN for an empty sequence).
+ * feql_scan_backward takes h_{l-1} from h, which holds the states of fp32 data; those of
+ * fp16 data are rounded there, by more than h - u where the two are close, so fp16 data is
+ * refused (FEQL_ERR_UNSUPPORTED) and goes to feql_scan_backward_diff, as fp32 data is there.
  *   h, h0 : the forward's output and initial states (NULL as there)
+ *   diff  : as written by feql_scan_forward_diff
  *   dhN   : device fp32 [B][C][T] or NULL (zero)   dh0 : the same, or NULL */
 int feql_scan_backward(const void *dh, const void *u, const void *g, const void *h,
                        const float *h0, const float *dhN, const int32_t *offsets, void *du,
                        void *dg, float *dh0, void *ws, size_t ws_bytes, int64_t B, int64_t N,
                        int C, int T, int shared, int dtype, feql_stream stream);
+int feql_scan_backward_diff(const void *dh, const void *g, const float *diff, const float *dhN,
+                            const int32_t *offsets, void *du, void *dg, float *dh0, void *ws,
+                            size_t ws_bytes, int64_t B, int64_t N, int C, int T, int shared,
+                            int dtype, feql_stream stream);
 
 /* One token of each of B sequences: state (fp32 [B][C][T]) becomes
  * a state + (1 - a) u in place, h [B][C][T] its value in the data type. */
