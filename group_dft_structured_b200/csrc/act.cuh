@@ -141,20 +141,29 @@ __device__ __forceinline__ void act_pair(const Epilogue &e, const float (&z)[2],
   }
 }
 
-// dz = dy slope on a packed fp16 pair, rounded once.
-__device__ __forceinline__ uint32_t act_grad2(uint32_t dy, uint32_t slope) {
-  const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&dy),
-                            *reinterpret_cast<const __half2 *>(&slope));
+// GELU's and SiLU's slopes reach 1.13, so dz = dy slope of a finite fp16 dy can leave
+// fp16's range.  It is held divided by a power of two, as the layer's operand planes
+// are, so that the layer's backward takes every finite dy with an activation too.
+
+// dz / 4 on a packed fp16 pair, rounded once (dy / 4 is exact above the subnormals).
+__device__ __forceinline__ uint32_t act_grad_q(uint32_t dy, uint32_t slope) {
+  const __half2 q = __hmul2(*reinterpret_cast<const __half2 *>(&dy), __float2half2_rn(0.25f));
+  const __half2 h = __hmul2(q, *reinterpret_cast<const __half2 *>(&slope));
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// dz = dy slope on n values, 16 bytes per access; HBM-bound (three streams), 144 us
-// on 401408 x 96 x 4 fp16 (6.4 TB/s).
+// What the passes that read dz from memory multiply their results by.
+template <typename Ty>
+constexpr int act_dz_scale() { return sizeof(Ty) == 2 ? 2 : 1; }
+
+// dz = dy slope (fp16: dz / 2) on n values, 16 bytes per access; HBM-bound (three
+// streams), 144 us on 401408 x 96 x 4 fp16 (6.4 TB/s).
 template <typename Ty>
 __global__ void __launch_bounds__(256)
 act_bwd_kernel(const Ty *__restrict__ dy, const Ty *__restrict__ slope, Ty *__restrict__ dz,
                int64_t n) {
   constexpr int V = 16 / sizeof(Ty);
+  constexpr float k = 1.f / act_dz_scale<Ty>();
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   for (int64_t i = i0; i < n / V; i += step) {
@@ -165,12 +174,12 @@ act_bwd_kernel(const Ty *__restrict__ dy, const Ty *__restrict__ slope, Ty *__re
     a.unpack(d);
     b.unpack(w);
 #pragma unroll
-    for (int j = 0; j < V; ++j) d[j] *= w[j];
+    for (int j = 0; j < V; ++j) d[j] *= k * w[j];
     a.pack(d);
     a.store(dz + i * V);
   }
   const int64_t at = n / V * V + i0;
-  if (i0 < n % V) dz[at] = narrow<Ty>(widen(dy[at]) * widen(slope[at]));
+  if (i0 < n % V) dz[at] = narrow<Ty>(widen(dy[at]) * (k * widen(slope[at])));
 }
 
 }  // namespace feql

@@ -132,10 +132,11 @@ bool is_tf32(int dt) { return dt == FEQL_FP32_3XTF32; }
 int what_kind(int dt) { return is_tc(dt) ? kWhatF16 : (is_tf32(dt) ? kWhatTF32 : kWhatSimt); }
 // ---------------------------------------------------------------- tc launch
 // tf32: fp32 data in the split-TF32 mode (FEQL_FP32_3XTF32), else fp16.
-// ep: activation, residual and saved z, or nullptr.
+// ep: activation, residual and saved slope, or nullptr; twice: fp16 data without ep,
+// twice the result (as g8 and simt passes below).
 int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const void *bias,
                    void *out, int64_t N, cudaStream_t stream, bool tf32 = false,
-                   const Epilogue *ep = nullptr) {
+                   const Epilogue *ep = nullptr, bool twice = false) {
   DeviceInfo dev;
   int st = device_info(&dev);
   if (st != FEQL_OK) return st;
@@ -206,7 +207,9 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
     st = make_tmap_f16(&tm_res, p.ep.res, N, static_cast<int64_t>(P.Do) * kT, 32, 8 * kT);
     if (st != FEQL_OK) return st;
   }
-  auto kernel = tf32 ? tc_fourier_gemm_kernel<true> : tc_fourier_gemm_kernel<false>;
+  auto kernel = tf32    ? tc_fourier_gemm_kernel<true>
+                : twice ? tc_fourier_gemm_kernel<false, kEpNone, 2>
+                        : tc_fourier_gemm_kernel<false>;
   if (ep != nullptr) {
     switch (epilogue_kind(*ep)) {
       case kEpMax:
@@ -233,7 +236,7 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
 
 template <typename T>
 int launch_simt_fwd(const void *in, const float *Wp, const void *bias, void *out, int64_t N,
-                    int Ci, int Do, cudaStream_t stream, const Epilogue *ep = nullptr) {
+                    int Ci, int Do, cudaStream_t stream, const Epilogue *ep, bool twice) {
   const int64_t gx = cdiv(N, kSimtTile);
   if (gx > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(Do, kSimtTile)));
@@ -241,6 +244,8 @@ int launch_simt_fwd(const void *in, const float *Wp, const void *bias, void *out
   auto kernel = ep == nullptr ? simt_fwd_kernel<T>
                 : ep_is_max(epilogue_kind(*ep)) ? simt_fwd_kernel<T, kEpMax>
                                                 : simt_fwd_kernel<T, kEpSigmoid>;
+  if constexpr (sizeof(T) == 2)
+    if (twice) kernel = simt_fwd_kernel<T, kEpNone, 2>;
   kernel<<<grid, kSimtThreads, 0, stream>>>(
       static_cast<const T *>(in), Wp, static_cast<const T *>(bias), static_cast<T *>(out), N, Ci,
       Do, ep != nullptr ? *ep : Epilogue{});
@@ -314,7 +319,7 @@ int64_t tc_dw_ws_floats(const TcDwParams &p) {
 }
 
 int launch_tc_dw(TcDwParams p, const void *x, const void *dy, __half *dW, __half *db, float *ws,
-                 const DeviceInfo &dev, cudaStream_t stream) {
+                 const DeviceInfo &dev, cudaStream_t stream, float scale = 1.f) {
   if (dev.cc_major != 10) return FEQL_ERR_UNSUPPORTED;
   p.ws = ws;
   p.ws_db = ws + static_cast<int64_t>(p.splits) * 4 * p.D * p.Cs;
@@ -347,7 +352,7 @@ int launch_tc_dw(TcDwParams p, const void *x, const void *dy, __half *dW, __half
   }
   {
     const int r = launch_dw_tc_reduce(p.ws, p.ws_db, dW, db, p.N > 0 ? p.splits : 0, p.C, p.D,
-                                      p.Cs, dev.sms, stream);
+                                      p.Cs, dev.sms, stream, scale);
     if (r != 0) return r == 1 ? FEQL_ERR_UNSUPPORTED : FEQL_ERR_CUDA;
   }
   return launch_status();
@@ -442,7 +447,7 @@ int launch_tc_bwd(TcBwdParams p, const void *x, const void *dy, const uint8_t *w
 // ---------------------------------------------------------------------------
 template <class Gp>
 int launch_g8_fwd(const void *in, const uint8_t *wt, const G8Plan &P, const __half *bias,
-                   void *out, int64_t N, cudaStream_t stream, const Epilogue *ep = nullptr) {
+                   void *out, int64_t N, cudaStream_t stream, const Epilogue *ep, bool twice) {
   DeviceInfo dev;
   int st = device_info(&dev);
   if (st != FEQL_OK) return st;
@@ -496,7 +501,8 @@ int launch_g8_fwd(const void *in, const uint8_t *wt, const G8Plan &P, const __ha
     st = make_tmap_f16(&tm_slope, p.ep.slope, N, static_cast<int64_t>(P.Do) * T, 32, 8 * T);
   if (st != FEQL_OK) return st;
   const int smem = g8_fwd_smem(p).total + 1024;
-  auto kernel = ep == nullptr ? tc_g8_fwd_kernel<Gp>
+  auto kernel = twice           ? tc_g8_fwd_kernel<Gp, kEpNone, 2>
+                : ep == nullptr ? tc_g8_fwd_kernel<Gp>
                 : epilogue_kind(*ep) == kEpMax      ? tc_g8_fwd_kernel<Gp, kEpMax>
                 : epilogue_kind(*ep) == kEpMaxSlope ? tc_g8_fwd_kernel<Gp, kEpMaxSlope>
                 : epilogue_kind(*ep) == kEpSigmoid  ? tc_g8_fwd_kernel<Gp, kEpSigmoid>
@@ -541,7 +547,7 @@ int64_t g8_dw_ws_floats(const G8DwParams &p, int T) {
 
 template <class Gp>
 int launch_g8_dw(const void *x, const void *dy, __half *dW, __half *db, float *ws,
-                  size_t ws_bytes, int64_t N, int C, int D, cudaStream_t stream) {
+                  size_t ws_bytes, int64_t N, int C, int D, cudaStream_t stream, float scale) {
   DeviceInfo dev;
   int st = device_info(&dev);
   if (st != FEQL_OK) return st;
@@ -581,7 +587,7 @@ int launch_g8_dw(const void *x, const void *dy, __half *dW, __half *db, float *w
   const int64_t rblocks = g8_reduce_blocks(C, D);
   if (rblocks > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
   g8_dw_reduce_kernel<Gp><<<static_cast<unsigned>(rblocks), kRed8Out * kRed8Groups, 0, stream>>>(
-      p.ws, p.ws_db, dW, db, p.splits, C, D, p.Cs);
+      p.ws, p.ws_db, dW, db, p.splits, C, D, p.Cs, scale);
   return launch_status();
 }
 
@@ -701,7 +707,7 @@ int g8_weight_fft(const void *W, void *What, int C, int D, feql_stream stream) {
 
 template <class Gp>
 int g8_pass(const void *in, const void *What, const void *bias, void *out, int64_t N, int C, int D,
-            feql_stream stream, int dir, const Epilogue *ep = nullptr) {
+            feql_stream stream, int dir, const Epilogue *ep = nullptr, bool twice = false) {
   if (N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK) return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (in == nullptr || What == nullptr || out == nullptr)) return FEQL_ERR_INVALID_ARG;
   if (!aligned16(in) || !aligned16(What) || !aligned16(out)) return FEQL_ERR_INVALID_ARG;
@@ -710,7 +716,7 @@ int g8_pass(const void *in, const void *What, const void *bias, void *out, int64
   const G8Layout L = make_g8_layout(C, D, Gp::kWRows);
   const uint8_t *wt = static_cast<const uint8_t *>(What) + (dir == 0 ? L.off_fwd : L.off_dx);
   return launch_g8_fwd<Gp>(in, wt, dir == 0 ? L.fwd : L.dx, static_cast<const __half *>(bias),
-                           out, N, reinterpret_cast<cudaStream_t>(stream), ep);
+                           out, N, reinterpret_cast<cudaStream_t>(stream), ep, twice);
 }
 
 size_t g8_dw_workspace_bytes(int64_t N, int C, int D, int T) {
@@ -722,7 +728,7 @@ size_t g8_dw_workspace_bytes(int64_t N, int C, int D, int T) {
 
 template <class Gp>
 int g8_dw(const void *x, const void *dy, void *dW, void *db, void *ws, size_t ws_bytes, int64_t N,
-          int C, int D, feql_stream stream) {
+          int C, int D, feql_stream stream, float scale = 1.f) {
   if (dW == nullptr || ws == nullptr || N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK)
     return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (x == nullptr || dy == nullptr)) return FEQL_ERR_INVALID_ARG;
@@ -731,7 +737,7 @@ int g8_dw(const void *x, const void *dy, void *dW, void *db, void *ws, size_t ws
     return FEQL_ERR_INVALID_ARG;
   return launch_g8_dw<Gp>(x, dy, static_cast<__half *>(dW), static_cast<__half *>(db),
                           static_cast<float *>(ws), ws_bytes, N, C, D,
-                          reinterpret_cast<cudaStream_t>(stream));
+                          reinterpret_cast<cudaStream_t>(stream), scale);
 }
 
 }  // namespace
@@ -775,7 +781,7 @@ int feql_weight_fft(const void *W, void *What, int C, int D, int dtype, feql_str
 
 static int pass_common(const void *in, const void *What, const void *bias, void *out, int64_t N,
                        int C, int D, int dtype, feql_stream stream, int dir,
-                       const Epilogue *ep = nullptr) {
+                       const Epilogue *ep = nullptr, bool twice = false) {
   if (!valid_dtype(dtype) || N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK)
     return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (in == nullptr || What == nullptr || out == nullptr)) return FEQL_ERR_INVALID_ARG;
@@ -793,11 +799,11 @@ static int pass_common(const void *in, const void *What, const void *bias, void 
   }
   if (is_tc(dt)) {
     const uint8_t *wt = static_cast<const uint8_t *>(What) + (dir == 0 ? L.off_fwd : L.off_dx);
-    return launch_tc_gemm(in, wt, dir == 0 ? L.fwd : L.dx, bias, out, N, s, false, ep);
+    return launch_tc_gemm(in, wt, dir == 0 ? L.fwd : L.dx, bias, out, N, s, false, ep, twice);
   }
   const float *Wp = static_cast<const float *>(What) + (dir == 0 ? L.off_fwd : L.off_dx) / 4;
-  if (is_half(dt)) return launch_simt_fwd<__half>(in, Wp, bias, out, N, Ci, Do, s, ep);
-  return launch_simt_fwd<float>(in, Wp, bias, out, N, Ci, Do, s, ep);
+  if (is_half(dt)) return launch_simt_fwd<__half>(in, Wp, bias, out, N, Ci, Do, s, ep, twice);
+  return launch_simt_fwd<float>(in, Wp, bias, out, N, Ci, Do, s, ep, false);
 }
 
 int feql_forward(const void *x, const void *What, const void *b, void *y, int64_t N, int C, int D,
@@ -852,8 +858,10 @@ int feql_backward(const void *x, const void *dy, const void *What, void *dx, voi
   return feql_backward_dw(x, dy, dW, db, ws, ws_bytes, N, C, D, dtype, stream);
 }
 
-int feql_backward_dw(const void *x, const void *dy, void *dW, void *db, void *ws, size_t ws_bytes,
-                     int64_t N, int C, int D, int dtype, feql_stream stream) {
+// scale: a power of two on dW and db.
+static int backward_dw(const void *x, const void *dy, void *dW, void *db, void *ws,
+                       size_t ws_bytes, int64_t N, int C, int D, int dtype, feql_stream stream,
+                       float scale) {
   if (!valid_dtype(dtype) || dW == nullptr || ws == nullptr) return FEQL_ERR_INVALID_ARG;
   if (N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK) return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (x == nullptr || dy == nullptr)) return FEQL_ERR_INVALID_ARG;
@@ -871,7 +879,7 @@ int feql_backward_dw(const void *x, const void *dy, void *dW, void *db, void *ws
     TcDwParams p = make_tc_dw_plan(N, C, D, dev.sms);
     if (ws_bytes < static_cast<size_t>(tc_dw_ws_floats(p)) * 4) return FEQL_ERR_INVALID_ARG;
     return launch_tc_dw(p, x, dy, static_cast<__half *>(dW), static_cast<__half *>(db),
-                        static_cast<float *>(ws), dev, s);
+                        static_cast<float *>(ws), dev, s, scale);
   }
   const DwPlan q = make_dw_plan(N, C, D, dev.sms);
   if (ws_bytes < static_cast<size_t>(q.ws_floats) * 4) return FEQL_ERR_INVALID_ARG;
@@ -885,15 +893,20 @@ int feql_backward_dw(const void *x, const void *dy, void *dW, void *db, void *ws
         static_cast<const __half *>(x), static_cast<const __half *>(dy), wsf, wsdb, N, C, D,
         q.split_len);
     dw_reduce_kernel<__half><<<split_sum_blocks(C, D), kSumThreads, 0, s>>>(
-        wsf, wsdb, static_cast<__half *>(dW), static_cast<__half *>(db), q.splits, C, D);
+        wsf, wsdb, static_cast<__half *>(dW), static_cast<__half *>(db), q.splits, C, D, scale);
   } else {
     simt_dw_partial_kernel<float><<<grid, kSimtThreads, 0, s>>>(
         static_cast<const float *>(x), static_cast<const float *>(dy), wsf, wsdb, N, C, D,
         q.split_len);
     dw_reduce_kernel<float><<<split_sum_blocks(C, D), kSumThreads, 0, s>>>(
-        wsf, wsdb, static_cast<float *>(dW), static_cast<float *>(db), q.splits, C, D);
+        wsf, wsdb, static_cast<float *>(dW), static_cast<float *>(db), q.splits, C, D, scale);
   }
   return launch_status();
+}
+
+int feql_backward_dw(const void *x, const void *dy, void *dW, void *db, void *ws, size_t ws_bytes,
+                     int64_t N, int C, int D, int dtype, feql_stream stream) {
+  return backward_dw(x, dy, dW, db, ws, ws_bytes, N, C, D, dtype, stream, 1.f);
 }
 
 // ---------------------------------------------------------------------------
@@ -928,12 +941,14 @@ int feql_ct_weight_fft(int T, const void *W, void *What, int C, int D, int dtype
 
 static int ct_pass(int T, const void *in, const void *What, const void *bias, void *out, int64_t N,
                    int C, int D, int dtype, feql_stream stream, int dir,
-                   const Epilogue *ep = nullptr) {
+                   const Epilogue *ep = nullptr, bool twice = false) {
   int path = 0;
   const int st = ct_route(T, C, D, dtype, &path);
   if (st != FEQL_OK) return st;
-  if (path == kCtTensor8) return g8_pass<Cyclic8>(in, What, bias, out, N, C, D, stream, dir, ep);
-  if (path == kCtTensor6) return g8_pass<Cyclic6>(in, What, bias, out, N, C, D, stream, dir, ep);
+  if (path == kCtTensor8) 
+    return g8_pass<Cyclic8>(in, What, bias, out, N, C, D, stream, dir, ep, twice);
+  if (path == kCtTensor6)
+    return g8_pass<Cyclic6>(in, What, bias, out, N, C, D, stream, dir, ep, twice);
   if (N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK) return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (in == nullptr || What == nullptr || out == nullptr)) return FEQL_ERR_INVALID_ARG;
   if (!aligned16(in) || !aligned16(What) || !aligned16(out)) return FEQL_ERR_INVALID_ARG;
@@ -942,8 +957,9 @@ static int ct_pass(int T, const void *in, const void *What, const void *bias, vo
   const float *Wp = static_cast<const float *>(What) + (dir == 0 ? 0 : static_cast<int64_t>(T) * C * D);
   const int Ci = dir == 0 ? C : D, Do = dir == 0 ? D : C;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return is_half(resolve(dtype)) ? ct_simt_pass<__half>(T, in, Wp, bias, out, N, Ci, Do, s, ep)
-                                 : ct_simt_pass<float>(T, in, Wp, bias, out, N, Ci, Do, s, ep);
+  return is_half(resolve(dtype))
+             ? ct_simt_pass<__half>(T, in, Wp, bias, out, N, Ci, Do, s, ep, twice)
+             : ct_simt_pass<float>(T, in, Wp, bias, out, N, Ci, Do, s, ep, false);
 }
 
 int feql_ct_forward(int T, const void *x, const void *What, const void *b, void *y, int64_t N,
@@ -970,14 +986,17 @@ size_t feql_ct_backward_dw_workspace_bytes(int T, int64_t N, int C, int D, int d
   return static_cast<size_t>(ct_dw_ws_floats(make_ct_dw_plan(N, C, D, dev.sms), T, C, D)) * 4;
 }
 
-int feql_ct_backward_dw(int T, const void *x, const void *dy, void *dW, void *db, void *ws,
-                        size_t ws_bytes, int64_t N, int C, int D, int dtype, feql_stream stream) {
-  if (T == 4) return feql_backward_dw(x, dy, dW, db, ws, ws_bytes, N, C, D, dtype, stream);
+static int ct_backward_dw(int T, const void *x, const void *dy, void *dW, void *db, void *ws,
+                          size_t ws_bytes, int64_t N, int C, int D, int dtype, feql_stream stream,
+                          float scale) {
+  if (T == 4) return backward_dw(x, dy, dW, db, ws, ws_bytes, N, C, D, dtype, stream, scale);
   int path = 0;
   int st = ct_route(T, C, D, dtype, &path);
   if (st != FEQL_OK) return st;
-  if (path == kCtTensor8) return g8_dw<Cyclic8>(x, dy, dW, db, ws, ws_bytes, N, C, D, stream);
-  if (path == kCtTensor6) return g8_dw<Cyclic6>(x, dy, dW, db, ws, ws_bytes, N, C, D, stream);
+  if (path == kCtTensor8)
+    return g8_dw<Cyclic8>(x, dy, dW, db, ws, ws_bytes, N, C, D, stream, scale);
+  if (path == kCtTensor6)
+    return g8_dw<Cyclic6>(x, dy, dW, db, ws, ws_bytes, N, C, D, stream, scale);
   if (dW == nullptr || ws == nullptr || N < 0 || N > kMaxTokens || check_shape(C, D) != FEQL_OK)
     return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (x == nullptr || dy == nullptr)) return FEQL_ERR_INVALID_ARG;
@@ -990,8 +1009,13 @@ int feql_ct_backward_dw(int T, const void *x, const void *dy, void *dW, void *db
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   float *w = static_cast<float *>(ws);
   return is_half(resolve(dtype))
-             ? ct_simt_dw<__half>(T, x, dy, dW, db, w, ws_bytes, N, C, D, s, dev.sms)
-             : ct_simt_dw<float>(T, x, dy, dW, db, w, ws_bytes, N, C, D, s, dev.sms);
+             ? ct_simt_dw<__half>(T, x, dy, dW, db, w, ws_bytes, N, C, D, s, dev.sms, scale)
+             : ct_simt_dw<float>(T, x, dy, dW, db, w, ws_bytes, N, C, D, s, dev.sms, scale);
+}
+
+int feql_ct_backward_dw(int T, const void *x, const void *dy, void *dW, void *db, void *ws,
+                        size_t ws_bytes, int64_t N, int C, int D, int dtype, feql_stream stream) {
+  return ct_backward_dw(T, x, dy, dW, db, ws, ws_bytes, N, C, D, dtype, stream, 1.f);
 }
 
 // ---------------------------------------------------------------------------
@@ -1109,6 +1133,7 @@ static int backward_act(GroupKind G, const void *x, const void *dy, const void *
   const ActWorkspace w = act_workspace(G, N, C, D, act, dtype);
   if (ws_bytes < w.total) return FEQL_ERR_INVALID_ARG;
   const void *dz = dy;
+  bool twice = false;  // dz holds half of it
   if (act != FEQL_ACT_NONE && N > 0) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // where the layer's fused backward holds the slopes too, dz stays on chip
@@ -1135,17 +1160,21 @@ static int backward_act(GroupKind G, const void *x, const void *dy, const void *
     st = launch_status();
     if (st != FEQL_OK) return st;
     dz = to;
+    twice = is_half(dtype);
   }
-  if (!G.p4m && G.T == kT && dx != nullptr && dW != nullptr && N > 0)
+  if (!G.p4m && G.T == kT && dx != nullptr && dW != nullptr && N > 0 && !twice)
     return feql_backward(x, dz, What, dx, dW, db, ws, w.dw, N, C, D, dtype, stream);
   if (dx != nullptr) {
-    st = G.p4m ? feql_p4m_backward_dx(dz, What, dx, N, C, D, dtype, stream)
-               : feql_ct_backward_dx(G.T, dz, What, dx, N, C, D, dtype, stream);
+    st = G.p4m         ? g8_pass<Dihedral4>(dz, What, nullptr, dx, N, C, D, stream, 1, nullptr, twice)
+         : G.T == kT   ? pass_common(dz, What, nullptr, dx, N, C, D, dtype, stream, 1, nullptr, twice)
+                       : ct_pass(G.T, dz, What, nullptr, dx, N, C, D, dtype, stream, 1, nullptr,
+                                 twice);
     if (st != FEQL_OK) return st;
   }
   if (dW == nullptr) return FEQL_OK;
-  return G.p4m ? feql_p4m_backward_dw(x, dz, dW, db, ws, w.dw, N, C, D, dtype, stream)
-               : feql_ct_backward_dw(G.T, x, dz, dW, db, ws, w.dw, N, C, D, dtype, stream);
+  const float scale = twice ? 2.f : 1.f;
+  return G.p4m ? g8_dw<Dihedral4>(x, dz, dW, db, ws, w.dw, N, C, D, stream, scale)
+               : ct_backward_dw(G.T, x, dz, dW, db, ws, w.dw, N, C, D, dtype, stream, scale);
 }
 
 int feql_forward_act(const void *x, const void *What, const void *b, const void *res, void *y,

@@ -705,7 +705,8 @@ struct G8Units {
 // residual by TMA into a box of each epilogue warp, its next one loaded as soon as
 // one has been read, the slopes through boxes beside y's (direct accesses, a row of
 // 128 bytes to a lane, took 65 us instead of 45 on 50000 x 12 -> 48, p4m).
-template <class Gp, int kEp = kEpNone>
+// kOut: a power of two that the results are multiplied by (kEpNone).
+template <class Gp, int kEp = kEpNone, int kOut = 1>
 __global__ void __maxnreg__(96)
 tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
                  const __grid_constant__ CUtensorMap tm_res,
@@ -925,7 +926,7 @@ tc_g8_fwd_kernel(const __grid_constant__ CUtensorMap tm_in, const __grid_constan
             float F[T], y[T];
 #pragma unroll
             for (int bk = 0; bk < T; ++bk) F[bk] = __uint_as_float(Y[bk][i]);
-            Gp::inverse(F, y, 64.f);  // planes and weights both carry 1/8
+            Gp::inverse(F, y, 64.f * kOut);  // planes and weights both carry 1/8
             const float bv = sbias[d0 + 4 * h + i];
 #pragma unroll
             for (int e = 0; e < T / 2; ++e) {
@@ -1270,7 +1271,8 @@ tc_g8_dw_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant
 // the eight bin planes, and db[d].  A block takes 16 consecutive (d, c) outputs
 // (the last blocks take db); its 32 warps each sum every 32nd split (the loads
 // of a warp's splits are independent, so they overlap), then warp 0 adds the
-// 32 partial sums in warp order: the same grouping on every run.
+// 32 partial sums in warp order: the same grouping on every run.  scale: a power of two
+// on dW and db.
 constexpr int kRed8Out = 16, kRed8Groups = 32;
 
 __host__ __device__ inline int64_t g8_reduce_blocks(int C, int D) {
@@ -1281,7 +1283,7 @@ template <class Gp>
 __global__ void __launch_bounds__(kRed8Out * kRed8Groups)
 g8_dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db,
                      __half *__restrict__ dW, __half *__restrict__ db, int splits, int C, int D,
-                     int Cs) {
+                     int Cs, float scale) {
   constexpr int T = Gp::kT;
   __shared__ float part[kRed8Groups][T][kRed8Out];
   const int64_t n = static_cast<int64_t>(D) * C;
@@ -1312,7 +1314,7 @@ g8_dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_d
 #pragma unroll
         for (int k = 0; k < T; ++k) t[k] += part[q][k][lo];
       float y[T];
-      Gp::inverse(t, y, 64.f);  // x and dy planes both carry 1/8
+      Gp::inverse(t, y, 64.f * scale);  // x and dy planes both carry 1/8
       uint32_t hv[T / 2];
 #pragma unroll
       for (int k = 0; k < T / 2; ++k) hv[k] = pack_half2(y[2 * k], y[2 * k + 1]);
@@ -1328,7 +1330,7 @@ g8_dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_d
     if (grp == 0 && d < D) {
       float t = 0.f;
       for (int q = 0; q < kRed8Groups; ++q) t += part[q][0][lo];
-      db[d] = __float2half_rn(8.f * t);  // bin 0 of the dy planes carries 1/8
+      db[d] = __float2half_rn(8.f * scale * t);  // bin 0 of the dy planes carries 1/8
     }
   }
 }

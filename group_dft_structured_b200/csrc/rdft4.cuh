@@ -43,4 +43,17 @@ __device__ __forceinline__ void rdft4_pair_q(const uint4 &v, uint32_t &b0, uint3
   b1n = as_u32(__highs2half2(d0, d1));
 }
 
+// The same of a fibre whose values carry the 1/4 already.
+__device__ __forceinline__ void rdft4_pair(const uint4 &v, uint32_t &b0, uint32_t &b2,
+                                           uint32_t &b1r, uint32_t &b1n) {
+  const __half2 a0 = as_h2(v.x), c0 = as_h2(v.y), a1 = as_h2(v.z), c1 = as_h2(v.w);
+  const __half2 s0 = __hadd2(a0, c0), d0 = __hsub2(a0, c0);
+  const __half2 s1 = __hadd2(a1, c1), d1 = __hsub2(a1, c1);
+  const __half2 p = __lows2half2(s0, s1), q = __highs2half2(s0, s1);
+  b0 = as_u32(__hadd2(p, q));
+  b2 = as_u32(__hsub2(p, q));
+  b1r = as_u32(__lows2half2(d0, d1));
+  b1n = as_u32(__highs2half2(d0, d1));
+}
+
 }  // namespace feql

@@ -69,8 +69,8 @@ __device__ __forceinline__ void irdft4(float Y0, float Y2, float Y1r, float Y1i,
 }
 
 // Forward / dX: out[n][o][:] = irdft( sum_i What_k[o][i] * rdft(in[n][i][:]) ) (+ bias[o]).
-// kEp != kEpNone: then y = res + act(z) (act.cuh).
-template <typename T, int kEp = kEpNone>
+// kEp != kEpNone: then y = res + act(z) (act.cuh).  kOut: a power of two on the results.
+template <typename T, int kEp = kEpNone, int kOut = 1>
 __global__ void __launch_bounds__(kSimtThreads)
 simt_fwd_kernel(const T *__restrict__ in, const float *__restrict__ Wp, const T *__restrict__ bias,
                 T *__restrict__ out, int64_t N, int Ci, int Do, const Epilogue ep = {}) {
@@ -145,6 +145,9 @@ simt_fwd_kernel(const T *__restrict__ in, const float *__restrict__ Wp, const T 
       if (o >= Do) continue;
       float y[4];
       irdft4(acc[0][i][j], acc[1][i][j], acc[2][i][j], acc[3][i][j], y);
+      if constexpr (kOut != 1)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) y[t] *= kOut;
       if (bias != nullptr) {
         const float bv = to_f32(bias[o]);
         y[0] += bv; y[1] += bv; y[2] += bv; y[3] += bv;
@@ -253,11 +256,12 @@ simt_dw_partial_kernel(const T *__restrict__ x, const T *__restrict__ dy, float 
 }
 
 // Deterministic reduction over splits (fixed order), inverse rDFT, cast:
-//   dW[d][c][u] = (G0 + (-1)^u G2)/4 + Re(G1 i^u)/2,  db[d] = sum of partials.
+//   dW[d][c][u] = (G0 + (-1)^u G2)/4 + Re(G1 i^u)/2,  db[d] = sum of partials,
+// both times scale (a power of two).
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads)
 dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db, T *__restrict__ dW,
-                 T *__restrict__ db, int splits, int C, int D) {
+                 T *__restrict__ db, int splits, int C, int D, float scale) {
   __shared__ float buf[kSumLines][kSumOut];
   const int64_t plane = static_cast<int64_t>(D) * C, blocks_w = (plane + kSumOut - 1) / kSumOut;
   const int lane = threadIdx.x % kSumOut;
@@ -266,13 +270,14 @@ dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db, 
     split_sums<kT>(ws, plane, e, splits, buf);
     if (threadIdx.x < kSumOut && e < plane) {
       float w[4];
-      irdft4(buf[0][lane], buf[1][lane], buf[2][lane], buf[3][lane], w);
+      irdft4(scale * buf[0][lane], scale * buf[1][lane], scale * buf[2][lane],
+             scale * buf[3][lane], w);
       Vec4<T>::store(dW + e * kT, w);
     }
   } else if (db != nullptr) {
     const int64_t d = (blockIdx.x - blocks_w) * static_cast<int64_t>(kSumOut) + lane;
     split_sums<1>(ws_db, D, d, splits, buf);
-    if (threadIdx.x < kSumOut && d < D) db[d] = static_cast<T>(buf[0][lane]);
+    if (threadIdx.x < kSumOut && d < D) db[d] = static_cast<T>(scale * buf[0][lane]);
   }
 }
 

@@ -139,8 +139,8 @@ __global__ void ct_simt_wfft_kernel(const Ty *__restrict__ W, float *__restrict_
 }
 
 // Forward / dX: out[n][o][:] = irDFT( per bin sum_i Wp_k[o][i] * rDFT(in[n][i][:]) ) (+ bias);
-// kEp != kEpNone: then res + act of it (act.cuh).
-template <int T, typename Ty, int kEp = kEpNone>
+// kEp != kEpNone: then res + act of it (act.cuh).  kOut: a power of two on the results.
+template <int T, typename Ty, int kEp = kEpNone, int kOut = 1>
 __global__ void __launch_bounds__(kCtThreads)
 ct_simt_fwd_kernel(const Ty *__restrict__ in, const float *__restrict__ Wp,
                    const Ty *__restrict__ bias, Ty *__restrict__ out, int64_t N, int Ci, int Do,
@@ -228,6 +228,7 @@ ct_simt_fwd_kernel(const Ty *__restrict__ in, const float *__restrict__ Wp,
       Ty *dst = out + (n * Do + o) * T;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
+        if constexpr (kOut != 1) y[t] *= kOut;
         float v = y[t] + bv;
         if constexpr (kEp != kEpNone) {
           // not contracted with the inverse's last product: the same y in both forms
@@ -352,11 +353,13 @@ ct_simt_dw_kernel(const Ty *__restrict__ x, const Ty *__restrict__ dy, float *__
   }
 }
 
-// Fixed-order sum of the split partials, then dW[d][c][:] = irDFT(G[d][c]) and db.
+// Fixed-order sum of the split partials, then dW[d][c][:] = irDFT(G[d][c]) and db, times
+// scale (a power of two).
 template <int T, typename Ty>
 __global__ void __launch_bounds__(kSumThreads)
 ct_simt_dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db,
-                         Ty *__restrict__ dW, Ty *__restrict__ db, int splits, int C, int D) {
+                         Ty *__restrict__ dW, Ty *__restrict__ db, int splits, int C, int D,
+                         float scale) {
   __shared__ float cs[CtBins<T>::kBins][T], sn[CtBins<T>::kBins][T];
   __shared__ float buf[kSumLines][kSumOut];
   ct_twiddles<T>(cs, sn);
@@ -369,7 +372,7 @@ ct_simt_dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__
     if (threadIdx.x < kSumOut && e < plane) {
       float G[T], y[T];
 #pragma unroll
-      for (int p = 0; p < T; ++p) G[p] = buf[p][lane];
+      for (int p = 0; p < T; ++p) G[p] = scale * buf[p][lane];
       ct_inverse<T>(G, cs, sn, y);
 #pragma unroll
       for (int t = 0; t < T; ++t) dW[e * T + t] = ct_cast<Ty>(y[t]);
@@ -377,7 +380,7 @@ ct_simt_dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__
   } else if (db != nullptr) {
     const int64_t d = (blockIdx.x - blocks_w) * static_cast<int64_t>(kSumOut) + lane;
     split_sums<1>(ws_db, D, d, splits, buf);
-    if (threadIdx.x < kSumOut && d < D) db[d] = ct_cast<Ty>(buf[0][lane]);
+    if (threadIdx.x < kSumOut && d < D) db[d] = ct_cast<Ty>(scale * buf[0][lane]);
   }
 }
 

@@ -43,13 +43,14 @@ inline int64_t ct_dw_ws_floats(const CtDwPlan &p, int T, int C, int D) {
 template <typename Ty>
 int ct_simt_wfft(int T, const void *W, void *What, int C, int D, cudaStream_t s, int sms);
 
-// Forward or dX pass; ep: activation, residual and saved z, or nullptr.
+// Forward or dX pass; ep: activation, residual and saved slope, or nullptr; twice: of
+// fp16 data, without ep, twice the result.
 template <typename Ty>
 int ct_simt_pass(int T, const void *in, const float *Wp, const void *bias, void *out, int64_t N,
-                 int Ci, int Do, cudaStream_t s, const Epilogue *ep = nullptr);
+                 int Ci, int Do, cudaStream_t s, const Epilogue *ep, bool twice);
 
 template <typename Ty>
 int ct_simt_dw(int T, const void *x, const void *dy, void *dW, void *db, float *ws, size_t ws_bytes,
-               int64_t N, int C, int D, cudaStream_t s, int sms);
+               int64_t N, int C, int D, cudaStream_t s, int sms, float scale);
 
 }  // namespace feql

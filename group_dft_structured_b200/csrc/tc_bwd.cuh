@@ -117,8 +117,8 @@ __host__ __device__ inline BwSmem tc_bwd_smem(const TcBwdParams &p) {
 // kAct: the gradient through an activation, dz = dy slope (act.cuh), in place of dy.
 // A stage's slopes come by TMA into one buffer beside the stages' (the transform
 // reads it first, so it is free again while the stage's MMAs run), and the
-// transform multiplies its dy fibres before their rDFT: dz is rounded to fp16 as
-// the separate kernel rounds it, and never goes to memory.  401408 x 24 -> 96: 226 us
+// transform multiplies its dy fibres before their rDFT: dz / 4 is rounded to fp16 (the
+// planes' own scale), and never goes to memory.  401408 x 24 -> 96: 226 us
 // for the two kernels, 144 us for this one.
 template <bool kDbCol, bool kAct = false>
 __global__ void __maxnreg__(80)
@@ -330,8 +330,10 @@ tc_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__
               if (b < p.nqd) {  // the same for a whole warp
                 const uint4 z = *reinterpret_cast<const uint4 *>(smem + L.sl + b * kBwBox + r * 128 +
                                                                 ((q ^ (r & 7)) << 4));
-                v = make_uint4(act_grad2(v.x, z.x), act_grad2(v.y, z.y), act_grad2(v.z, z.z),
-                               act_grad2(v.w, z.w));
+                v = make_uint4(act_grad_q(v.x, z.x), act_grad_q(v.y, z.y), act_grad_q(v.z, z.z),
+                               act_grad_q(v.w, z.w));
+                rdft4_pair(v, pl[k][0][q], pl[k][1][q], pl[k][2][q], pl[k][3][q]);
+                continue;
               }
             }
             rdft4_pair_q(v, pl[k][0][q], pl[k][1][q], pl[k][2][q], pl[k][3][q]);

@@ -372,7 +372,7 @@ constexpr int64_t kRedScalarMaxOut = 8192;  // D * C up to which the scalar kern
 __global__ void __launch_bounds__(kRedOut * kRedGroups)
 dw_tc_reduce_scalar_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db,
                     __half *__restrict__ dW, __half *__restrict__ db, int splits, int C, int D,
-                    int Cs) {
+                    int Cs, float scale) {
   __shared__ float part[kRedGroups][4][kRedOut];
   pdl_wait();
   const int64_t plane = static_cast<int64_t>(D) * Cs;
@@ -399,10 +399,11 @@ dw_tc_reduce_scalar_kernel(const float *__restrict__ ws, const float *__restrict
       for (int q = 0; q < kRedGroups; ++q)
 #pragma unroll
         for (int k = 0; k < 4; ++k) t[k] += part[q][k][lo];
-      const float ev = 4.f * (t[0] + t[1]), od = 4.f * (t[0] - t[1]);
+      const float k4 = 4.f * scale, k8 = 8.f * scale;
+      const float ev = k4 * (t[0] + t[1]), od = k4 * (t[0] - t[1]);
       uint2 pk;
-      pk.x = pack_half2(ev + 8.f * t[2], od - 8.f * t[3]);
-      pk.y = pack_half2(ev - 8.f * t[2], od + 8.f * t[3]);
+      pk.x = pack_half2(ev + k8 * t[2], od - k8 * t[3]);
+      pk.y = pack_half2(ev - k8 * t[2], od + k8 * t[3]);
       *reinterpret_cast<uint2 *>(dW + e * kT) = pk;
     }
   } else if (db != nullptr) {
@@ -416,7 +417,7 @@ dw_tc_reduce_scalar_kernel(const float *__restrict__ ws, const float *__restrict
     if (grp == 0 && d < D) {
       float t = 0.f;
       for (int q = 0; q < kRedGroups; ++q) t += part[q][0][lo];
-      db[d] = __float2half_rn(4.f * t);
+      db[d] = __float2half_rn(4.f * scale * t);
     }
   }
 }
@@ -429,7 +430,7 @@ __host__ __device__ inline int64_t dw_reduce_scalar_blocks(int C, int D) {
 // Sum of the split partials in a fixed order, inverse rDFT, fp16 cast:
 //   dW[d][c][u] = (G0 + (-1)^u G2)/4 + Re(G1 i^u)/2,   db[d] = sum of partials.
 // The partials come from planes divided by 4 on both sides (G/16, and db/4),
-// so the constants applied are 4, 8 and 4.
+// so the constants applied are 4, 8 and 4, times scale (a power of two).
 // A dW block owns `q` quads (one d, four consecutive c, all four bins: 16
 // floats) and 256/q split groups; thread (group g, quad) adds splits g, g +
 // groups, ... with 16-byte loads, then the groups are folded pairwise in a fixed
@@ -458,7 +459,7 @@ __host__ __device__ inline RedPlan make_red_plan(int C, int D, int sms) {
 __global__ void __launch_bounds__(kRedThreads)
 dw_tc_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db,
                     __half *__restrict__ dW, __half *__restrict__ db, int splits, int C, int D,
-                    int Cs, int q, int64_t wblocks) {
+                    int Cs, int q, int64_t wblocks, float scale) {
   __shared__ float red[16][kRedThreads];
   pdl_wait();
   const int t = threadIdx.x;
@@ -503,10 +504,11 @@ dw_tc_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_d
         const int c = c0 + i;
         if (c >= C) break;
         const float g0 = red[i][t], g2 = red[4 + i][t], gr = red[8 + i][t], gi = red[12 + i][t];
-        const float ev = 4.f * (g0 + g2), od = 4.f * (g0 - g2);
+        const float k4 = 4.f * scale, k8 = 8.f * scale;
+        const float ev = k4 * (g0 + g2), od = k4 * (g0 - g2);
         uint2 pk;
-        pk.x = pack_half2(ev + 8.f * gr, od - 8.f * gi);
-        pk.y = pack_half2(ev - 8.f * gr, od + 8.f * gi);
+        pk.x = pack_half2(ev + k8 * gr, od - k8 * gi);
+        pk.y = pack_half2(ev - k8 * gr, od + k8 * gi);
         *reinterpret_cast<uint2 *>(dW + (static_cast<int64_t>(d) * C + c) * kT) = pk;
       }
     }
@@ -524,7 +526,7 @@ dw_tc_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_d
       if (grp < h) red[0][t] += red[0][t + h * kRedDbItems];
     }
     __syncthreads();
-    if (grp == 0 && d < D) db[d] = __float2half_rn(4.f * red[0][t]);
+    if (grp == 0 && d < D) db[d] = __float2half_rn(4.f * scale * red[0][t]);
   }
 }
 
@@ -533,7 +535,8 @@ dw_tc_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_d
 // stream: its blocks take the SMs as that kernel's CTAs exit and wait there
 // (pdl_wait) for its partial sums, so no launch gap separates the two.
 inline int launch_dw_tc_reduce(const float *ws, const float *ws_db, __half *dW, __half *db,
-                               int splits, int C, int D, int Cs, int sms, cudaStream_t stream) {
+                               int splits, int C, int D, int Cs, int sms, cudaStream_t stream,
+                               float scale = 1.f) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -546,14 +549,15 @@ inline int launch_dw_tc_reduce(const float *ws, const float *ws_db, __half *dW, 
   if (static_cast<int64_t>(D) * C <= kRedScalarMaxOut) {
     cfg.gridDim = dim3(static_cast<unsigned>(dw_reduce_scalar_blocks(C, D)));
     cfg.blockDim = dim3(kRedOut * kRedGroups);
-    e = cudaLaunchKernelEx(&cfg, dw_tc_reduce_scalar_kernel, ws, ws_db, dW, db, splits, C, D, Cs);
+    e = cudaLaunchKernelEx(&cfg, dw_tc_reduce_scalar_kernel, ws, ws_db, dW, db, splits, C, D, Cs,
+                           scale);
   } else {
     const RedPlan rp = make_red_plan(C, D, sms);
     if (rp.blocks > 0x7fffffff) return 1;
     cfg.gridDim = dim3(static_cast<unsigned>(rp.blocks));
     cfg.blockDim = dim3(kRedThreads);
     e = cudaLaunchKernelEx(&cfg, dw_tc_reduce_kernel, ws, ws_db, dW, db, splits, C, D, Cs, rp.q,
-                           rp.wblocks);
+                           rp.wblocks, scale);
   }
   return e == cudaSuccess ? 0 : 2;
 }

@@ -181,7 +181,8 @@ struct TcUnits {
 // ring of kResDepth slots, so the loads run kResDepth blocks ahead (direct loads in
 // the block that uses them cost an HBM latency each: 123 us instead of 78 with two
 // teams on 65536 x 192 -> 192; 85 us with three, 3.6 TB/s).
-template <bool kTF32, int kEp = kEpNone>
+// kOut: a power of two that the fp16 results are multiplied by (kEpNone).
+template <bool kTF32, int kEp = kEpNone, int kOut = 1>
 __global__ void __maxnreg__(96)
 tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
                        const __grid_constant__ CUtensorMap tm_res, const TcFwdParams p) {
@@ -672,9 +673,10 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
                 const float Yr = __uint_as_float(yr[hf][i]), Yi = __uint_as_float(yi[hf][i]);
                 const float bv = cc ? b1 : b0;
                 // planes and weights are both stored divided by 4 (Y = 16 * acc)
-                const float e = fmaf(4.f, Y0 + Y2, bv), o = fmaf(4.f, Y0 - Y2, bv);
-                w[2 * cc] = pack_half2(fmaf(8.f, Yr, e), fmaf(-8.f, Yi, o));
-                w[2 * cc + 1] = pack_half2(fmaf(-8.f, Yr, e), fmaf(8.f, Yi, o));
+                constexpr float k4 = 4.f * kOut, k8 = 8.f * kOut;
+                const float e = fmaf(k4, Y0 + Y2, bv), o = fmaf(k4, Y0 - Y2, bv);
+                w[2 * cc] = pack_half2(fmaf(k8, Yr, e), fmaf(-k8, Yi, o));
+                w[2 * cc + 1] = pack_half2(fmaf(-k8, Yr, e), fmaf(k8, Yi, o));
               }
               const int64_t row = row0 + 16 * hf + 8 * rr;
               if (row < p.N)

@@ -281,7 +281,9 @@ int feql_p4m_forward_act(const void *x, const void *What, const void *b, const v
                          feql_stream stream);
 
 /* Backward: dz = dy slope, then dx, dW and db of the layer for dz (the
- * residual's gradient is dy itself).  dz is rounded to the data type.
+ * residual's gradient is dy itself).  dz is rounded to the data type; in fp16 a power of
+ * two below 1 rides along, so every finite dy is accepted, as by the layer (slopes reach
+ * 1.13), and what falls among the subnormals is rounded to steps of at most 2^-22.
  *   slope : as saved by the forward pass (NULL for FEQL_ACT_NONE: dz = dy)
  *   dx : device [N][C][T] or NULL          dW : [D][C][T] or NULL
  *   db : [D] or NULL (NULL without dW); not both dx and dW NULL
