@@ -172,14 +172,19 @@ class EqLinear(torch.nn.Module):
 
     def fourier_weight(self) -> torch.Tensor:
         W = self.weight
+        if W.is_inference():  # changes of such a weight leave no trace
+            return self._transformed()
         key = (W.device, W.dtype, W.data_ptr(), W._version, tuple(W.shape))
         if self._what is None or self._what_key != key:
-            with torch.no_grad():
-                Wc = W.detach().contiguous()
-                self._what = (_L.p4m_weight_fft(Wc, mode_for(W.dtype)) if self.group == "p4m"
-                              else _L.ct_weight_fft(Wc, mode_for(W.dtype)))
+            self._what = self._transformed()
             self._what_key = key
         return self._what
+
+    def _transformed(self) -> torch.Tensor:
+        wfft = _L.p4m_weight_fft if self.group == "p4m" else _L.ct_weight_fft
+        # an ordinary tensor, which later calls may save for their backward pass
+        with torch.inference_mode(False), torch.no_grad():
+            return wfft(self.weight.detach().contiguous(), mode_for(self.weight.dtype))
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         C, D, T = self.in_channels, self.out_channels, self.group_order

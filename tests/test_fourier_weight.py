@@ -1,0 +1,91 @@
+"""EqLinear's Fourier weight buffer follows the weight: across inference mode, captured
+graphs and streams.  The first tests put a counting stand-in in the place of the
+library's transform and need no GPU."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import group_dft_structured_b200 as F
+from group_dft_structured_b200 import module as M
+from group_dft_structured_b200.module import EqLinear
+
+
+# ------------------------------------------------------------------ CPU ---
+
+class Fake:
+    """The weight transform and what torch says of streams."""
+
+    def __init__(self, patch):
+        self.calls, self.stream, self.capturing = 0, 1, False
+        patch.setattr(M._L, "ct_weight_fft", self.transform)
+        patch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capturing)
+        patch.setattr(torch.cuda, "current_stream",
+                      lambda device=None: type("S", (), {"cuda_stream": self.stream}))
+
+    def transform(self, W, mode, stream=None):
+        self.calls += 1
+        return 2 * W
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    return Fake(monkeypatch)
+
+
+def test_once_per_weight(fake):
+    m = EqLinear(3, 5)
+    first = m.fourier_weight()
+    assert m.fourier_weight() is first and fake.calls == 1
+    with torch.no_grad():
+        m.weight.mul_(2)
+    assert torch.equal(m.fourier_weight(), 2 * m.weight) and fake.calls == 2
+
+
+def test_made_in_inference_mode_and_used_outside(fake):
+    m = EqLinear(3, 5)
+    with torch.inference_mode():
+        What = m.fourier_weight()
+    assert not What.is_inference()
+    assert m.fourier_weight() is What and fake.calls == 1
+
+
+def test_weights_made_in_inference_mode(fake):
+    with torch.inference_mode():
+        m = EqLinear(3, 5)
+        m.fourier_weight()
+        m.weight.mul_(2)
+        assert torch.equal(m.fourier_weight(), 2 * m.weight)
+
+
+# ------------------------------------------------------------------ GPU ---
+
+@pytest.fixture
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from group_dft_structured_b200 import build
+    build.build()
+    F.load()
+    torch.manual_seed(7)
+    yield
+    assert F.feql_device_status() == F.FEQL_OK
+
+
+KINDS = [dict(), dict(activation="gelu"), dict(group="p4m", group_order=8, activation="relu")]
+
+
+def layer(kind, **kw):
+    m = EqLinear(16, 24, device="cuda", **kind, **kw)
+    return m, torch.randn(70, 16 * m.group_order, device="cuda").half()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_inference_then_training(gpu, kind):
+    m, x = layer(kind)
+    with torch.inference_mode():
+        want = m(x).clone()
+    y = m(x)
+    y.sum().backward()
+    assert torch.equal(y, want) and m.weight.grad.isfinite().all()
