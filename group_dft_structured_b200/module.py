@@ -134,7 +134,7 @@ class EqLinear(torch.nn.Module):
     group D4 (T = 8: rotations (r, 0) at 0..3, reflected (r, 1) at 4..7).  The
     Fourier weight buffer is rebuilt when the weight changes (tracked by its
     storage and version counter), so it is computed once per optimizer step, or
-    once for inference.  ``activation`` ("relu", "gelu": the tanh form, "silu") is
+    once for inference; a captured graph computes it at every replay.  ``activation`` ("relu", "gelu": the tanh form, "silu") is
     applied to the output and ``forward``'s ``residual`` added after it, both in
     the epilogue of the layer's products.
     """
@@ -172,7 +172,10 @@ class EqLinear(torch.nn.Module):
 
     def fourier_weight(self) -> torch.Tensor:
         W = self.weight
-        if W.is_inference():  # changes of such a weight leave no trace
+        # An inference tensor's changes leave no version.  A graph under capture has the
+        # transform in itself: its replays follow the weight, and nothing that they have
+        # yet to compute is kept for eager calls.
+        if W.is_inference() or torch.cuda.is_current_stream_capturing():
             return self._transformed()
         key = (W.device, W.dtype, W.data_ptr(), W._version, tuple(W.shape))
         if self._what is None or self._what_key != key:

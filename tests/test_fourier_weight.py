@@ -58,6 +58,19 @@ def test_weights_made_in_inference_mode(fake):
         assert torch.equal(m.fourier_weight(), 2 * m.weight)
 
 
+def test_a_captured_transform_is_in_the_graph_alone(fake):
+    m = EqLinear(3, 5)
+    fake.capturing = True
+    captured = m.fourier_weight()
+    fake.capturing = False
+    eager = m.fourier_weight()
+    assert eager is not captured and fake.calls == 2
+    fake.capturing = True  # with the eager one at hand
+    assert m.fourier_weight() is not eager and fake.calls == 3
+    fake.capturing = False
+    assert m.fourier_weight() is eager and fake.calls == 3
+
+
 # ------------------------------------------------------------------ GPU ---
 
 @pytest.fixture
@@ -89,3 +102,27 @@ def test_inference_then_training(gpu, kind):
     y = m(x)
     y.sum().backward()
     assert torch.equal(y, want) and m.weight.grad.isfinite().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("warm", [False, True])
+@pytest.mark.parametrize("kind", KINDS)
+def test_captured_calls_follow_the_weight(gpu, kind, warm):
+    m, x = layer(kind)
+    with torch.no_grad():
+        if warm:
+            m(x)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            y = m(x)
+        eager = m(x)  # before any replay
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager)
+        for _ in range(2):
+            m.weight.mul_(-1.5)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, m(x)) and not torch.equal(y, eager)
