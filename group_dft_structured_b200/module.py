@@ -134,7 +134,8 @@ class EqLinear(torch.nn.Module):
     group D4 (T = 8: rotations (r, 0) at 0..3, reflected (r, 1) at 4..7).  The
     Fourier weight buffer is rebuilt when the weight changes (tracked by its
     storage and version counter), so it is computed once per optimizer step, or
-    once for inference; a captured graph computes it at every replay.  ``activation`` ("relu", "gelu": the tanh form, "silu") is
+    once for inference, on each stream that calls; a captured graph computes it at
+    every replay.  ``activation`` ("relu", "gelu": the tanh form, "silu") is
     applied to the output and ``forward``'s ``residual`` added after it, both in
     the epilogue of the layer's products.
     """
@@ -158,8 +159,7 @@ class EqLinear(torch.nn.Module):
             torch.empty((out_channels, in_channels, group_order), dtype=dtype, device=device))
         self.bias = (torch.nn.Parameter(torch.empty((out_channels,), dtype=dtype, device=device))
                      if bias else None)
-        self._what = None
-        self._what_key = None
+        self._whats = {}  # stream: (what the weight was, its Fourier weight buffer)
         self.reset_parameters()
 
     def reset_parameters(self) -> None:
@@ -178,10 +178,13 @@ class EqLinear(torch.nn.Module):
         if W.is_inference() or torch.cuda.is_current_stream_capturing():
             return self._transformed()
         key = (W.device, W.dtype, W.data_ptr(), W._version, tuple(W.shape))
-        if self._what is None or self._what_key != key:
-            self._what = self._transformed()
-            self._what_key = key
-        return self._what
+        # a buffer to each stream: made, used and given back in its order alone
+        stream = torch.cuda.current_stream(W.device).cuda_stream
+        kept = self._whats.get(stream)
+        if kept is None or kept[0] != key:
+            self._whats = {s: k for s, k in self._whats.items() if k[0] == key}
+            kept = self._whats[stream] = (key, self._transformed())
+        return kept[1]
 
     def _transformed(self) -> torch.Tensor:
         wfft = _L.p4m_weight_fft if self.group == "p4m" else _L.ct_weight_fft

@@ -71,6 +71,22 @@ def test_a_captured_transform_is_in_the_graph_alone(fake):
     assert m.fourier_weight() is eager and fake.calls == 3
 
 
+def test_streams_do_not_share_a_buffer(fake):
+    m = EqLinear(3, 5)
+    first = m.fourier_weight()
+    fake.stream = 2
+    second = m.fourier_weight()
+    assert second is not first and fake.calls == 2
+    fake.stream = 1
+    assert m.fourier_weight() is first and fake.calls == 2
+    with torch.no_grad():
+        m.weight.mul_(2)
+    for stream in (2, 1):
+        fake.stream = stream
+        assert torch.equal(m.fourier_weight(), 2 * m.weight)
+    assert fake.calls == 4 and len(m._whats) == 2
+
+
 # ------------------------------------------------------------------ GPU ---
 
 @pytest.fixture
@@ -126,3 +142,30 @@ def test_captured_calls_follow_the_weight(gpu, kind, warm):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, m(x)) and not torch.equal(y, eager)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_two_streams_at_once(gpu, kind):
+    """The first stream is far from done with its transform when the second calls."""
+    m, x = layer(kind)
+    m2, _ = layer(kind)
+    with torch.no_grad():
+        m2.weight.copy_(m.weight)
+        if m.bias is not None:
+            m2.bias.copy_(m.bias)
+        want = m2(x)
+        a, b = torch.cuda.Stream(), torch.cuda.Stream()
+        for step in range(3):
+            for s in (a, b):
+                s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(a):
+                torch.cuda._sleep(20000000)  # some 10 ms
+                ya = m(x)
+            with torch.cuda.stream(b):
+                yb = m(x)
+            torch.cuda.synchronize()
+            assert torch.equal(ya, want) and torch.equal(yb, want), step
+            m.weight.neg_()
+            m2.weight.neg_()
+            want = m2(x)
