@@ -202,20 +202,21 @@ class EqLinear(torch.nn.Module):
         x3 = x.reshape(-1, C, T).contiguous()
         if x3.dtype != self.weight.dtype:
             raise TypeError(f"input dtype {x3.dtype} differs from the weight's {self.weight.dtype}")
-        if residual is None and self.activation == "none":
-            y = EqLinearFunction.apply(x3, self.weight, self.bias, self.fourier_weight(),
-                                       mode_for(self.weight.dtype), self.group)
-            return y.reshape(*lead, D * T)
+        if self.weight.device != x.device:
+            raise ValueError(f"input on {x.device}, weight on {self.weight.device}")
         if residual is not None:
             if residual.shape != (*lead, D * T):
                 raise ValueError(f"expected a residual of shape {(*lead, D * T)}, got "
                                  f"{tuple(residual.shape)}")
             residual = residual.reshape(-1, D, T)
-        with torch.cuda.device(x.device):
+        mode = mode_for(self.weight.dtype)
+        with torch.cuda.device(x.device):  # which need not be the current one
             What = self.fourier_weight()
-        y = EqLinearActFunction.apply(x3, self.weight, self.bias, residual, What,
-                                      mode_for(self.weight.dtype), self.group,
-                                      ACTIVATIONS[self.activation])
+            if residual is None and self.activation == "none":
+                y = EqLinearFunction.apply(x3, self.weight, self.bias, What, mode, self.group)
+            else:
+                y = EqLinearActFunction.apply(x3, self.weight, self.bias, residual, What, mode,
+                                              self.group, ACTIVATIONS[self.activation])
         return y.reshape(*lead, D * T)
 
     def extra_repr(self) -> str:
