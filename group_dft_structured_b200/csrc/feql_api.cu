@@ -1119,8 +1119,9 @@ static int backward_act(GroupKind G, const void *x, const void *dy, const void *
                         int64_t N, int C, int D, int act, int dtype, feql_stream stream) {
   int st = act_check(G, N, C, D, act, dtype);
   if (st != FEQL_OK) return st;
-  if (ws == nullptr || (dx == nullptr && dW == nullptr) || (dW == nullptr && db != nullptr))
-    return FEQL_ERR_INVALID_ARG;
+  if (dW == nullptr && db != nullptr) return FEQL_ERR_INVALID_ARG;
+  if (N == 0 && dW == nullptr) return FEQL_OK;  // the dx of no tokens may be NULL
+  if (ws == nullptr || (dx == nullptr && dW == nullptr)) return FEQL_ERR_INVALID_ARG;
   if (N > 0 && (dy == nullptr || (act != FEQL_ACT_NONE && slope == nullptr) ||
                 (dx != nullptr && What == nullptr) || (dW != nullptr && x == nullptr)))
     return FEQL_ERR_INVALID_ARG;

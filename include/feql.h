@@ -286,7 +286,7 @@ int feql_p4m_forward_act(const void *x, const void *What, const void *b, const v
  * 1.13), and what falls among the subnormals is rounded to steps of at most 2^-22.
  *   slope : as saved by the forward pass (NULL for FEQL_ACT_NONE: dz = dy)
  *   dx : device [N][C][T] or NULL          dW : [D][C][T] or NULL
- *   db : [D] or NULL (NULL without dW); not both dx and dW NULL
+ *   db : [D] or NULL (NULL without dW); not both dx and dW NULL (unless N == 0)
  *   ws : ws_bytes >= feql_*_backward_act_workspace_bytes for these sizes (which
  *        includes room for dz) */
 size_t feql_backward_act_workspace_bytes(int64_t N, int C, int D, int act, int dtype);
