@@ -888,17 +888,21 @@ static int backward_dw(const void *x, const void *dy, void *dW, void *db, void *
   dim3 grid(static_cast<unsigned>(cdiv(D, kSimtTile)), static_cast<unsigned>(cdiv(C, kSimtTile)),
             static_cast<unsigned>(q.splits));
   if (grid.y > 65535) return FEQL_ERR_UNSUPPORTED;
+  const bool wide = split_sum_wide(C, D, q.splits, dev.sms);
+  const unsigned blocks = split_sum_blocks(C, D, wide, dev.sms);
   if (is_half(dt)) {
     simt_dw_partial_kernel<__half><<<grid, kSimtThreads, 0, s>>>(
         static_cast<const __half *>(x), static_cast<const __half *>(dy), wsf, wsdb, N, C, D,
         q.split_len);
-    dw_reduce_kernel<__half><<<split_sum_blocks(C, D), kSumThreads, 0, s>>>(
+    auto reduce = wide ? dw_reduce_kernel<__half, true> : dw_reduce_kernel<__half, false>;
+    reduce<<<blocks, kSumThreads, 0, s>>>(
         wsf, wsdb, static_cast<__half *>(dW), static_cast<__half *>(db), q.splits, C, D, scale);
   } else {
     simt_dw_partial_kernel<float><<<grid, kSimtThreads, 0, s>>>(
         static_cast<const float *>(x), static_cast<const float *>(dy), wsf, wsdb, N, C, D,
         q.split_len);
-    dw_reduce_kernel<float><<<split_sum_blocks(C, D), kSumThreads, 0, s>>>(
+    auto reduce = wide ? dw_reduce_kernel<float, true> : dw_reduce_kernel<float, false>;
+    reduce<<<blocks, kSumThreads, 0, s>>>(
         wsf, wsdb, static_cast<float *>(dW), static_cast<float *>(db), q.splits, C, D, scale);
   }
   return launch_status();

@@ -258,10 +258,27 @@ simt_dw_partial_kernel(const T *__restrict__ x, const T *__restrict__ dy, float 
 // Deterministic reduction over splits (fixed order), inverse rDFT, cast:
 //   dW[d][c][u] = (G0 + (-1)^u G2)/4 + Re(G1 i^u)/2,  db[d] = sum of partials,
 // both times scale (a power of two).
-template <typename T>
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kSumThreads)
 dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db, T *__restrict__ dW,
                  T *__restrict__ db, int splits, int C, int D, float scale) {
+  if constexpr (kWide) {
+    const int64_t plane = static_cast<int64_t>(D) * C;
+    for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < plane + D;
+         e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+      if (e < plane) {
+        float g[4], w[4];
+        split_walk<kT>(ws, plane, e, splits, g);
+        irdft4(scale * g[0], scale * g[1], scale * g[2], scale * g[3], w);
+        Vec4<T>::store(dW + e * kT, w);
+      } else if (db != nullptr) {
+        float s[1];
+        split_walk<1>(ws_db, D, e - plane, splits, s);
+        db[e - plane] = static_cast<T>(scale * s[0]);
+      }
+    }
+    return;
+  }
   __shared__ float buf[kSumLines][kSumOut];
   const int64_t plane = static_cast<int64_t>(D) * C, blocks_w = (plane + kSumOut - 1) / kSumOut;
   const int lane = threadIdx.x % kSumOut;

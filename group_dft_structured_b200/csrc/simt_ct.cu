@@ -50,7 +50,9 @@ int ct_simt_dw_launch(const void *x, const void *dy, void *dW, void *db, float *
         static_cast<const Ty *>(x), static_cast<const Ty *>(dy), ws, ws_db, N, C, D, p.split_len,
         p.tiles_d, p.tiles_c);
   }
-  ct_simt_dw_reduce_kernel<T, Ty><<<split_sum_blocks(C, D), kSumThreads, 0, s>>>(
+  const bool wide = split_sum_wide(C, D, p.splits, sms);
+  auto reduce = wide ? ct_simt_dw_reduce_kernel<T, Ty, true> : ct_simt_dw_reduce_kernel<T, Ty, false>;
+  reduce<<<split_sum_blocks(C, D, wide, sms), kSumThreads, 0, s>>>(
       ws, ws_db, static_cast<Ty *>(dW), static_cast<Ty *>(db), p.splits, C, D, scale);
   return launch_status();
 }

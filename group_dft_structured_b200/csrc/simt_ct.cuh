@@ -355,15 +355,35 @@ ct_simt_dw_kernel(const Ty *__restrict__ x, const Ty *__restrict__ dy, float *__
 
 // Fixed-order sum of the split partials, then dW[d][c][:] = irDFT(G[d][c]) and db, times
 // scale (a power of two).
-template <int T, typename Ty>
+template <int T, typename Ty, bool kWide>
 __global__ void __launch_bounds__(kSumThreads)
 ct_simt_dw_reduce_kernel(const float *__restrict__ ws, const float *__restrict__ ws_db,
                          Ty *__restrict__ dW, Ty *__restrict__ db, int splits, int C, int D,
                          float scale) {
   __shared__ float cs[CtBins<T>::kBins][T], sn[CtBins<T>::kBins][T];
-  __shared__ float buf[kSumLines][kSumOut];
   ct_twiddles<T>(cs, sn);
   __syncthreads();
+  if constexpr (kWide) {
+    const int64_t plane = static_cast<int64_t>(D) * C;
+    for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < plane + D;
+         e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+      if (e < plane) {
+        float G[T], y[T];
+        split_walk<T>(ws, plane, e, splits, G);
+#pragma unroll
+        for (int p = 0; p < T; ++p) G[p] *= scale;
+        ct_inverse<T>(G, cs, sn, y);
+#pragma unroll
+        for (int t = 0; t < T; ++t) dW[e * T + t] = ct_cast<Ty>(y[t]);
+      } else if (db != nullptr) {
+        float s[1];
+        split_walk<1>(ws_db, D, e - plane, splits, s);
+        db[e - plane] = ct_cast<Ty>(scale * s[0]);
+      }
+    }
+    return;
+  }
+  __shared__ float buf[kSumLines][kSumOut];
   const int64_t plane = static_cast<int64_t>(D) * C, blocks_w = (plane + kSumOut - 1) / kSumOut;
   const int lane = threadIdx.x % kSumOut;
   if (blockIdx.x < blocks_w) {

@@ -21,7 +21,7 @@ struct CtDwPlan {
 };
 
 // Token splits: about two blocks per SM over all (d, c) tiles, at most 64 (the
-// reduce sums them serially per output).
+// reduce adds them in order, by split_sum.cuh).
 inline CtDwPlan make_ct_dw_plan(int64_t N, int C, int D, int sms) {
   CtDwPlan p;
   p.tiles_d = static_cast<int>(cdiv(D, kCtTile));
