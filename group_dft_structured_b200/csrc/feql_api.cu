@@ -131,6 +131,19 @@ bool is_tf32(int dt) { return dt == FEQL_FP32_3XTF32; }
 // Layout kind of the Fourier-weight buffer of a (resolved) mode.
 int what_kind(int dt) { return is_tc(dt) ? kWhatF16 : (is_tf32(dt) ? kWhatTF32 : kWhatSimt); }
 // ---------------------------------------------------------------- tc launch
+// The kernel of an epilogue (split TF32 takes a slope or none in either kind).
+using TcKernel = void (*)(const CUtensorMap, const CUtensorMap, const TcFwdParams);
+template <bool kTF32, int kTeams>
+TcKernel tc_ep_kernel(int kind) {
+  constexpr int kMax = kTF32 ? kEpMax : kEpMaxSlope, kSig = kTF32 ? kEpSigmoid : kEpSigmoidSlope;
+  switch (kind) {
+    case kEpMax: return tc_fourier_gemm_kernel<kTF32, kEpMax, 1, kTeams>;
+    case kEpMaxSlope: return tc_fourier_gemm_kernel<kTF32, kMax, 1, kTeams>;
+    case kEpSigmoid: return tc_fourier_gemm_kernel<kTF32, kEpSigmoid, 1, kTeams>;
+    default: return tc_fourier_gemm_kernel<kTF32, kSig, 1, kTeams>;
+  }
+}
+
 // tf32: fp32 data in the split-TF32 mode (FEQL_FP32_3XTF32), else fp16.
 // ep: activation, residual and saved slope, or nullptr; twice: fp16 data without ep,
 // twice the result (as g8 and simt passes below).
@@ -160,7 +173,9 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
   p.bias_floats = P.nD * P.BD;
   p.out = out;
   p.ep = ep != nullptr ? *ep : Epilogue{};
-  p.res_ring = !tf32 && p.ep.res != nullptr ? 1 : 0;
+  const int kind = ep != nullptr ? epilogue_kind(*ep) : kEpNone;
+  const int teams = tc_two_teams(kind, P.nK, P.BD / 8) ? 2 : 3;
+  p.res_slots = !tf32 && p.ep.res != nullptr ? 4 * teams * kResDepth : 0;
   const int slot = tf32 ? 2 * kXChunkBytes : kXChunkBytes;  // input chunk / its planes
   const int budget = dev.smem_optin - 1024;  // 1 KB for aligning the base
   // Resident weights when the CTA's slice fits beside >= 4 input stages and
@@ -192,7 +207,7 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
   // 14.9; 8192 x 48 -> 64 (64, 2): 10.5 and 11.6.  fp32 and the other kinds gain too.
   p.share = 1;
   if (ep != nullptr && p.n_units <= dev.sms / 2) {
-    const int most = static_cast<int>(cdiv(P.BD / 8, kEpTeams));  // a block for every team
+    const int most = static_cast<int>(cdiv(P.BD / 8, teams));  // a block for every team
     p.share = dev.sms / p.n_units < most ? dev.sms / p.n_units : most;
     if (p.share < 1) p.share = 1;
     grid *= p.share;
@@ -203,31 +218,16 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
             : make_tmap_f16(&tm_in, in, N, static_cast<int64_t>(P.Ci) * kT);
   if (st != FEQL_OK) return st;
   CUtensorMap tm_res = tm_in;
-  if (p.res_ring) {  // kResBox: 32 rows x 8 channels
+  if (p.res_slots != 0) {  // kResBox: 32 rows x 8 channels
     st = make_tmap_f16(&tm_res, p.ep.res, N, static_cast<int64_t>(P.Do) * kT, 32, 8 * kT);
     if (st != FEQL_OK) return st;
   }
   auto kernel = tf32    ? tc_fourier_gemm_kernel<true>
                 : twice ? tc_fourier_gemm_kernel<false, kEpNone, 2>
                         : tc_fourier_gemm_kernel<false>;
-  if (ep != nullptr) {
-    switch (epilogue_kind(*ep)) {
-      case kEpMax:
-        kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpMax> : tc_fourier_gemm_kernel<false, kEpMax>;
-        break;
-      case kEpMaxSlope:
-        kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpMax>
-                      : tc_fourier_gemm_kernel<false, kEpMaxSlope>;
-        break;
-      case kEpSigmoid:
-        kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpSigmoid>
-                      : tc_fourier_gemm_kernel<false, kEpSigmoid>;
-        break;
-      default:
-        kernel = tf32 ? tc_fourier_gemm_kernel<true, kEpSigmoid>
-                      : tc_fourier_gemm_kernel<false, kEpSigmoidSlope>;
-    }
-  }
+  if (ep != nullptr)
+    kernel = tf32 ? (teams == 2 ? tc_ep_kernel<true, 2>(kind) : tc_ep_kernel<true, 3>(kind))
+                  : (teams == 2 ? tc_ep_kernel<false, 2>(kind) : tc_ep_kernel<false, 3>(kind));
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return FEQL_ERR_CUDA;
   kernel<<<grid, kTcThreads, smem, stream>>>(tm_in, tm_res, p);

@@ -63,8 +63,9 @@ constexpr bool kSkipFirstRelease = false;
 constexpr int kTcWarps = 20;
 constexpr int kTcThreads = kTcWarps * 32;
 constexpr int kTcEpi0 = 12;                       // first epilogue warp
-constexpr int kEpTeams = 3;                       // epilogue teams of the kEp kernels
-constexpr int kEpFirst = 8;                       // their first warp (warps 8 .. 19)
+// First epilogue warp of the kEp kernels: three epilogue teams (warps 8 .. 19) beside one
+// transform team, or two of each.
+constexpr int ep_first(int teams) { return teams == 3 ? 8 : kTcEpi0; }
 
 // Transform ordinal (0..4*kTeams-1) of warp w, or -1 when w is not a transform warp.
 __device__ __forceinline__ int tc_xf_ordinal(int w) {
@@ -72,8 +73,8 @@ __device__ __forceinline__ int tc_xf_ordinal(int w) {
   return w - 2 - (w > 5) - (w > 9);
 }
 
-// The same for the kEp kernels' one transform team: warps 2, 3, 4 and 6.
-__device__ __forceinline__ int tc_ep_xf_ordinal(int w) {
+// The same for one transform team: warps 2, 3, 4 and 6.
+__device__ __forceinline__ int tc_xf_ordinal_one(int w) {
   return w < 2 || w > 6 || w == 5 ? -1 : w - 2 - (w > 5);
 }
 constexpr int kXChunkBytes = kBM * kCK * kT * 2;  // 16 KB: 128 rows x 128 B
@@ -97,10 +98,21 @@ struct TcFwdParams {
   int stage_bytes;      // input chunk slot (16 KB; 32 KB of planes in split-TF32 mode)
                         // + weight chunk unless resident, 1 KB aligned
   int bias_floats;      // nD * BD
-  int res_ring;         // 1: the epilogue warps' residual rings are there
+  int res_slots;        // residual boxes of all epilogue warps' rings
   void *out;            // [N][Do][4], fp16 (fp32 in split-TF32 mode)
   Epilogue ep;          // activation, residual, saved slope (kernels with kEp)
 };
+
+// Two epilogue teams beside two transform teams, where a tile's input chunks are at least
+// as many as its output blocks (one and a half times, for the costlier sigmoid kinds);
+// else three beside one.  us, two and two against one and three: 65536 x 192 -> 192 with a
+// residual 82 and 89, with GELU 87 and 82; 401408 x 96 -> 24 ReLU 72 and 90, GELU and
+// slopes 92 and 103; 401408 x 24 -> 96 residual 133 and 118, GELU and slopes 204 and 172;
+// 100000 x 64 -> 64 GELU 42 and 39; split TF32 20000 x 96 -> 96 ReLU 48 and 53, GELU 79
+// and 72.
+inline bool tc_two_teams(int kind, int chunks, int blocks) {
+  return ep_is_max(kind) ? chunks >= blocks : 2 * chunks >= 3 * blocks;
+}
 
 struct TcSmem {
   // offsets (bytes) from the 1024-aligned dynamic smem base
@@ -112,11 +124,11 @@ __host__ __device__ inline TcSmem tc_fwd_smem(const TcFwdParams &p) {
   s.wres = 0;
   s.stage0 = p.resident ? p.wres_bytes : 0;
   s.res = s.stage0 + p.stages * p.stage_bytes;
-  s.bias = s.res + (p.res_ring ? 4 * kEpTeams * kResDepth * kResBox : 0);
+  s.bias = s.res + p.res_slots * kResBox;
   s.bars = s.bias + static_cast<int>(align_up(p.bias_floats * 4, 16));
   // full, tready, empty per stage; acc_full, acc_empty per acc buffer; final; wfull; tmem
   // slot; residual boxes
-  s.total = s.bars + (3 * p.stages + 2 * 2 + 2) * 8 + 16 + 4 * kEpTeams * kResDepth * 8;
+  s.total = s.bars + (3 * p.stages + 2 * 2 + 2) * 8 + 16 + p.res_slots * 8;
   return s;
 }
 
@@ -170,19 +182,21 @@ struct TcUnits {
 // fp32 rows.  Bins are not scaled (fp32 has the range).
 //
 // kEp != kEpNone: y = res + act(z) in the epilogue (act.cuh), the slope act'(z)
-// stored beside y when the backward pass will want it.  The epilogue then has the
+// stored beside y when the backward pass will want it.  The epilogue then often has the
 // most work (some 13 instructions per value with an activation and its slope, on
-// two or three warps per SM sub-partition), so the warps are dealt out anew: one
+// two or three warps per SM sub-partition): then the warps are dealt out anew, one
 // transform team and three epilogue teams, which share every tile's 8-channel
-// blocks (401408 x 24 -> 96 with GELU and slopes: 199 us with two and two, 172 us
-// so; two and three need 24 warps of 80 registers, which spill: 210 us).  An fp16
+// blocks.  Layers with many input channels to an output keep two and two teams
+// (tc_two_teams; both need 20 warps; two and three are 24 warps of 80 registers, which
+// spill: 210 us on 401408 x 24 -> 96 with GELU and slopes).  An fp16
 // residual comes by TMA: each epilogue warp loads the 32-row x 8-channel boxes
 // (2 KB) of its own blocks, in the order in which it will use them, into a private
 // ring of kResDepth slots, so the loads run kResDepth blocks ahead (direct loads in
-// the block that uses them cost an HBM latency each: 123 us instead of 78 with two
-// teams on 65536 x 192 -> 192; 85 us with three, 3.6 TB/s).
-// kOut: a power of two that the fp16 results are multiplied by (kEpNone).
-template <bool kTF32, int kEp = kEpNone, int kOut = 1>
+// the block that uses them cost an HBM latency each, half as long again on
+// 65536 x 192 -> 192; six boxes a warp leave fewer input stages: 88 us there, not 82).
+// kOut: a power of two that the fp16 results are multiplied by (kEpNone).  kEpTeams: the
+// epilogue teams of a kEp kernel, 3 or 2.
+template <bool kTF32, int kEp = kEpNone, int kOut = 1, int kEpTeams = 3>
 __global__ void __maxnreg__(96)
 tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
                        const __grid_constant__ CUtensorMap tm_res, const TcFwdParams p) {
@@ -203,10 +217,11 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
   uint64_t *res_full = wfull + 3;  // [epilogue warp][slot]
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr bool kOneXf = kEp != kEpNone && kEpTeams == 3;
 
   if (threadIdx.x == 0) {
     if (kEp != kEpNone)
-      for (int i = 0; i < 4 * kEpTeams * kResDepth; ++i) mbar_init(&res_full[i], 1);
+      for (int i = 0; i < p.res_slots; ++i) mbar_init(&res_full[i], 1);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&tready[s], 4);
@@ -337,11 +352,11 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
       mma_commit(final_bar);
       mbar_wait(final_bar, 0);
     }
-  } else if ((kEp != kEpNone ? tc_ep_xf_ordinal(warp) : tc_xf_ordinal(warp)) >= 0) {
+  } else if ((kOneXf ? tc_xf_ordinal_one(warp) : tc_xf_ordinal(warp)) >= 0) {
     // ---------------------------------------------------------- transform
     // kTeams teams of 4 warps take alternate chunks of the ring.
-    constexpr int kXfTeams = kEp != kEpNone ? 1 : kTeams;
-    const int xo = kEp != kEpNone ? tc_ep_xf_ordinal(warp) : tc_xf_ordinal(warp);
+    constexpr int kXfTeams = kOneXf ? 1 : kTeams;
+    const int xo = kOneXf ? tc_xf_ordinal_one(warp) : tc_xf_ordinal(warp);
     const int team = xo / 4;
     const int r = (xo % 4) * 32 + lane;  // row of the chunk (token within the tile)
     int s = 0, c = 0;
@@ -407,11 +422,11 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
         if (++s == p.stages) { s = 0; ph ^= 1; }
       }
     }
-  } else if (kEp != kEpNone && warp >= kEpFirst) {
+  } else if (kEp != kEpNone && warp >= ep_first(kEpTeams)) {
     // ------------------------------ epilogue with activation and residual
     // As below, but all teams share every tile: team t takes the 8-channel
     // blocks t, t + bstep, ... (teams counted through the CTAs of the unit)
-    const int ew = warp - kEpFirst, bstep = kEpTeams * p.share;
+    const int ew = warp - ep_first(kEpTeams), bstep = kEpTeams * p.share;
     const int eteam = ew / 4 + kEpTeams * (static_cast<int>(blockIdx.x) % p.share);
     const int quad = warp & 3;
     const int blocks = p.BD / 8;
@@ -419,7 +434,7 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
     const int tcp = 2 * (lane & 3);
     const int64_t row_elems = static_cast<int64_t>(p.Do) * kT;
     // the residual ring: the block that the next load is for, slots issued and used
-    const bool ring = !kTF32 && p.res_ring && last >= 0;
+    const bool ring = !kTF32 && p.res_slots != 0 && last >= 0;
     uint8_t *rbox = smem + L.res + ew * kResDepth * kResBox;
     uint64_t *rbar = res_full + ew * kResDepth;
     TcUnits ahead(p);
