@@ -284,12 +284,12 @@ def _forward_act(calls, p4m, x, What, b, D, mode, act, res, save_z):
         b = _take(b, "b", (D,), x.dtype, at)
         res = _take(res, "res", (N, D, T), x.dtype, at)
         y = x.new_empty((N, D, T))
-        z = torch.empty_like(y) if save_z and act != FEQL_ACT_NONE else None
-        forward(T, x, What, b, res, y, z, N, C, D, act, mode)
-    return y, z
+        slope = torch.empty_like(y) if save_z and act != FEQL_ACT_NONE else None
+        forward(T, x, What, b, res, y, slope, N, C, D, act, mode)
+    return y, slope
 
 
-def _backward_act(calls, p4m, x, dy, z, What, mode, act, with_dx, with_dw, with_db):
+def _backward_act(calls, p4m, x, dy, slope, What, mode, act, with_dx, with_dw, with_db):
     N, C, T = _layer_input(x, mode, p4m)
     if dy.dim() != 3:
         raise ValueError(f"dy has shape {tuple(dy.shape)}, expected (N, D, T)")
@@ -302,7 +302,7 @@ def _backward_act(calls, p4m, x, dy, z, What, mode, act, with_dx, with_dw, with_
         at = x.get_device()
         x = _dense(x)
         dy = _take(dy, "dy", (N, D, T), x.dtype, at)
-        z = _take(z, "z", (N, D, T), x.dtype, at)
+        slope = _take(slope, "slope", (N, D, T), x.dtype, at)
         What = _take(What, "What", (nbytes,), torch.uint8, at)
         ws_bytes = _bytes(workspace, at, T, N, C, D, act, mode)
         ws = x.new_empty(ws_bytes, dtype=torch.uint8)
@@ -313,24 +313,28 @@ def _backward_act(calls, p4m, x, dy, z, What, mode, act, with_dx, with_dw, with_
         if with_db:
             db = x.new_empty(D)
         if with_dx or dW is not None:
-            backward(T, x, dy, z, What, dx, dW, db, ws, ws_bytes, N, C, D, act, mode)
+            backward(T, x, dy, slope, What, dx, dW, db, ws, ws_bytes, N, C, D, act, mode)
     return dx, (dW if with_dw else None), db
 
 
 def ct_forward_act(x: torch.Tensor, What: torch.Tensor, b, D: int, mode: int, act: int, res=None,
                    save_z: bool = False):
-    """y = res + act(z), z = the C_T layer of x plus b: (y, saved z).
+    """y = res + act(z), z = the C_T layer of x plus b: (y, slope).
 
-    The ``z`` returned is what ct_backward_act takes of it, the activation's slope
-    there; None without ``save_z`` or activation.
+    ``slope`` is act'(z), all that ct_backward_act takes of z; None without an
+    activation, or unless ``save_z`` asks for what the backward pass needs of z.
     """
     return _forward_act(_CYCLIC_CALLS, False, x, What, b, D, mode, act, res, save_z)
 
 
-def ct_backward_act(x: torch.Tensor, dy: torch.Tensor, z, What: torch.Tensor, mode: int, act: int,
-                    with_dx: bool = True, with_dw: bool = True, with_db: bool = True):
-    """dx, dW, db of ct_forward_act (the residual's gradient is dy), None where not asked."""
-    return _backward_act(_CYCLIC_CALLS, False, x, dy, z, What, mode, act, with_dx, with_dw, with_db)
+def ct_backward_act(x: torch.Tensor, dy: torch.Tensor, slope, What: torch.Tensor, mode: int,
+                    act: int, with_dx: bool = True, with_dw: bool = True, with_db: bool = True):
+    """dx, dW, db of ct_forward_act (the residual's gradient is dy), None where not asked.
+
+    ``slope``: as ct_forward_act returned it (not z).
+    """
+    return _backward_act(_CYCLIC_CALLS, False, x, dy, slope, What, mode, act, with_dx, with_dw,
+                         with_db)
 
 
 def p4m_forward_act(x: torch.Tensor, What: torch.Tensor, b, D: int, mode: int, act: int, res=None,
@@ -339,10 +343,11 @@ def p4m_forward_act(x: torch.Tensor, What: torch.Tensor, b, D: int, mode: int, a
     return _forward_act(_P4M_CALLS, True, x, What, b, D, mode, act, res, save_z)
 
 
-def p4m_backward_act(x: torch.Tensor, dy: torch.Tensor, z, What: torch.Tensor, mode: int, act: int,
-                     with_dx: bool = True, with_dw: bool = True, with_db: bool = True):
+def p4m_backward_act(x: torch.Tensor, dy: torch.Tensor, slope, What: torch.Tensor, mode: int,
+                     act: int, with_dx: bool = True, with_dw: bool = True, with_db: bool = True):
     """ct_backward_act of the p4m layer."""
-    return _backward_act(_P4M_CALLS, True, x, dy, z, What, mode, act, with_dx, with_dw, with_db)
+    return _backward_act(_P4M_CALLS, True, x, dy, slope, What, mode, act, with_dx, with_dw,
+                         with_db)
 
 
 def norm_forward(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5,

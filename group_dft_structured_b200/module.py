@@ -106,22 +106,22 @@ class EqLinearActFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, b, res, What, mode: int, group: str, act: int):
         run = _L.p4m_forward_act if group == "p4m" else _L.ct_forward_act
-        y, z = run(x, What, b, W.shape[0], mode, act, res=res,
-                   save_z=any(ctx.needs_input_grad[:3]))
-        ctx.save_for_backward(x, What, z)
+        y, slope = run(x, What, b, W.shape[0], mode, act, res=res,
+                       save_z=any(ctx.needs_input_grad[:3]))
+        ctx.save_for_backward(x, What, slope)
         ctx.mode, ctx.group, ctx.act = mode, group, act
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        x, What, z = ctx.saved_tensors
+        x, What, slope = ctx.saved_tensors
         need_x, need_W, need_b, need_res = ctx.needs_input_grad[:4]
         dx = dW = db = None
         if need_x or need_W or need_b:
             run = _L.p4m_backward_act if ctx.group == "p4m" else _L.ct_backward_act
-            dx, dW, db = run(x, dy, z, What, ctx.mode, ctx.act, with_dx=need_x, with_dw=need_W,
-                             with_db=need_b)
+            dx, dW, db = run(x, dy, slope, What, ctx.mode, ctx.act, with_dx=need_x,
+                             with_dw=need_W, with_db=need_b)
         return dx, dW, db, (dy if need_res else None), None, None, None, None
 
 
