@@ -367,6 +367,11 @@ tc_fourier_gemm_kernel(const __grid_constant__ CUtensorMap tm_in,
           if (++s == p.stages) { s = 0; ph ^= 1; }
           continue;
         }
+        // An odd ring gives a slot to the teams in turn, so this one has not waited for the
+        // slot's load before.  Loads may land out of order: with that one still on its way,
+        // full's parity would tell the phase before it from this one's no more.  Its MMAs'
+        // release comes after it, and this chunk's not before this team is done.
+        if (kXfTeams == 2 && (p.stages & 1) && ok) ok = mbar_wait(&empty[s], ph ^ 1);
         if (ok) ok = mbar_wait(&full[s], ph);
         uint8_t *st = smem + L.stage0 + s * p.stage_bytes;
         // row r: 8 x 16 B; fp16: logical chunk q = channels 2q, 2q+1 (x 4 group
