@@ -130,6 +130,15 @@ bool is_tc(int dt) { return dt == FEQL_FP16; }
 bool is_tf32(int dt) { return dt == FEQL_FP32_3XTF32; }
 // Layout kind of the Fourier-weight buffer of a (resolved) mode.
 int what_kind(int dt) { return is_tc(dt) ? kWhatF16 : (is_tf32(dt) ? kWhatTF32 : kWhatSimt); }
+// Lets a kernel have all the shared memory of a block (the tensor-core kernels have no
+// static part).  The limit is the function's, not the launch's: the same value from every
+// thread, so that none lowers it between another's call and launch.
+template <class Kernel>
+bool allow_smem(Kernel kernel, const DeviceInfo &dev) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              dev.smem_optin) == cudaSuccess;
+}
+
 // ---------------------------------------------------------------- tc launch
 // The kernel of an epilogue (split TF32 takes a slope or none in either kind).
 using TcKernel = void (*)(const CUtensorMap, const CUtensorMap, const TcFwdParams);
@@ -228,8 +237,7 @@ int launch_tc_gemm(const void *in, const uint8_t *wt, const TcPlan &P, const voi
   if (ep != nullptr)
     kernel = tf32 ? (teams == 2 ? tc_ep_kernel<true, 2>(kind) : tc_ep_kernel<true, 3>(kind))
                   : (teams == 2 ? tc_ep_kernel<false, 2>(kind) : tc_ep_kernel<false, 3>(kind));
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return FEQL_ERR_CUDA;
+  if (!allow_smem(kernel, dev)) return FEQL_ERR_CUDA;
   kernel<<<grid, kTcThreads, smem, stream>>>(tm_in, tm_res, p);
   return launch_status();
 }
@@ -344,9 +352,7 @@ int launch_tc_dw(TcDwParams p, const void *x, const void *dy, __half *dW, __half
                                              p.nqc_max) == FEQL_OK;
     if (!p.stack_x) st = make_tmap_f16(&tm_x, x, p.N, static_cast<int64_t>(p.C) * kT, p.TB);
     if (st != FEQL_OK) return st;
-    if (cudaFuncSetAttribute(tc_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-        cudaSuccess)
-      return FEQL_ERR_CUDA;
+    if (!allow_smem(tc_dw_kernel, dev)) return FEQL_ERR_CUDA;
     const int grid = p.tiles_d * p.tiles_c * p.splits;
     tc_dw_kernel<<<grid, kDwThreads, smem, stream>>>(tm_dy, tm_x, p);
   }
@@ -428,9 +434,7 @@ int launch_tc_bwd(TcBwdParams p, const void *x, const void *dy, const uint8_t *w
     if (st != FEQL_OK) return st;
     kernel = dbcol ? tc_bwd_kernel<true, true> : tc_bwd_kernel<false, true>;
   }
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return FEQL_ERR_CUDA;
+  if (!allow_smem(kernel, dev)) return FEQL_ERR_CUDA;
   kernel<<<p.splits, kBwThreads, smem, stream>>>(tm_dy, tm_x, tm_s, p);
   if (cudaGetLastError() != cudaSuccess) return FEQL_ERR_CUDA;
   // the split reduce as the kernel's programmatic dependent (see tc_dw.cuh)
@@ -507,9 +511,7 @@ int launch_g8_fwd(const void *in, const uint8_t *wt, const G8Plan &P, const __ha
                 : epilogue_kind(*ep) == kEpMaxSlope ? tc_g8_fwd_kernel<Gp, kEpMaxSlope>
                 : epilogue_kind(*ep) == kEpSigmoid  ? tc_g8_fwd_kernel<Gp, kEpSigmoid>
                                                     : tc_g8_fwd_kernel<Gp, kEpSigmoidSlope>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return FEQL_ERR_CUDA;
+  if (!allow_smem(kernel, dev)) return FEQL_ERR_CUDA;
   const int grid = p.n_units < dev.sms ? p.n_units : dev.sms;
   kernel<<<grid, kG8Threads, smem, stream>>>(tm, tm_out, tm_res, tm_slope, p);
   return launch_status();
@@ -577,9 +579,7 @@ int launch_g8_dw(const void *x, const void *dy, __half *dW, __half *db, float *w
     if (!p.stack_x) st = make_tmap_f16(&tm_x, x, N, static_cast<int64_t>(C) * T, kG8DwTB, 8 * T);
     if (st != FEQL_OK) return st;
     const int smem = g8_dw_smem(p).total + 1024;
-    if (cudaFuncSetAttribute(tc_g8_dw_kernel<Gp>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-        cudaSuccess)
-      return FEQL_ERR_CUDA;
+    if (!allow_smem(tc_g8_dw_kernel<Gp>, dev)) return FEQL_ERR_CUDA;
     const int64_t grid = static_cast<int64_t>(p.splits) * p.tiles_d * p.tiles_c;
     if (grid > INT32_MAX) return FEQL_ERR_UNSUPPORTED;
     tc_g8_dw_kernel<Gp><<<static_cast<unsigned>(grid), kG8DwThreads, smem, stream>>>(tm_dy, tm_x, p);
@@ -651,8 +651,7 @@ int launch_mlp(const void *x, const uint8_t *wt, const __half *b1, const __half 
   st = make_tmap_f16(&tm_out, y, N, static_cast<int64_t>(p.P.Co) * kT, 32);
   if (st != FEQL_OK) return st;
   auto kernel = p.wslots > 0 ? tc_mlp_kernel<true> : tc_mlp_kernel<false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return FEQL_ERR_CUDA;
+  if (!allow_smem(kernel, dev)) return FEQL_ERR_CUDA;
   const int grid = p.nM < dev.sms ? p.nM : dev.sms;
   kernel<<<grid, kMlpThreads, smem, stream>>>(tm_in, tm_out, p);
   return launch_status();
