@@ -159,7 +159,7 @@ class EqLinear(torch.nn.Module):
             torch.empty((out_channels, in_channels, group_order), dtype=dtype, device=device))
         self.bias = (torch.nn.Parameter(torch.empty((out_channels,), dtype=dtype, device=device))
                      if bias else None)
-        self._whats = {}  # stream: (what the weight was, its Fourier weight buffer)
+        self._whats = {}  # stream: (what the weight was, its Fourier weight buffer, its memory)
         self.reset_parameters()
 
     def reset_parameters(self) -> None:
@@ -178,12 +178,13 @@ class EqLinear(torch.nn.Module):
         if W.is_inference() or torch.cuda.is_current_stream_capturing():
             return self._transformed()
         key = (W.device, W.dtype, W.data_ptr(), W._version, tuple(W.shape))
-        # a buffer to each stream: made, used and given back in its order alone
+        # a buffer to each stream: made, used and given back in its order alone; with the
+        # weight's memory, which no other weight can have as long as the buffer is kept
         stream = torch.cuda.current_stream(W.device).cuda_stream
         kept = self._whats.get(stream)
         if kept is None or kept[0] != key:
             self._whats = {s: k for s, k in self._whats.items() if k[0] == key}
-            kept = self._whats[stream] = (key, self._transformed())
+            kept = self._whats[stream] = (key, self._transformed(), W.detach())
         return kept[1]
 
     def _transformed(self) -> torch.Tensor:

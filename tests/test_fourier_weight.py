@@ -87,6 +87,18 @@ def test_streams_do_not_share_a_buffer(fake):
     assert fake.calls == 4 and len(m._whats) == 2
 
 
+def test_another_weight_at_the_same_address(fake):
+    m = EqLinear(40, 50)
+    for k in range(1, 30):
+        del m.weight
+        m.weight = torch.nn.Parameter(torch.full((50, 40, 4), float(k), dtype=torch.float16))
+        assert torch.equal(m.fourier_weight(), 2 * m.weight), k
+    for k in range(1, 30):  # a weight of the moment, as torch.func.functional_call sets it
+        m._parameters["weight"] = None
+        m._parameters["weight"] = torch.full((50, 40, 4), float(k), dtype=torch.float16)
+        assert torch.equal(m.fourier_weight(), 2 * m.weight), k
+
+
 # ------------------------------------------------------------------ GPU ---
 
 @pytest.fixture
@@ -169,3 +181,16 @@ def test_two_streams_at_once(gpu, kind):
             m.weight.neg_()
             m2.weight.neg_()
             want = m2(x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_weights_of_the_moment(gpu, kind):
+    m, x = layer(kind)
+    for k in range(6):  # each freed before the next is made: the same address
+        W = torch.randn_like(m.weight) * 0.1
+        y = torch.func.functional_call(m, {"weight": W}, (x,))
+        with torch.no_grad():
+            m.weight.copy_(W)
+            del W
+            assert torch.equal(y, m(x)), k
