@@ -135,7 +135,8 @@ class EqLinear(torch.nn.Module):
     Fourier weight buffer is rebuilt when the weight changes (tracked by its
     storage and version counter), so it is computed once per optimizer step, or
     once for inference, on each stream that calls; a captured graph computes it at
-    every replay.  ``activation`` ("relu", "gelu": the tanh form, "silu") is
+    every replay.  (Write to the weight itself, under ``torch.no_grad()``: a write
+    through ``weight.data`` leaves no version and is not seen, here or by autograd.)  ``activation`` ("relu", "gelu": the tanh form, "silu") is
     applied to the output and ``forward``'s ``residual`` added after it, both in
     the epilogue of the layer's products.
     """
@@ -186,6 +187,12 @@ class EqLinear(torch.nn.Module):
             self._whats = {s: k for s, k in self._whats.items() if k[0] == key}
             kept = self._whats[stream] = (key, self._transformed(), W.detach())
         return kept[1]
+
+    def __getstate__(self):  # copies and files hold the weight alone
+        return {**self.__dict__, "_whats": {}}
+
+    def __setstate__(self, state):
+        super().__setstate__({**state, "_whats": {}})
 
     def _transformed(self) -> torch.Tensor:
         wfft = _L.p4m_weight_fft if self.group == "p4m" else _L.ct_weight_fft

@@ -87,6 +87,25 @@ def test_streams_do_not_share_a_buffer(fake):
     assert fake.calls == 4 and len(m._whats) == 2
 
 
+def test_copies_and_files_hold_the_weight_alone(fake):
+    import copy
+    import io
+    m = EqLinear(3, 5)
+    m.fourier_weight()
+    size = lambda m: (lambda f: (torch.save(m, f), f.tell())[1])(io.BytesIO())
+    fresh = EqLinear(3, 5)
+    assert abs(size(m) - size(fresh)) < 64  # no buffer in it
+    f = io.BytesIO()
+    torch.save(m, f)
+    f.seek(0)
+    for other in (copy.deepcopy(m), torch.load(f, weights_only=False)):
+        assert other._whats == {} and torch.equal(other.weight, m.weight)
+        with torch.no_grad():
+            other.weight.mul_(3)
+        assert torch.equal(other.fourier_weight(), 2 * other.weight)
+    assert len(m._whats) == 1
+
+
 def test_another_weight_at_the_same_address(fake):
     m = EqLinear(40, 50)
     for k in range(1, 30):
