@@ -68,6 +68,7 @@ class EqLinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, b, What, mode: int, group: str = "cyclic"):
         D = W.shape[0]
+        b = None if b is None else _L._dense(b)
         y = (_L.p4m_forward(x, What, b, D, mode) if group == "p4m"
              else _L.ct_forward(x, What, b, D, mode))
         ctx.save_for_backward(x, What)
@@ -81,7 +82,7 @@ class EqLinearFunction(torch.autograd.Function):
         x, What = ctx.saved_tensors
         C, D, T = ctx.shape
         need_x, need_W, need_b = ctx.needs_input_grad[:3]
-        dy = dy.contiguous()
+        dy = _L._dense(dy)
         dx = dW = db = None
         if ctx.group == "p4m":
             if need_x:
@@ -198,7 +199,7 @@ class EqLinear(torch.nn.Module):
         wfft = _L.p4m_weight_fft if self.group == "p4m" else _L.ct_weight_fft
         # an ordinary tensor, which later calls may save for their backward pass
         with torch.inference_mode(False), torch.no_grad():
-            return wfft(self.weight.detach().contiguous(), mode_for(self.weight.dtype))
+            return wfft(_L._dense(self.weight.detach()), mode_for(self.weight.dtype))
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         C, D, T = self.in_channels, self.out_channels, self.group_order
@@ -208,6 +209,8 @@ class EqLinear(torch.nn.Module):
             raise RuntimeError("EqLinear runs on CUDA tensors only (libfeql.so kernels)")
         lead = x.shape[:-1]
         x3 = x.reshape(-1, C, T).contiguous()
+        if x3.data_ptr() % 16 != 0:  # a part of a larger tensor
+            x3 = x3.clone()  # (not _dense: in autograd's sight)
         if x3.dtype != self.weight.dtype:
             raise TypeError(f"input dtype {x3.dtype} differs from the weight's {self.weight.dtype}")
         if self.weight.device != x.device:
