@@ -78,6 +78,7 @@ class EqLinearFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, What = ctx.saved_tensors
         C, D, T = ctx.shape
