@@ -200,7 +200,7 @@ constexpr int scan_rows_bwd(bool half, int V) { return half ? (V == 4 ? 4 : 8) :
 // a sequence by itself when there are enough (sequence, tile) units to fill
 // the GPU with warps or the sequences are short; else eight warps share a
 // tile of rows.  (Six warps and 96 registers, for three blocks per SM, were
-// measured: no faster, 105 against 104 us on 128 x 3136 x 24 x 4 backward.)  Then
+// measured: no faster.)  Then
 // sequences are cut into segments where whole ones would leave SMs idle: dense
 // sequences when not every SM gets a unit, packed ones (whose longest the host
 // does not know) always, in segments of an even share for two blocks (16 of one
@@ -244,9 +244,10 @@ ScanPlan scan_plan(int B, int64_t N, int C, int T, bool shared, bool packed, boo
   q.s.whole = 0;
   q.s.per = 1;
   // Dense sequences that fill the GPU once or twice and then less than half of it:
-  // those of the last round are cut (128 x 3136 x 24 x 4 backward, 384 units of which
-  // 296 run at a time: 91 us, 99 with whole ones; all of them cut 105, since the maps
-  // read all of dh and g).
+  // those of the last round are cut.  128 x 3136 x 24 x 4 backward, 384 units of which
+  // 296 run at a time: 85 us, 92 with whole ones; 50 x 3000 x 96 x 4 fp32 forward 136 and
+  // 215.  Where the rest is near half a round it can cost a little: 128 x 3136 x 24 x 4
+  // forward with a gate per value 71 and 66.
   const int64_t cap = static_cast<int64_t>(sms) * scan_blocks(8, !bwd && sh && q.V > 1);
   if (!packed && q.NW == 8 && units > cap && units < 3 * cap) {
     const int64_t whole = units / cap * cap / q.s.ntiles, rest = (B - whole) * q.s.ntiles;

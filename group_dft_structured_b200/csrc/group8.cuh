@@ -704,7 +704,8 @@ struct G8Units {
 // kEp != kEpNone: y = res + act(z) (act.cuh).  Residual and slopes move as y does: the
 // residual by TMA into a box of each epilogue warp, its next one loaded as soon as
 // one has been read, the slopes through boxes beside y's (direct accesses, a row of
-// 128 bytes to a lane, took 65 us instead of 45 on 50000 x 12 -> 48, p4m).
+// 128 bytes to a lane, took nearly half as long again on 50000 x 12 -> 48, p4m: 51 us so
+// with SiLU and residual).
 // kOut: a power of two that the results are multiplied by (kEpNone).
 template <class Gp, int kEp = kEpNone, int kOut = 1>
 __global__ void __maxnreg__(96)

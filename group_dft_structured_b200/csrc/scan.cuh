@@ -36,10 +36,11 @@
 // dg's own, where the bound is one.)
 //
 // Measured, fp16: 128 x 3136 x 24 x 4 with channel gates, forward 44 us (173 MB,
-// 3.9 TB/s) and backward 91 us (405 MB, 4.4 TB/s); one sequence of 65536 x 96 x 4,
-// 29 us for the maps and 34 for the scan (151 MB, 252 with the second reading).
-// DRAM is 40 % busy and the instructions issue on 50 to 65 % of the cycles: the
-// converts, the joins and the walk over the rows bound it, not the loads.
+// 3.9 TB/s), of a training step 63 (327 MB, 5.2 TB/s), and backward 74 us (346 MB, 4.7
+// TB/s) with 9 for its maps; one sequence of 65536 x 96 x 4, 25 us for the maps and 35
+// for the scan (151 MB, 252 with the second reading).  DRAM is 40 to 54 % busy and the
+// instructions issue on 50 to 60 % of the cycles: the converts, the joins and the walk
+// over the rows bound it as much as the loads.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -119,7 +119,7 @@ __host__ __device__ inline BwSmem tc_bwd_smem(const TcBwdParams &p) {
 // reads it first, so it is free again while the stage's MMAs run), and the
 // transform multiplies its dy fibres before their rDFT: dz / 4 is rounded to fp16 (the
 // planes' own scale), and never goes to memory.  401408 x 24 -> 96: 226 us
-// for the two kernels, 144 us for this one.
+// for the two kernels, 135 us for this one.
 template <bool kDbCol, bool kAct = false>
 __global__ void __maxnreg__(80)
 tc_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x,
