@@ -948,7 +948,7 @@ static int ct_pass(int T, const void *in, const void *What, const void *bias, vo
   int path = 0;
   const int st = ct_route(T, C, D, dtype, &path);
   if (st != FEQL_OK) return st;
-  if (path == kCtTensor8) 
+  if (path == kCtTensor8)
     return g8_pass<Cyclic8>(in, What, bias, out, N, C, D, stream, dir, ep, twice);
   if (path == kCtTensor6)
     return g8_pass<Cyclic6>(in, What, bias, out, N, C, D, stream, dir, ep, twice);

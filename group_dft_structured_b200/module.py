@@ -186,8 +186,10 @@ class EqLinear(torch.nn.Module):
         stream = torch.cuda.current_stream(W.device).cuda_stream
         kept = self._whats.get(stream)
         if kept is None or kept[0] != key:
-            self._whats = {s: k for s, k in self._whats.items() if k[0] == key}
-            kept = self._whats[stream] = (key, self._transformed(), W.detach())
+            kept = (key, self._transformed(), W.detach())
+            # (a new dict: other threads may be looking at this one)
+            self._whats = {s: k for s, k in list(self._whats.items()) if k[0] == key}
+            self._whats[stream] = kept
         return kept[1]
 
     def __getstate__(self):  # copies and files hold the weight alone

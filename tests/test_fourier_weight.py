@@ -118,6 +118,37 @@ def test_another_weight_at_the_same_address(fake):
         assert torch.equal(m.fourier_weight(), 2 * m.weight), k
 
 
+def test_threads_on_their_own_streams(fake, monkeypatch):
+    """Many threads, each on a stream of its own, while the weight keeps changing."""
+    import sys
+    import threading
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: type(
+        "S", (), {"cuda_stream": threading.get_ident()}))
+    m, failed = EqLinear(3, 5), []
+
+    def loop():
+        try:
+            for _ in range(300):
+                with torch.no_grad():
+                    m.weight.add_(1)
+                m.fourier_weight()
+        except BaseException as e:
+            failed.append(repr(e))
+
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=loop) for _ in range(8)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    assert not failed, failed
+    assert torch.equal(m.fourier_weight(), 2 * m.weight)
+
+
 # ------------------------------------------------------------------ GPU ---
 
 @pytest.fixture
