@@ -103,13 +103,16 @@ class EqLinearFunction(torch.autograd.Function):
 class EqLinearActFunction(torch.autograd.Function):
     """y = res + act(z), z = EqLinear(x) + b on (N, C, T) tensors; the arguments of
     EqLinearFunction, ``res`` (or None) and one of FEQL_ACT_*.  Backward: dz =
-    dy act'(z) from the saved slopes, then dx, dW, db as asked for; dres = dy."""
+    dy act'(z) from the saved slopes, then dx, dW, db as asked for; dres = dy.
+    ``train``: whether gradients are recorded (torch.is_grad_enabled() at the call,
+    which a Function cannot see: without it weights that want gradients would have
+    inference save for them)."""
 
     @staticmethod
-    def forward(ctx, x, W, b, res, What, mode: int, group: str, act: int):
+    def forward(ctx, x, W, b, res, What, mode: int, group: str, act: int, train: bool = True):
         run = _L.p4m_forward_act if group == "p4m" else _L.ct_forward_act
         y, slope = run(x, What, b, W.shape[0], mode, act, res=res,
-                       save_z=any(ctx.needs_input_grad[:3]))
+                       save_z=train and any(ctx.needs_input_grad[:3]))
         ctx.save_for_backward(x, What, slope)
         ctx.mode, ctx.group, ctx.act = mode, group, act
         return y
@@ -124,7 +127,7 @@ class EqLinearActFunction(torch.autograd.Function):
             run = _L.p4m_backward_act if ctx.group == "p4m" else _L.ct_backward_act
             dx, dW, db = run(x, dy, slope, What, ctx.mode, ctx.act, with_dx=need_x,
                              with_dw=need_W, with_db=need_b)
-        return dx, dW, db, (dy if need_res else None), None, None, None, None
+        return dx, dW, db, (dy if need_res else None), None, None, None, None, None
 
 
 class EqLinear(torch.nn.Module):
@@ -230,7 +233,8 @@ class EqLinear(torch.nn.Module):
                 y = EqLinearFunction.apply(x3, self.weight, self.bias, What, mode, self.group)
             else:
                 y = EqLinearActFunction.apply(x3, self.weight, self.bias, residual, What, mode,
-                                              self.group, ACTIVATIONS[self.activation])
+                                              self.group, ACTIVATIONS[self.activation],
+                                              torch.is_grad_enabled())
         return y.reshape(*lead, D * T)
 
     def extra_repr(self) -> str:
@@ -283,11 +287,13 @@ class EqLinear(torch.nn.Module):
 
 
 class EqNormFunction(torch.autograd.Function):
-    """Layer norm of (N, C, T) features over C*T, affine per channel."""
+    """Layer norm of (N, C, T) features over C*T, affine per channel (``train`` as for
+    EqLinearActFunction)."""
 
     @staticmethod
-    def forward(ctx, x, gamma, beta, eps: float):
-        y, stats = _L.norm_forward(x, gamma, beta, eps, save_stats=any(ctx.needs_input_grad))
+    def forward(ctx, x, gamma, beta, eps: float, train: bool = True):
+        y, stats = _L.norm_forward(x, gamma, beta, eps,
+                                   save_stats=train and any(ctx.needs_input_grad))
         ctx.save_for_backward(x, stats, gamma)
         return y
 
@@ -298,7 +304,7 @@ class EqNormFunction(torch.autograd.Function):
         need_x, need_g, need_b = ctx.needs_input_grad[:3]
         dx, dgamma, dbeta = _L.norm_backward(dy, x, stats, gamma, with_params=need_g or need_b)
         return (dx if need_x else None, dgamma if need_g else None, dbeta if need_b else None,
-                None)
+                None, None)
 
 
 class EqNorm(torch.nn.Module):
@@ -322,7 +328,8 @@ class EqNorm(torch.nn.Module):
         C, T = self.channels, self.group_order
         if x.shape[-1] != C * T:
             raise ValueError(f"expected features of size C*T = {C * T}, got {x.shape[-1]}")
-        y = EqNormFunction.apply(x.reshape(-1, C, T), self.weight, self.bias, self.eps)
+        y = EqNormFunction.apply(x.reshape(-1, C, T), self.weight, self.bias, self.eps,
+                                 torch.is_grad_enabled())
         return y.reshape(x.shape)
 
     def extra_repr(self) -> str:
@@ -331,11 +338,13 @@ class EqNorm(torch.nn.Module):
 
 
 class EqScanFunction(torch.autograd.Function):
-    """layer.scan_forward with autograd: (h, hN) of (u, g, h0, offsets)."""
+    """layer.scan_forward with autograd: (h, hN) of (u, g, h0, offsets); ``train`` as for
+    EqLinearActFunction."""
 
     @staticmethod
-    def forward(ctx, u, g, h0, offsets):
-        h, hN, saved = _L.scan_forward(u, g, h0, offsets, save=any(ctx.needs_input_grad[:3]))
+    def forward(ctx, u, g, h0, offsets, train: bool = True):
+        h, hN, saved = _L.scan_forward(u, g, h0, offsets,
+                                       save=train and any(ctx.needs_input_grad[:3]))
         if saved is not None:
             # fp16 data: the backward pass reads neither u nor h0 (kept all the same, so that
             # a state that step() changes in between is refused in both types)
@@ -351,7 +360,8 @@ class EqScanFunction(torch.autograd.Function):
             dh = torch.zeros(kept.shape, dtype=g.dtype, device=g.device)
         du, dg, dh0 = _L.scan_backward(dh, u, g, (kept, h0), dhN, offsets)
         need = ctx.needs_input_grad
-        return (du if need[0] else None, dg if need[1] else None, dh0 if need[2] else None, None)
+        return (du if need[0] else None, dg if need[1] else None, dh0 if need[2] else None, None,
+                None)
 
 
 class EqScan(torch.nn.Module):
@@ -386,7 +396,7 @@ class EqScan(torch.nn.Module):
         C, T = self.channels, self.group_order
         uv, gv = self._split(u, gate)
         h0 = None if state is None else state.reshape(-1, C, T)
-        h, hN = EqScanFunction.apply(uv, gv, h0, offsets)
+        h, hN = EqScanFunction.apply(uv, gv, h0, offsets, torch.is_grad_enabled())
         return h.reshape(u.shape), hN.reshape(-1, C * T)
 
     @torch.no_grad()
