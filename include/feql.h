@@ -45,6 +45,11 @@
  *    2^-14) it is rounded to the subnormal spacing 2^-24, at most twice per
  *    butterfly stage: an absolute error per bin of at most 2^-21 for p4 and
  *    2^-19 for the order-6 and -8 groups.
+ *  - Accuracy (FEQL_FP16): the operands of the products, the bins of x, dy and W
+ *    along the group axis, are rounded to fp16 (W's once, those of x and dy up to
+ *    three times) and accumulated in fp32.  Outputs are 3 to 7e-4 off (rms,
+ *    relative) where rounding the exact result gives 2e-4.  FEQL_FP16_SIMT rounds
+ *    the outputs alone and, through an activation, its slope and dz.
  */
 #ifndef FEQL_H
 #define FEQL_H
