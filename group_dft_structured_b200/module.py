@@ -60,7 +60,7 @@ class EqLinearFunction(torch.autograd.Function):
     (group "cyclic"), or the p4m group convolution W[d,c,h^-1 g] (group "p4m").
 
     ``What`` is the layer's Fourier weight buffer (``layer.ct_weight_fft`` of W),
-    passed in so that callers can reuse it while W is unchanged.  Backward
+    passed in so that callers who know that W is unchanged can reuse it.  Backward
     returns the gradients autograd asks for: dx from the dX pass, dW and db from
     the dW pass; for p4 with all of them needed, from the fused single pass.
     """
@@ -137,11 +137,8 @@ class EqLinear(torch.nn.Module):
     (any T; the tensor cores serve T = 4, 8, p4m, and 6 with C and D multiples
     of 4) or float32.  ``group="p4m"`` selects the point
     group D4 (T = 8: rotations (r, 0) at 0..3, reflected (r, 1) at 4..7).  The
-    Fourier weight buffer is rebuilt when the weight changes (tracked by its
-    storage and version counter), so it is computed once per optimizer step, or
-    once for inference, on each stream that calls; a captured graph computes it at
-    every replay.  (Write to the weight itself, under ``torch.no_grad()``: a write
-    through ``weight.data`` leaves no version and is not seen, here or by autograd.)  ``activation`` ("relu", "gelu": the tanh form, "silu") is
+    weight is transformed at every call, by one small kernel; ``freeze()`` keeps the
+    result for a model that is served.  ``activation`` ("relu", "gelu": the tanh form, "silu") is
     applied to the output and ``forward``'s ``residual`` added after it, both in
     the epilogue of the layer's products.
     """
@@ -165,6 +162,7 @@ class EqLinear(torch.nn.Module):
             torch.empty((out_channels, in_channels, group_order), dtype=dtype, device=device))
         self.bias = (torch.nn.Parameter(torch.empty((out_channels,), dtype=dtype, device=device))
                      if bias else None)
+        self._frozen = False
         self._whats = {}  # stream: (what the weight was, its Fourier weight buffer, its memory)
         self.reset_parameters()
 
@@ -178,12 +176,15 @@ class EqLinear(torch.nn.Module):
 
     def fourier_weight(self) -> torch.Tensor:
         W = self.weight
-        # An inference tensor's changes leave no version.  A graph under capture has the
-        # transform in itself: its replays follow the weight, and nothing that they have
-        # yet to compute is kept for eager calls.
-        if W.is_inference() or torch.cuda.is_current_stream_capturing():
+        # Nothing tells reliably whether a weight has changed (a fused optimizer's step, a
+        # replayed graph and a write through .data leave no version), so it is transformed
+        # at every call unless it is declared constant.  A graph under capture has the
+        # transform in itself, and nothing that it has yet to compute is kept.
+        if (not self._frozen or (W.requires_grad and torch.is_grad_enabled())
+                or torch.cuda.is_current_stream_capturing()):
             return self._transformed()
-        key = (W.device, W.dtype, W.data_ptr(), W._version, tuple(W.shape))
+        key = (W.device, W.dtype, W.data_ptr(), None if W.is_inference() else W._version,
+               tuple(W.shape))
         # a buffer to each stream: made, used and given back in its order alone; with the
         # weight's memory, which no other weight can have as long as the buffer is kept
         stream = torch.cuda.current_stream(W.device).cuda_stream
@@ -195,11 +196,23 @@ class EqLinear(torch.nn.Module):
             self._whats[stream] = kept
         return kept[1]
 
+    def freeze(self, frozen: bool = True) -> "EqLinear":
+        """Declares the weight constant from here on, as in a served model: its Fourier
+        weight buffer is then kept (one for each stream that calls) wherever no gradient of
+        the weight is recorded.  ``freeze(False)`` and ``train()`` end it."""
+        self._frozen, self._whats = frozen, {}
+        return self
+
+    def train(self, mode: bool = True):
+        if mode:
+            self.freeze(False)
+        return super().train(mode)
+
     def __getstate__(self):  # copies and files hold the weight alone
         return {**self.__dict__, "_whats": {}}
 
     def __setstate__(self, state):
-        super().__setstate__({**state, "_whats": {}})
+        super().__setstate__({"_frozen": False, **state, "_whats": {}})
 
     def _transformed(self) -> torch.Tensor:
         wfft = _L.p4m_weight_fft if self.group == "p4m" else _L.ct_weight_fft
@@ -440,6 +453,13 @@ class EqScanBlock(torch.nn.Module):
 
     def _mlp(self, x):
         return self.fc2(self.fc1(self.norm2(x)), residual=x)
+
+    def freeze(self, frozen: bool = True) -> "EqScanBlock":
+        """EqLinear.freeze of all its layers."""
+        for m in self.modules():
+            if isinstance(m, EqLinear):
+                m.freeze(frozen)
+        return self
 
     def forward(self, x: torch.Tensor, state: torch.Tensor | None = None,
                 offsets: torch.Tensor | None = None):

@@ -1,5 +1,5 @@
-"""EqLinear's Fourier weight buffer follows the weight: across inference mode, captured
-graphs and streams.  The first tests put a counting stand-in in the place of the
+"""EqLinear's Fourier weight buffer follows the weight: at every call, and where a frozen
+layer keeps it, across inference mode, captured graphs and streams.  The first tests put a counting stand-in in the place of the
 library's transform and need no GPU."""
 
 import pytest
@@ -33,8 +33,48 @@ def fake(monkeypatch):
     return Fake(monkeypatch)
 
 
-def test_once_per_weight(fake):
+def frozen(C, D):
+    return EqLinear(C, D).requires_grad_(False).freeze()
+
+
+def test_at_every_call(fake):
+    """Whatever changes the weight, seen or not by its version."""
     m = EqLinear(3, 5)
+    for k in range(1, 4):
+        assert torch.equal(m.fourier_weight(), 2 * m.weight) and fake.calls == 2 * k - 1
+        m.weight.data.mul_(2)
+        with torch.no_grad():
+            assert torch.equal(m.fourier_weight(), 2 * m.weight) and fake.calls == 2 * k
+
+
+def test_frozen_until_it_trains(fake):
+    m = EqLinear(3, 5).freeze()
+    with torch.no_grad():
+        first = m.fourier_weight()
+        assert m.fourier_weight() is first and fake.calls == 1
+    m.fourier_weight()  # the weight's gradient is recorded: not kept
+    assert fake.calls == 2
+    with torch.no_grad():
+        assert m.eval().fourier_weight() is first
+        for end in (lambda: m.train(), lambda: m.freeze(False), lambda: torch.nn.Sequential(m).train()):
+            m.freeze()
+            kept = m.fourier_weight()
+            assert m.fourier_weight() is kept
+            end()
+            assert m.fourier_weight() is not kept and m._whats == {}
+
+
+def test_blocks_freeze_their_layers(fake):
+    b = M.EqScanBlock(3, 5).requires_grad_(False)
+    assert b.freeze() is b
+    layers = [b.value, b.gate, b.out, b.fc1, b.fc2]
+    assert all(m.fourier_weight() is m.fourier_weight() for m in layers)
+    b.train()
+    assert not any(m._frozen for m in layers)
+
+
+def test_once_per_weight(fake):
+    m = frozen(3, 5)
     first = m.fourier_weight()
     assert m.fourier_weight() is first and fake.calls == 1
     with torch.no_grad():
@@ -43,7 +83,7 @@ def test_once_per_weight(fake):
 
 
 def test_made_in_inference_mode_and_used_outside(fake):
-    m = EqLinear(3, 5)
+    m = frozen(3, 5)
     with torch.inference_mode():
         What = m.fourier_weight()
     assert not What.is_inference()
@@ -59,7 +99,7 @@ def test_weights_made_in_inference_mode(fake):
 
 
 def test_a_captured_transform_is_in_the_graph_alone(fake):
-    m = EqLinear(3, 5)
+    m = frozen(3, 5)
     fake.capturing = True
     captured = m.fourier_weight()
     fake.capturing = False
@@ -72,7 +112,7 @@ def test_a_captured_transform_is_in_the_graph_alone(fake):
 
 
 def test_streams_do_not_share_a_buffer(fake):
-    m = EqLinear(3, 5)
+    m = frozen(3, 5)
     first = m.fourier_weight()
     fake.stream = 2
     second = m.fourier_weight()
@@ -90,10 +130,10 @@ def test_streams_do_not_share_a_buffer(fake):
 def test_copies_and_files_hold_the_weight_alone(fake):
     import copy
     import io
-    m = EqLinear(3, 5)
+    m = frozen(3, 5)
     m.fourier_weight()
     size = lambda m: (lambda f: (torch.save(m, f), f.tell())[1])(io.BytesIO())
-    fresh = EqLinear(3, 5)
+    fresh = frozen(3, 5)
     assert abs(size(m) - size(fresh)) < 64  # no buffer in it
     f = io.BytesIO()
     torch.save(m, f)
@@ -107,10 +147,11 @@ def test_copies_and_files_hold_the_weight_alone(fake):
 
 
 def test_another_weight_at_the_same_address(fake):
-    m = EqLinear(40, 50)
+    m = frozen(40, 50)
     for k in range(1, 30):
         del m.weight
-        m.weight = torch.nn.Parameter(torch.full((50, 40, 4), float(k), dtype=torch.float16))
+        m.weight = torch.nn.Parameter(torch.full((50, 40, 4), float(k), dtype=torch.float16),
+                                      requires_grad=False)
         assert torch.equal(m.fourier_weight(), 2 * m.weight), k
     for k in range(1, 30):  # a weight of the moment, as torch.func.functional_call sets it
         m._parameters["weight"] = None
@@ -124,7 +165,7 @@ def test_threads_on_their_own_streams(fake, monkeypatch):
     import threading
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: type(
         "S", (), {"cuda_stream": threading.get_ident()}))
-    m, failed = EqLinear(3, 5), []
+    m, failed = frozen(3, 5), []
 
     def loop():
         try:
@@ -175,6 +216,7 @@ def layer(kind, **kw):
 @pytest.mark.parametrize("kind", KINDS)
 def test_inference_then_training(gpu, kind):
     m, x = layer(kind)
+    m.freeze()
     with torch.inference_mode():
         want = m(x).clone()
     y = m(x)
@@ -187,6 +229,7 @@ def test_inference_then_training(gpu, kind):
 @pytest.mark.parametrize("kind", KINDS)
 def test_captured_calls_follow_the_weight(gpu, kind, warm):
     m, x = layer(kind)
+    m.freeze(warm)
     with torch.no_grad():
         if warm:
             m(x)
@@ -212,6 +255,7 @@ def test_two_streams_at_once(gpu, kind):
     """The first stream is far from done with its transform when the second calls."""
     m, x = layer(kind)
     m2, _ = layer(kind)
+    m.freeze()
     with torch.no_grad():
         m2.weight.copy_(m.weight)
         if m.bias is not None:
@@ -244,3 +288,61 @@ def test_weights_of_the_moment(gpu, kind):
             m.weight.copy_(W)
             del W
             assert torch.equal(y, m(x)), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,how", [("SGD", "fused"), ("SGD", "foreach"), ("AdamW", "fused"),
+                                      ("AdamW", "foreach"), ("AdamW", "capturable")])
+@pytest.mark.parametrize("kind", KINDS)
+def test_optimizers_that_leave_no_version(gpu, kind, name, how):
+    """Training goes on with the weights that a step has made, and so does what comes after."""
+    m, x = layer(kind)
+    # (fp16 states: an eps of 1e-8 would be 0 there and the step 0 / 0)
+    eps = dict(eps=1e-3) if name == "AdamW" else {}
+    opt = getattr(torch.optim, name)(m.parameters(), lr=1e-2, **{how: True}, **eps)
+    for _ in range(3):
+        with torch.no_grad():
+            before = m(x)
+        opt.zero_grad()
+        m(x).float().square().mean().backward()
+        opt.step()
+        twin, _ = layer(kind)
+        with torch.no_grad():
+            for p, q in zip(twin.parameters(), m.parameters()):
+                p.copy_(q)
+            want = twin(x)
+            assert torch.equal(m(x), want) and not torch.equal(want, before)
+        assert torch.equal(m(x), want)
+
+
+@pytest.mark.gpu
+def test_steps_replayed_in_a_graph(gpu):
+    """A captured training step moves the weights without a trace on the host."""
+    m, x = layer(KINDS[1])
+    opt = torch.optim.SGD(m.parameters(), lr=1e-2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        opt.zero_grad(set_to_none=True)
+        m(x).float().square().mean().backward()
+        opt.step()
+
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    opt.zero_grad(set_to_none=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        with torch.no_grad():
+            before = m(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        twin, _ = layer(KINDS[1])
+        with torch.no_grad():
+            for p, q in zip(twin.parameters(), m.parameters()):
+                p.copy_(q)
+            assert torch.equal(m(x), twin(x)) and not torch.equal(m(x), before)
